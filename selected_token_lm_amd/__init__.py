@@ -15,6 +15,8 @@ library is missing or the device is not gfx950, calls raise.
     logp, lse, z = linear_logp_fwd_save(h, W, y)          # save-logits variant
     logp, lse, loss, g = linear_logp_fwd_rl(h, W, y, logp_old, adv)  # + RL objective
     grad_h, grad_W = linear_logp_bwd_saved(h, W, y, lse, g, z)
+    logp, entropy, top_logp, top_ids = linear_logp_top(h, W, y, top_k)   # vocab_ops.py, autograd-aware
+    loss = linear_distill(h, W, ids, logits, temperature)                # vocab_ops.py, autograd-aware
 """
 from __future__ import annotations
 
@@ -29,6 +31,8 @@ __all__ = [
     "lse_merge", "linear_logp", "gemm_bf16_nt", "linear_logp_fwd_save", "linear_logp_bwd_saved",
     "saved_logits_ld", "rl_token_loss", "profile_begin", "profile_end",
     "linear_logp_fwd_noalloc", "NOALLOC_SCRATCH_BYTES", "linear_logp_fwd_rl",
+    "linear_logp_top", "linear_logp_top_fwd", "linear_logp_top_bwd", "linear_distill", "linear_distill_fwd",
+    "linear_distill_bwd", "vocab_workspace_bytes", "MAX_K",
 ]
 
 IGNORE_INDEX = -100
@@ -104,7 +108,7 @@ def lib():
         if not os.path.exists(library_path):
             raise RuntimeError(f"{library_path} is not built; run `python -m selected_token_lm_amd.build`")
         L = ctypes.CDLL(library_path)
-        for name, (res, args) in _SIGNATURES.items():
+        for name, (res, args) in {**_SIGNATURES, **vocab_ops.SIGNATURES}.items():
             fn = getattr(L, name)
             fn.restype = res
             fn.argtypes = args
@@ -481,3 +485,10 @@ def linear_logp(h, W, y, ignore_index: int = IGNORE_INDEX):
     autograd; call ``linear_logp_bwd`` directly to keep it in fp32.
     """
     return _LinearLogp.apply(h, W, y, ignore_index)
+
+
+from . import vocab_ops  # noqa: E402  (uses the helpers above)
+from .vocab_ops import (  # noqa: E402
+    MAX_K, VOP_DISTILL_BWD, VOP_DISTILL_FWD, VOP_TOP_BWD, VOP_TOP_FWD, linear_distill, linear_distill_bwd,
+    linear_distill_fwd, linear_logp_top, linear_logp_top_bwd, linear_logp_top_fwd, vocab_workspace_bytes,
+)

@@ -1,303 +1,27 @@
 // Host side of the C ABI declared in include/rlk.h: argument validation,
 // workspace layout and kernel launches.  Everything is enqueued on the
 // caller's stream; nothing here allocates device memory or synchronises.
-#include <hip/hip_runtime.h>
+#include "rlk_host.h"
 
-#include <algorithm>
-#include <atomic>
-#include <cstdarg>
-#include <cstdio>
-#include <cstdlib>
-#include <cstring>
-#include <mutex>
-#include <string>
-#include <vector>
-
-#include "rlk.h"
 #include "rlk_bench.h"
-#include "rlk_kernels.h"
-#include "rlk_tiles_w8.h"
+#include "rlk_rows.h"
+
+namespace rlk {
+
+void launch_compact_rows(hipStream_t st, const int32_t* y, int T, int ignore_index, int32_t* idx, int32_t* yA,
+                         int32_t* n_act, float* zero0, float* zero1, float* zero2) {
+  hipLaunchKernelGGL(compact_rows, dim3(1), dim3(1024), 0, st, y, T, ignore_index, idx, yA, n_act, zero0, zero1,
+                     nullptr, zero2, nullptr);
+}
+
+void launch_zero_rows(hipStream_t st, const int32_t* y, int T, int ignore_index, int H, uint16_t* rows) {
+  hipLaunchKernelGGL(zero_rows, dim3((unsigned)std::min((int64_t)T, kRowBlocks)), dim3(256), 0, st, y, T, ignore_index,
+                     H, rows);
+}
+
+}  // namespace rlk
 
 namespace {
-
-thread_local std::string g_last_error;
-
-rlk_status fail(rlk_status s, const char* fmt, ...) __attribute__((format(printf, 2, 3)));
-rlk_status fail(rlk_status s, const char* fmt, ...) {
-  char buf[512];
-  va_list ap;
-  va_start(ap, fmt);
-  vsnprintf(buf, sizeof(buf), fmt, ap);
-  va_end(ap);
-  g_last_error = buf;
-  return s;
-}
-
-rlk_status ok() {
-  g_last_error.clear();
-  return RLK_OK;
-}
-
-inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
-inline size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
-inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-// Limits that keep every 32-bit index inside the kernels in range.
-constexpr int64_t kMaxT = int64_t(1) << 24;
-constexpr int64_t kMaxH = 1 << 16;
-constexpr int64_t kMaxV = 8000000;  // 32 splits x chunks stay within one grid dimension
-constexpr int64_t kMaxGemmMN = int64_t(1) << 24;
-constexpr int64_t kMaxGemmK = int64_t(1) << 20;  // 255 rows x K x 2 bytes stay below 2^32
-
-struct Geom {
-  int64_t V, S, cps, S_pad;
-};
-
-Geom geom_of(int64_t V_global) {
-  Geom g;
-  g.V = V_global;
-  g.S = ceil_div(V_global, rlk::kNSplit);
-  g.cps = ceil_div(g.S, rlk::kChunk);
-  g.S_pad = g.cps * rlk::kChunk;
-  return g;
-}
-
-// --- workspace layouts -------------------------------------------------------
-struct FwdWs {
-  size_t idx, yA, n_act, zt, hA, rec, total;
-  int64_t rec_chunks, T_pad;
-};
-
-// Record slots: one per (chunk of the full vocabulary of V rows, row).
-FwdWs fwd_layout(int64_t T, int64_t H, int64_t V) {
-  FwdWs w;
-  w.T_pad = ceil_div(std::max<int64_t>(T, 1), rlk::kBM) * rlk::kBM;
-  size_t off = 0;
-  w.idx = off;
-  off = align256(off + sizeof(int32_t) * T);
-  w.yA = off;
-  off = align256(off + sizeof(int32_t) * T);
-  w.n_act = off;
-  off = align256(off + sizeof(int32_t));
-  w.zt = off;
-  off = align256(off + sizeof(float) * T);
-  w.hA = off;
-  off = align256(off + 2 * (size_t)w.T_pad * H);
-  w.rec_chunks = rlk::kNSplit * geom_of(V).cps;
-  w.rec = off;
-  off = align256(off + sizeof(float2) * (size_t)w.rec_chunks * (size_t)T);
-  w.total = off;
-  return w;
-}
-
-// Splits per backward group: the largest power of two G <= 32 whose dz
-// block (T_pad x G x S_pad bf16) fits the budget (default 2.5 GiB, env
-// RLK_DZ_BUDGET_MB overrides it, at most 3.5 GiB).  G changes no result
-// bit, only the workspace size and the number of launches.  The cap keeps
-// the per-lane byte offsets of a 256-row dz tile (255 rows x G x S_pad x
-// 2 B, less than the block since T_pad >= 256) inside the 32 unsigned bits
-// the tile loaders use.
-int64_t dz_budget_bytes() {
-  constexpr int64_t kMaxBudget = int64_t(3584) << 20;
-  const char* e = std::getenv("RLK_DZ_BUDGET_MB");
-  if (e && *e) {
-    const long long mb = std::atoll(e);
-    if (mb > 0) return std::min<int64_t>((int64_t)mb << 20, kMaxBudget);
-  }
-  return (int64_t)2560 << 20;
-}
-
-struct BwdWs {
-  size_t idx, n_act, rowinfo, hA, dZ, ghacc, total;
-  int64_t T_pad, S_pad, G;
-};
-
-BwdWs bwd_layout(int64_t T, int64_t H, int64_t V) {
-  const Geom g = geom_of(V);
-  BwdWs w;
-  w.T_pad = ceil_div(std::max<int64_t>(T, 1), rlk::kBM) * rlk::kBM;
-  w.S_pad = ceil_div(g.S, 64) * 64;
-  const int64_t per_split = 2 * w.T_pad * w.S_pad;
-  const int64_t budget = dz_budget_bytes();
-  w.G = 1;
-  while (w.G < rlk::kNSplit && 2 * w.G * per_split <= budget) w.G *= 2;
-  size_t off = 0;
-  w.idx = off;
-  off = align256(off + sizeof(int32_t) * T);
-  w.n_act = off;
-  off = align256(off + sizeof(int32_t));
-  w.rowinfo = off;
-  off = align256(off + 16 * (size_t)w.T_pad);
-  w.hA = off;
-  off = align256(off + 2 * (size_t)w.T_pad * H);
-  w.dZ = off;
-  off = align256(off + (size_t)per_split * w.G);
-  w.ghacc = off;
-  if (w.G < rlk::kNSplit) off = align256(off + 4 * (size_t)T * H);
-  w.total = off;
-  return w;
-}
-
-// --- device check ----------------------------------------------------------------
-std::mutex g_dev_mu;
-int g_dev_ok[64];   // 0 unknown, 1 gfx950, -1 other
-int g_dev_cus[64];  // compute units of a checked device
-
-rlk_status check_device() {
-  int dev = 0;
-  hipError_t e = hipGetDevice(&dev);
-  if (e != hipSuccess) return fail(RLK_ERR_HIP, "hipGetDevice: %s", hipGetErrorString(e));
-  if (dev < 0 || dev >= 64) return fail(RLK_ERR_UNSUPPORTED_DEVICE, "device index %d", dev);
-  std::lock_guard<std::mutex> lk(g_dev_mu);
-  if (g_dev_ok[dev] == 0) {
-    hipDeviceProp_t prop;
-    e = hipGetDeviceProperties(&prop, dev);
-    if (e != hipSuccess) return fail(RLK_ERR_HIP, "hipGetDeviceProperties: %s", hipGetErrorString(e));
-    g_dev_ok[dev] = (std::strncmp(prop.gcnArchName, "gfx950", 6) == 0) ? 1 : -1;
-    g_dev_cus[dev] = prop.multiProcessorCount;
-    if (g_dev_ok[dev] < 0) return fail(RLK_ERR_UNSUPPORTED_DEVICE, "device %d is %s, not gfx950", dev, prop.gcnArchName);
-  }
-  if (g_dev_ok[dev] < 0) return fail(RLK_ERR_UNSUPPORTED_DEVICE, "device %d is not gfx950", dev);
-  return RLK_OK;
-}
-
-// Compute units of the current device (after check_device succeeded on it).
-int device_cus() {
-  int dev = 0;
-  if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= 64) return 256;
-  std::lock_guard<std::mutex> lk(g_dev_mu);
-  return g_dev_cus[dev] > 0 ? g_dev_cus[dev] : 256;
-}
-
-// grad_h in two row passes (gradh_tile's kPart) when its whole tiles would
-// leave most compute units idle while each runs the vocabulary-long chain:
-// a pass's chain takes ~70 % of a tile's and the passes add ~40 % to
-// grad_h's work, which pays while three times the tile count fits on the
-// units (the grad_W tiles fill the rest).  The environment variable
-// RLK_GRAD_H_PASSES = 0 / 1 forces either form (results are the same bits;
-// tests use it).
-bool grad_h_passes(int64_t row_tiles, int64_t n_tiles) {
-  const char* e = std::getenv("RLK_GRAD_H_PASSES");
-  if (e && *e) return std::atoi(e) != 0;
-  return 3 * row_tiles * n_tiles <= device_cus();
-}
-
-// Tile grids stay within the 2^31 - 1 threads a launch holds along x
-// (checked for the larger of the two block sizes).  Row-wise kernels take
-// at most kRowBlocks blocks and stride over the rows.
-constexpr int64_t kRowBlocks = int64_t(1) << 22;  // 256-thread blocks: 2^30 threads
-constexpr int64_t kRowBlocksY = 65535;            // the limit along y
-rlk_status check_grid(int64_t blocks) {
-  if (blocks * std::max(rlk::kThreads, rlk::kThreadsW8) > (int64_t)INT32_MAX)
-    return fail(RLK_ERR_BAD_SHAPE, "problem needs %lld tile blocks, more than one launch holds", (long long)blocks);
-  return RLK_OK;
-}
-
-rlk_status launched(const char* what) {
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return fail(RLK_ERR_HIP, "%s: %s", what, hipGetErrorString(e));
-  return RLK_OK;
-}
-
-// --- optional per-kernel timing (rlk_profile_begin / rlk_profile_end) ---------
-struct ProfRec {
-  const char* name;
-  hipEvent_t start, stop;
-};
-std::mutex g_prof_mu;
-// read without the lock on every launch: when timing is off (the normal
-// case) a launch takes no lock at all
-std::atomic<bool> g_prof_on{false};
-std::vector<ProfRec> g_prof_recs;
-std::vector<hipEvent_t> g_prof_pool;
-
-hipEvent_t prof_event() {
-  if (!g_prof_pool.empty()) {
-    hipEvent_t e = g_prof_pool.back();
-    g_prof_pool.pop_back();
-    return e;
-  }
-  hipEvent_t e = nullptr;
-  if (hipEventCreate(&e) != hipSuccess) return nullptr;
-  return e;
-}
-
-// Brackets one launch with events on its stream when timing is enabled.
-struct ProfScope {
-  const char* name;
-  hipStream_t st;
-  hipEvent_t a = nullptr, b = nullptr;
-  ProfScope(const char* n, hipStream_t s) : name(n), st(s) {
-    if (!g_prof_on.load(std::memory_order_relaxed)) return;
-    std::lock_guard<std::mutex> lk(g_prof_mu);
-    if (!g_prof_on.load(std::memory_order_relaxed)) return;
-    a = prof_event();
-    b = prof_event();
-    if (a && b) {
-      (void)hipEventRecord(a, st);
-    } else {  // event creation failed: this launch goes untimed
-      if (a) g_prof_pool.push_back(a);
-      if (b) g_prof_pool.push_back(b);
-      a = b = nullptr;
-    }
-  }
-  ~ProfScope() {
-    if (!a || !b) return;
-    std::lock_guard<std::mutex> lk(g_prof_mu);
-    (void)hipEventRecord(b, st);
-    g_prof_recs.push_back(ProfRec{name, a, b});
-  }
-};
-
-#define RLK_TRY(x)                  \
-  do {                              \
-    rlk_status _s = (x);            \
-    if (_s != RLK_OK) return _s;    \
-  } while (0)
-
-// Launch a kernel on stream `st`, timed when profiling is on; return on error.
-#define RLK_LAUNCH(kern, grid, block, st, ...)                        \
-  do {                                                                \
-    {                                                                 \
-      ProfScope _ps(#kern, st);                                       \
-      hipLaunchKernelGGL(rlk::kern, grid, block, 0, st, __VA_ARGS__); \
-    }                                                                 \
-    RLK_TRY(launched(#kern));                                         \
-  } while (0)
-
-// Same for a kernel given as a function pointer, timed under `name`.
-#define RLK_LAUNCH_FN(name, fn, grid, block, st, ...)           \
-  do {                                                          \
-    {                                                           \
-      ProfScope _ps(name, st);                                  \
-      hipLaunchKernelGGL(fn, grid, block, 0, st, __VA_ARGS__);  \
-    }                                                           \
-    RLK_TRY(launched(name));                                    \
-  } while (0)
-
-// Same for a launch made by a launcher of the eight-wave unit
-// (rlk_tiles_w8.h), timed under `name`.
-#define RLK_LAUNCH_W8(name, launcher, grid, st, args) \
-  do {                                                \
-    {                                                 \
-      ProfScope _ps(name, st);                        \
-      rlk::launcher(grid, st, args);                  \
-    }                                                 \
-    RLK_TRY(launched(name));                          \
-  } while (0)
-
-// Shapes first; with T == 0 there is nothing to read or write, so the
-// pointers are not checked (empty tensors may carry NULL).
-rlk_status check_common(const void* h, const void* W, const int32_t* y, int64_t T, int64_t H, int64_t V) {
-  if (T < 0 || T > kMaxT) return fail(RLK_ERR_BAD_SHAPE, "T=%lld out of [0, 2^24]", (long long)T);
-  if (H <= 0 || H > kMaxH || H % 64 != 0)
-    return fail(RLK_ERR_BAD_SHAPE, "H=%lld must be a positive multiple of 64 up to 65536", (long long)H);
-  if (V <= 0 || V > kMaxV) return fail(RLK_ERR_BAD_SHAPE, "V=%lld out of [1, 8000000]", (long long)V);
-  if (T == 0) return RLK_OK;
-  if (!h || !W || !y) return fail(RLK_ERR_NULL_ARG, "h, W and y are required");
-  if (!aligned16(h) || !aligned16(W) || !aligned16(y)) return fail(RLK_ERR_BAD_ALIGNMENT, "h, W, y must be 16-byte aligned");
-  return RLK_OK;
-}
 
 // Split range [s0, s0 + n) of an aligned vocabulary block, or an error.
 rlk_status split_range(int64_t vocab_start, int64_t vocab_len, int64_t V_global, int* s0, int* n) {
@@ -408,7 +132,7 @@ const char* rlk_status_string(rlk_status s) {
   }
 }
 
-const char* rlk_last_error_message(void) { return g_last_error.c_str(); }
+const char* rlk_last_error_message(void) { return g_last_error; }
 
 size_t rlk_workspace_bytes(int32_t op, int64_t T, int64_t H, int64_t V) {
   if (T < 0 || T > kMaxT || H <= 0 || H > kMaxH || H % 64 != 0 || V <= 0 || V > kMaxV) return 0;

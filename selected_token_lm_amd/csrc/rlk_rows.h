@@ -1,0 +1,23 @@
+// Launchers of the row kernels that rlk_api.hip builds, for the other
+// translation units; internal to the library (not exported).  They only
+// enqueue the launch on `st`; the caller checks hipGetLastError.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace rlk {
+
+// compact_rows: the rows t with y[t] != ignore_index, ascending, into idx
+// (their y into yA unless NULL) and their number into n_act; zero0 .. zero2
+// (each NULL or [T]) are set to 0 at the other rows.
+__attribute__((visibility("hidden"))) void launch_compact_rows(hipStream_t st, const int32_t* y, int T,
+                                                              int ignore_index, int32_t* idx, int32_t* yA,
+                                                              int32_t* n_act, float* zero0, float* zero1,
+                                                              float* zero2);
+
+// zero_rows: the rows of a bf16 [T, H] array with y[t] == ignore_index.
+__attribute__((visibility("hidden"))) void launch_zero_rows(hipStream_t st, const int32_t* y, int T, int ignore_index,
+                                                           int H, uint16_t* rows);
+
+}  // namespace rlk

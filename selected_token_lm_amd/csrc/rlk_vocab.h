@@ -1,0 +1,976 @@
+// HIP kernels of the operators on the whole next-token distribution (gfx950):
+// the selected log-probability with entropy and top alternatives
+// (linear_logp_top), and the divergence from a teacher's kept tokens
+// (linear_distill).  Declared in include/rlk/vocab_ops.h.
+//
+// Forward:
+//   distill_rows       which rows hold a teacher's token at all
+//   gather_rows_fill   compacted hidden rows; the outputs of inactive rows
+//   bucket_entries     the teacher's tokens of a row tile, sorted by vocabulary tile
+//   logit_tiles        MFMA logit tiles -> chunk statistics, and the logits
+//                      that the row kernels need (top: of a group of splits,
+//                      distill: of the teacher's tokens)
+//   top_merge          folds the statistics; the K best of a row
+//   distill_merge      folds the statistics; the row's divergence
+// Backward (per group of vocabulary splits, ascending):
+//   gather_rows_grad   compacted hidden rows and the rows' coefficients
+//   soft_dz_tiles      recomputed logits -> dz, bf16
+//   distill_scatter    dz at the teacher's tokens
+//   gradw_bf16_tiles   grad_W as bf16
+#pragma once
+
+#include "rlk_kernels.h"
+
+namespace rlk {
+namespace vocab {
+
+constexpr int kMaxK = 128;  // alternatives, or teacher's tokens, of a row
+
+// A product e^d * d is 0 where e^d is (d may be -inf there): d is cut off
+// where e^d rounds to 0 in fp32 (e^-103.98 is half the least denormal).
+constexpr float kDeepest = -104.f;
+
+// ---------------------------------------------------------------------------
+// Statistics with the first moment: m = max z, s = sum e(z - m),
+// u = sum e(z - m) (z - m) <= 0.  The entropy is then log s - u / s, a sum of
+// two terms >= 0.  m and s are the bits of ms_combine and chunk_stats.
+// ---------------------------------------------------------------------------
+struct MSU {
+  float m, s, u;
+};
+
+__device__ __forceinline__ MSU msu_identity() { return {-INFINITY, 0.f, 0.f}; }
+
+// a = lower vocabulary indices.  Moving a set from its max ma to m multiplies
+// s by e(ma - m) and gives u' = e(ma - m) u + s' (ma - m).
+__device__ __forceinline__ MSU msu_combine(MSU a, MSU b) {
+  const float m = fmaxf(a.m, b.m);
+  if (m == -INFINITY) return msu_identity();
+  const float ea = rlk_exp(a.m - m), eb = rlk_exp(b.m - m);
+  const float pa = a.s * ea, pb = b.s * eb;
+  const float ua = a.u * ea + pa * fmaxf(a.m - m, kDeepest);
+  const float ub = b.u * eb + pb * fmaxf(b.m - m, kDeepest);
+  return {m, pa + pb, ua + ub};
+}
+
+// exp_tree with the first moment beside it (x: sum e, y: sum e d).
+template <int N>
+__device__ __forceinline__ float2 moment_tree(const float (&v)[kRowVals], int k0, float m) {
+  if constexpr (N == 1) {
+    const float d = v[k0] - m, e = rlk_exp(d);
+    return make_float2(e, e * fmaxf(d, kDeepest));
+  } else {
+    const float2 l = moment_tree<N / 2>(v, k0, m);
+    const float2 r = moment_tree<N / 2>(v, k0 + N / 2, m);
+    return make_float2(l.x + r.x, l.y + r.y);
+  }
+}
+
+__device__ __forceinline__ MSU chunk_stats_moment(const float (&v)[kRowVals]) {
+  float mx = -INFINITY;
+#pragma unroll
+  for (int k = 0; k < kRowVals; ++k) mx = fmaxf(mx, v[k]);
+  mx = row_max(mx);
+  const float2 t = moment_tree<kRowVals>(v, 0, mx);
+  return {mx, row_sum(t.x), row_sum(t.y)};
+}
+
+// ---------------------------------------------------------------------------
+// Logits of a group of splits.  Tiles, statistics and target logit as in
+// fwd_tiles; records at [chunk of the vocabulary][active row].
+// kTop: also the first moment, and (z != NULL) every logit of the group: of
+//   active row i, chunk j of the group's split sl, at
+//   z + i * ldz + 128 (sl cps + j).
+// !kTop: logits times `scale` (1 / temperature); the tile's entries (see
+//   bucket_entries) pick the scaled logits of the teacher's tokens.
+// ---------------------------------------------------------------------------
+struct LogitArgs {
+  const uint16_t* hA;  // active rows of h, compacted, zero padded to a multiple of 256
+  const uint16_t* W;
+  const int32_t* n_act;
+  int H;
+  int G;        // splits of this launch: [gm.s0, gm.s0 + G)
+  SplitGeom gm;
+  TileGeom tg;
+  size_t rec_stride;
+  float2* rec;
+  // kTop
+  const int32_t* yA;  // targets of the active rows
+  float* zt;
+  float* rec_u;
+  float* z;
+  int64_t ldz;
+  // !kTop
+  float scale;
+  int K;
+  const int32_t* ent_off;  // [row tile][32 tps + 1]
+  const uint32_t* ent;     // [row tile][256 K]
+  float* z_ids;            // [active row][K]
+};
+
+// An entry: column and row within the tile, slot of the row.
+__device__ __forceinline__ uint32_t entry_of(int col, int row, int k) { return (uint32_t)(col | row << 8 | k << 16); }
+
+template <bool kTop>
+__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(RLK_WAVES / 4, RLK_WAVES / 4))) void logit_tiles(
+    LogitArgs a) {
+  __shared__ u32x4 lds[kLdsU4];
+  const int n_act = __builtin_amdgcn_readfirstlane(*a.n_act);
+  const int rtiles = (n_act + kBM - 1) / kBM;
+  const int C = a.G * a.tg.tps;
+  const int id = xcd_tile(rtiles * C, blockIdx.x);
+  if (id < 0) return;
+  int rt, ct;
+  grouped_tile(id, rtiles, rt, ct, C, row_group(rtiles));
+  const int i0 = rt * kBM;
+  const int sl = ct / a.tg.tps, j = ct - sl * a.tg.tps;
+  const int sbeg = (a.gm.s0 + sl) * a.gm.S;
+  const int send = min(sbeg + a.gm.S, a.gm.V);
+  const int c0 = sbeg + j * kBN;
+  if (c0 >= send) return;
+  const int c1 = min(c0 + kBN, send);
+  const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), wm = wave_m(w),
+            wn = wave_n(w);
+  // this lane's rows' targets, loaded as in fwd_tiles
+  int tgt[kMI];
+  const auto load_row = [&](int mi, int ln) {
+    if constexpr (kTop) tgt[mi] = a.yA[min(i0 + acc_row(wm, mi, ln), n_act - 1)];
+  };
+  const auto load_rows = [&]() {
+#pragma unroll
+    for (int mi = 0; mi < kTailRows; ++mi) load_row(mi, lane);
+  };
+  const RowsK A = rows_k(a.hA + (size_t)i0 * a.H, kBM - 1, a.H);
+  const RowsK B = rows_k(a.W + (size_t)c0 * a.H, c1 - 1 - c0, a.H);
+  Acc acc;
+  acc_zero(acc);
+  gemm_kk<0>(A, B, a.H / kBK, acc, lds, load_rows);
+
+  const int cc0 = c0 + kChunk * wn;  // this wave's chunk
+  const int width = min(cc0 + kChunk, c1) - cc0;
+  if (width <= 0) return;
+  const int jc = 2 * j + wn;  // its number in the split
+  const int g = (a.gm.s0 + sl) * a.gm.cps + jc;
+  int le = lane;  // an opaque copy, see fwd_tiles
+  asm volatile("" : "+v"(le));
+  const int rl = row_lane(le);
+  const int lim = width - 4 * rl;  // value k is valid iff chunk_col(k) < lim
+#pragma unroll
+  for (int mi = kTailRows; mi < kMI; ++mi) load_row(mi, le);
+  // the tile's entries
+  int e0 = 0, e1 = 0;
+  const uint32_t* ent = nullptr;
+  if constexpr (!kTop) {
+    const int32_t* off = a.ent_off + (size_t)rt * (kNSplit * a.tg.tps + 1) + (a.gm.s0 + sl) * a.tg.tps + j;
+    e0 = __builtin_amdgcn_readfirstlane(off[0]);
+    e1 = __builtin_amdgcn_readfirstlane(off[1]);
+    ent = a.ent + (size_t)rt * kBM * a.K;
+  }
+#pragma unroll
+  for (int mi = 0; mi < kMI; ++mi) {
+    const int i = i0 + acc_row(wm, mi, le);
+    __builtin_amdgcn_sched_barrier(0);
+    float v[kRowVals];
+#pragma unroll
+    for (int ni = 0; ni < kNI; ++ni)
+#pragma unroll
+      for (int r = 0; r < 4 * kQL; ++r)
+        v[4 * kQL * ni + r] = kTop ? acc.c[mi][ni][r] : acc.c[mi][ni][r] * a.scale;
+    // the wave's values in LDS (free once the engine has returned): lane l
+    // holds its element k at float4 slot 64 (k >> 2) + l of the wave's slots
+    float4* sl4 = reinterpret_cast<float4*>(lds) + 16 * kRowVals * w;
+    const auto stage = [&]() {
+#pragma unroll
+      for (int q = 0; q < kRowVals / 4; ++q)
+        sl4[64 * q + le] = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+    };
+    if constexpr (kTop) {
+      if (a.z && i < n_act) {
+        // whole chunks: the columns past the split's end hold logits of the
+        // clamped last row, which no reader takes
+        float* zr = a.z + (size_t)i * a.ldz + (size_t)kChunk * (sl * a.gm.cps + jc) + 4 * rl;
+#pragma unroll
+        for (int k = 0; k < kRowVals; k += 4)
+          *reinterpret_cast<float4*>(zr + chunk_col(k)) = make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
+      }
+      const int tc = tgt[mi] - cc0;
+      const bool hit = i < n_act && tc >= 0 && tc < width && ((tc >> 2) & (kLPR - 1)) == rl;
+      if (__builtin_amdgcn_ballot_w64(hit)) {  // rare: see fwd_tiles
+        stage();
+        if (hit) {
+          const int k = chunk_val(tc);
+          a.zt[i] = reinterpret_cast<const float*>(sl4 + 64 * (k >> 2) + le)[k & 3];
+        }
+      }
+    } else {
+      bool staged = false;
+      for (int eb = e0; eb < e1; eb += 64) {
+        const uint32_t x = eb + le < e1 ? ent[eb + le] : 0u;
+        const int row = (x >> 8) & 255, col = x & 255;
+        const bool mine = eb + le < e1 && row / kBlk == kMI * wm + mi && (col >> 7) == wn;
+        if (!__builtin_amdgcn_ballot_w64(mine)) continue;
+        if (!staged) {
+          stage();
+          // the wave's writes come before its lanes' reads of one another's values
+          __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+          __builtin_amdgcn_wave_barrier();
+          __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+          staged = true;
+        }
+        if (mine) {
+          const int c = col & (kChunk - 1), k = chunk_val(c);
+          const int from = row % kBlk + kBlk * ((c >> 2) & (kLPR - 1));
+          a.z_ids[(size_t)(i0 + row) * a.K + (x >> 16)] = reinterpret_cast<const float*>(sl4 + 64 * (k >> 2) + from)[k & 3];
+        }
+      }
+      // ... and the reads before the next row block's writes
+      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+    }
+    if (width < kChunk) {
+#pragma unroll
+      for (int k = 0; k < kRowVals; ++k)
+        if (chunk_col(k) >= lim) v[k] = -INFINITY;
+    }
+    if constexpr (kTop) {
+      const MSU st = chunk_stats_moment(v);
+      if (rl == 0 && i < n_act) {
+        a.rec[(size_t)g * a.rec_stride + i] = make_float2(st.m, st.s);
+        a.rec_u[(size_t)g * a.rec_stride + i] = st.u;
+      }
+    } else {
+      const float2 st = chunk_stats(v);
+      if (rl == 0 && i < n_act) a.rec[(size_t)g * a.rec_stride + i] = st;
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Row gathers
+// ---------------------------------------------------------------------------
+// hA[i] = h[idx[i]] for active rows i < n_act, zero rows for n_act <= i <
+// rows, and the K slots of the inactive rows t < T (act[t] == ignore):
+// slot_logp = -inf, slot_ids (optional) = -1.  Block 256, 16-byte pieces.
+struct GatherArgs {
+  const uint16_t* h;
+  const int32_t* idx;
+  const int32_t* n_act;
+  int T, rows, H;
+  uint16_t* hA;
+  const int32_t* act;
+  int ignore_index;
+  int K;
+  float* slot_logp;
+  int32_t* slot_ids;
+};
+
+__device__ __forceinline__ void gather_row(const uint16_t* h, const int32_t* idx, int n_act, int i, int H,
+                                           uint16_t* hA) {
+  u32x4* dst = reinterpret_cast<u32x4*>(hA + (size_t)i * H);
+  if (i < n_act) {
+    const u32x4* src = reinterpret_cast<const u32x4*>(h + (size_t)idx[i] * H);
+    for (int p = threadIdx.x; p < H / 8; p += 256) dst[p] = src[p];
+  } else {
+    for (int p = threadIdx.x; p < H / 8; p += 256) dst[p] = u32x4{0u, 0u, 0u, 0u};
+  }
+}
+
+__global__ __launch_bounds__(256) void gather_rows_fill(GatherArgs a) {
+  const int n_act = *a.n_act;
+  for (int i = blockIdx.x; i < a.rows; i += gridDim.x) {
+    gather_row(a.h, a.idx, n_act, i, a.H, a.hA);
+    if (i < a.T && a.act[i] == a.ignore_index) {
+      for (int k = threadIdx.x; k < a.K; k += 256) {
+        a.slot_logp[(size_t)i * a.K + k] = -INFINITY;
+        if (a.slot_ids) a.slot_ids[(size_t)i * a.K + k] = -1;
+      }
+    }
+  }
+}
+
+// hA as above, and per active row the coefficients of
+//     dz_v = g [v == target] - p_v (a + b (z_v - lse)),  p_v = e(z_v - lse):
+// rowinfo = {lse, a, b, target (bits)}, rowg = g; {0, 0, 0, -1} and 0 past
+// n_act.  top: a = g + b entropy, b = dL/dentropy.  distill: a = -(dL/dloss
+// / temperature), b = 0, no target; the teacher's share of dz comes from
+// distill_scatter.  A row without a defined loss (a target, or a kept
+// teacher's token, outside the vocabulary) gets NaN coefficients.
+struct GatherGradArgs {
+  const uint16_t* h;
+  const int32_t* idx;
+  const int32_t* n_act;
+  int rows, H, V;
+  uint16_t* hA;
+  const float* lse;
+  const float* g;           // may be NULL (top: zero)
+  float4* rowinfo;
+  float* rowg;
+  // top
+  const int32_t* y;
+  const float* entropy;
+  const float* g_entropy;   // may be NULL (zero)
+  // distill
+  const int32_t* act;       // 1 where a kept token lies outside the vocabulary
+  float scale;
+};
+
+template <bool kTop>
+__global__ __launch_bounds__(256) void gather_rows_grad(GatherGradArgs a) {
+  const int n_act = *a.n_act;
+  for (int i = blockIdx.x; i < a.rows; i += gridDim.x) {
+    gather_row(a.h, a.idx, n_act, i, a.H, a.hA);
+    if (threadIdx.x == 0) {
+      float4 ri = make_float4(0.f, 0.f, 0.f, __int_as_float(-1));
+      float gt = 0.f;
+      if (i < n_act) {
+        const int t = a.idx[i];
+        ri.x = a.lse[t];
+        if constexpr (kTop) {
+          const int yt = a.y[t];
+          gt = a.g ? a.g[t] : 0.f;
+          if (yt < 0 || yt >= a.V) gt = __builtin_nanf("");
+          ri.z = a.g_entropy ? a.g_entropy[t] : 0.f;
+          ri.y = gt + ri.z * a.entropy[t];
+          ri.w = __int_as_float(yt);
+        } else {
+          ri.y = a.act[t] == 1 ? __builtin_nanf("") : -(a.g[t] * a.scale);
+        }
+      }
+      a.rowinfo[i] = ri;
+      a.rowg[i] = gt;
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// The teacher's rows
+// ---------------------------------------------------------------------------
+// Slot k of a row is kept iff its id is >= 0 and its logit is not -inf.
+__device__ __forceinline__ bool slot_kept(int id, float logit) { return id >= 0 && logit != -INFINITY; }
+
+__device__ __forceinline__ float wave_max(float x) {
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) x = fmaxf(x, __shfl_xor(x, d));
+  return x;
+}
+__device__ __forceinline__ float wave_sum(float x) {
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) x = x + __shfl_xor(x, d);
+  return x;
+}
+
+// A teacher's row over a wave: lane l holds slots l and l + 64.
+// q = softmax of the kept logits / temperature, lq = log q.
+constexpr int kSlots2 = kMaxK / 64;
+struct TeacherRow {
+  int id[kSlots2];
+  bool kept[kSlots2];
+  float q[kSlots2], lq[kSlots2];
+};
+
+__device__ __forceinline__ TeacherRow teacher_row(const int32_t* ids, const float* logits, int K, float scale) {
+  const int lane = threadIdx.x & 63;
+  TeacherRow r;
+  float x[kSlots2], m = -INFINITY;
+  bool bad = false;  // fmaxf would drop a NaN
+#pragma unroll
+  for (int s = 0; s < kSlots2; ++s) {
+    const int k = lane + 64 * s;
+    r.id[s] = k < K ? ids[k] : -1;
+    const float l = k < K ? logits[k] : -INFINITY;
+    r.kept[s] = slot_kept(r.id[s], l);
+    x[s] = r.kept[s] ? l * scale : -INFINITY;
+    m = fmaxf(m, x[s]);
+    bad |= x[s] != x[s];
+  }
+  m = wave_max(m);
+  if (__builtin_amdgcn_ballot_w64(bad)) m = __builtin_nanf("");
+  float sum = 0.f;
+#pragma unroll
+  for (int s = 0; s < kSlots2; ++s) {
+    r.q[s] = r.kept[s] ? rlk_exp(x[s] - m) : 0.f;
+    sum = sum + r.q[s];
+  }
+  sum = wave_sum(sum);
+  const float L = rlk_log(sum);
+#pragma unroll
+  for (int s = 0; s < kSlots2; ++s) {
+    r.lq[s] = r.kept[s] ? (x[s] - m) - L : 0.f;
+    r.q[s] = r.kept[s] ? r.q[s] / sum : 0.f;
+  }
+  return r;
+}
+
+// act[t] = -100 for rows without a kept token, 1 for rows with a kept token
+// outside the vocabulary, else 0; q (optional) = the teacher's distribution.
+// One wave per row.
+__global__ __launch_bounds__(256) void distill_rows(const int32_t* __restrict__ ids, const float* __restrict__ logits,
+                                                    int T, int K, int V, float scale, int32_t* __restrict__ act,
+                                                    float* __restrict__ q) {
+  const int lane = threadIdx.x & 63;
+  for (int t = blockIdx.x * 4 + (threadIdx.x >> 6); t < T; t += gridDim.x * 4) {
+    const TeacherRow r = teacher_row(ids + (size_t)t * K, logits + (size_t)t * K, K, scale);
+    bool any = false, out = false;
+#pragma unroll
+    for (int s = 0; s < kSlots2; ++s) {
+      any |= r.kept[s];
+      out |= r.kept[s] && r.id[s] >= V;
+      if (q && lane + 64 * s < K) q[(size_t)t * K + lane + 64 * s] = r.q[s];
+    }
+    const bool any_w = __builtin_amdgcn_ballot_w64(any) != 0, out_w = __builtin_amdgcn_ballot_w64(out) != 0;
+    if (lane == 0) act[t] = !any_w ? -100 : out_w ? 1 : 0;
+  }
+}
+
+// The entries of each row tile (256 active rows), grouped by the vocabulary
+// tile their token lies in: off[rt][c] .. off[rt][c + 1] are those of tile c
+// (= split * tps + tile of the split).  Within a tile the order is left open:
+// every entry writes a place of its own.  One block per row tile.
+constexpr int kBucketThreads = 1024;
+constexpr int kMaxVTiles = 32768;  // 32 tps for the largest vocabulary: 31264
+__global__ __launch_bounds__(kBucketThreads) void bucket_entries(const int32_t* __restrict__ ids,
+                                                                 const float* __restrict__ logits,
+                                                                 const int32_t* __restrict__ idx,
+                                                                 const int32_t* __restrict__ n_act_p, int K,
+                                                                 SplitGeom gm, int tps, int32_t* __restrict__ off,
+                                                                 uint32_t* __restrict__ ent) {
+  __shared__ int32_t cnt[kMaxVTiles];
+  __shared__ int32_t wave_tot[kBucketThreads / 64];
+  const int rt = blockIdx.x, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int i0 = rt * kBM, n = min(kBM, *n_act_p - i0);
+  if (n <= 0) return;
+  const int C = kNSplit * tps;
+  for (int c = tid; c < C; c += kBucketThreads) cnt[c] = 0;
+  __syncthreads();
+  const auto each = [&](auto&& f) {
+    for (int e = tid; e < n * K; e += kBucketThreads) {
+      const int r = e / K, k = e - r * K;
+      const size_t at = (size_t)idx[i0 + r] * K + k;
+      const int id = ids[at];
+      if (id >= gm.V || !slot_kept(id, logits[at])) continue;
+      const int s = id / gm.S, c = id - s * gm.S;
+      f(s * tps + (c >> 8), entry_of(c & 255, r, k));
+    }
+  };
+  each([&](int c, uint32_t) { atomicAdd(&cnt[c], 1); });
+  __syncthreads();
+  // exclusive scan: thread tid takes `per` consecutive tiles
+  const int per = (C + kBucketThreads - 1) / kBucketThreads;
+  const int lo = min(tid * per, C), hi = min(lo + per, C);
+  int sum = 0;
+  for (int c = lo; c < hi; ++c) sum += cnt[c];
+  int incl = sum;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int v = __shfl_up(incl, d);
+    if (lane >= d) incl += v;
+  }
+  if (lane == 63) wave_tot[wave] = incl;
+  __syncthreads();
+  int pos = incl - sum;
+  for (int w = 0; w < wave; ++w) pos += wave_tot[w];
+  int32_t* o = off + (size_t)rt * (C + 1);
+  for (int c = lo; c < hi; ++c) {
+    const int v = cnt[c];
+    o[c] = pos;
+    cnt[c] = pos;
+    pos += v;
+  }
+  if (tid == kBucketThreads - 1) o[C] = pos;
+  __syncthreads();
+  uint32_t* e0 = ent + (size_t)rt * kBM * K;
+  each([&](int c, uint32_t x) { e0[atomicAdd(&cnt[c], 1)] = x; });
+}
+
+// ---------------------------------------------------------------------------
+// Folds.  Lane s < 32 folds split s of active row i (chunks left to right);
+// the splits then meet in a pairwise tree over the lanes (lane 2w j takes
+// lane 2w j + w): the order, and for m and s the bits, of merge_splits.
+// The result is valid in lane 0.
+// ---------------------------------------------------------------------------
+template <bool kMoment>
+__device__ __forceinline__ MSU fold_row(const float2* rec, const float* rec_u, size_t stride, int i,
+                                        const SplitGeom& gm) {
+  const int lane = threadIdx.x & 63;
+  MSU r = msu_identity();
+  if (lane < kNSplit) {
+    const int c0 = lane * gm.S, send = min(c0 + gm.S, gm.V);
+    const int nj = send > c0 ? (send - c0 + kChunk - 1) / kChunk : 0;
+    const size_t base = (size_t)lane * gm.cps * stride + i;
+    constexpr int kBatch = 8;
+    for (int j0 = 0; j0 < nj; j0 += kBatch) {
+      float2 ms[kBatch];
+      float u[kBatch];
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b)
+        if (j0 + b < nj) {
+          ms[b] = rec[base + (size_t)(j0 + b) * stride];
+          u[b] = kMoment ? rec_u[base + (size_t)(j0 + b) * stride] : 0.f;
+        }
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b)
+        if (j0 + b < nj) {
+          if constexpr (kMoment) {
+            r = msu_combine(r, MSU{ms[b].x, ms[b].y, u[b]});
+          } else {
+            const MS t = ms_combine(MS{r.m, r.s}, MS{ms[b].x, ms[b].y});
+            r.m = t.m;
+            r.s = t.s;
+          }
+        }
+    }
+  }
+#pragma unroll
+  for (int w = 1; w < kNSplit; w <<= 1) {
+    MSU b;
+    b.m = __shfl_down(r.m, w);
+    b.s = __shfl_down(r.s, w);
+    b.u = __shfl_down(r.u, w);
+    if constexpr (kMoment) {
+      r = msu_combine(r, b);
+    } else {
+      const MS t = ms_combine(MS{r.m, r.s}, MS{b.m, b.s});
+      r.m = t.m;
+      r.s = t.s;
+    }
+  }
+  return r;
+}
+
+// ---------------------------------------------------------------------------
+// The K best of a row, ties to the lowest id.
+//
+// A logit and its id make one 64-bit key (the logit's bits in an order that
+// integers keep, -0 as +0, then the id's complement): all keys of a row
+// differ, and a larger key is a better alternative.  Every one of the K best
+// lies in one of the K chunks with the largest (max, then lowest number):
+// of a chunk that is not among them, each of those K holds a better logit.
+// So: tau = the K-th largest chunk max (bit by bit, counting the chunks at or
+// above), the chunks above tau and then the first ones at tau, K in all; of
+// their logits those at or above tau go to a list; the list's K best by
+// counting.  When the list fills up it is cut to its K best, and tau to the
+// last of them (ties in number: the cut keeps the lowest ids).
+// Vocabularies of more than kSelChunks chunks take runs of R chunks as one.
+// ---------------------------------------------------------------------------
+constexpr int kSelWaves = 4;      // rows per block, one wave each
+constexpr int kSelChunks = 2048;  // chunk maxima of a row in LDS
+constexpr int kSelList = 512;     // keys of a row in LDS
+static_assert(kSelList >= kMaxK + 64, "room for a step after a cut");
+
+__device__ __forceinline__ uint32_t ordered_bits(float x) {
+  const uint32_t b = __float_as_uint(x + 0.f);
+  return b ^ ((b >> 31) ? 0xFFFFFFFFu : 0x80000000u);
+}
+__device__ __forceinline__ float from_ordered(uint32_t o) {
+  return __uint_as_float(o ^ ((o >> 31) ? 0x80000000u : 0xFFFFFFFFu));
+}
+
+// The lanes of a wave see one another's LDS writes.
+__device__ __forceinline__ void wave_lds_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
+// list[0..n) -> its min(n, K) best in descending order; returns their number.
+__device__ __forceinline__ int keep_best(uint64_t* list, int n, int K) {
+  const int lane = threadIdx.x & 63;
+  constexpr int kPer = kSelList / 64;
+  uint64_t x[kPer];
+  int rank[kPer];
+#pragma unroll
+  for (int e = 0; e < kPer; ++e) {
+    x[e] = 64 * e + lane < n ? list[64 * e + lane] : 0;
+    rank[e] = 0;
+  }
+  for (int j = 0; j < n; ++j) {
+    const uint64_t b = list[j];
+#pragma unroll
+    for (int e = 0; e < kPer; ++e)
+      if (64 * e < n) rank[e] += b > x[e];
+  }
+  wave_lds_sync();
+#pragma unroll
+  for (int e = 0; e < kPer; ++e)
+    if (64 * e + lane < n && rank[e] < K) list[rank[e]] = x[e];
+  wave_lds_sync();
+  return min(n, K);
+}
+
+struct TopMergeArgs {
+  const float2* rec;
+  const float* rec_u;
+  size_t rec_stride;
+  const float* zt;
+  const int32_t* idx;
+  const int32_t* n_act;
+  const int32_t* y;
+  SplitGeom gm;    // gm.s0: first split of the group
+  int G;           // splits of the group whose logits z holds
+  int first, last; // is it the first / last group
+  int R;           // chunks taken as one
+  const float* z;
+  int64_t ldz;
+  int K;
+  uint64_t* best;  // [active row][K] keys of the groups so far, best first
+  float* logp;
+  float* lse;      // may be NULL
+  float* entropy;
+  float* top_logp;
+  int32_t* top_ids;
+};
+
+__global__ __launch_bounds__(64 * kSelWaves) void top_merge(TopMergeArgs a) {
+  __shared__ uint32_t maxima[kSelWaves][kSelChunks];
+  __shared__ uint64_t lists[kSelWaves][kSelList];
+  __shared__ int32_t picks[kSelWaves][kMaxK];
+  const int w = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const int i = blockIdx.x * kSelWaves + w;
+  if (i >= *a.n_act) return;  // (a wave's rows are its own: no block barrier below)
+  uint64_t* list = lists[w];
+  int n = 0;
+  if (a.K > 0) {
+    uint32_t* mx = maxima[w];
+    // maxima of the group's chunks (0: no columns)
+    const int nch = a.G * a.gm.cps, nq = (nch + a.R - 1) / a.R;
+    int valid = 0;
+    for (int q0 = 0; q0 < nq; q0 += 64) {
+      const int q = q0 + lane;
+      uint32_t m = 0;
+      for (int c = q * a.R; q < nq && c < min((q + 1) * a.R, nch); ++c) {
+        const int sl = c / a.gm.cps, j = c - sl * a.gm.cps;
+        const int sbeg = (a.gm.s0 + sl) * a.gm.S;
+        if (sbeg + j * kChunk >= min(sbeg + a.gm.S, a.gm.V)) continue;
+        m = max(m, ordered_bits(a.rec[((size_t)a.gm.s0 * a.gm.cps + c) * a.rec_stride + i].x));
+      }
+      if (q < nq) mx[q] = m;
+      valid += __builtin_popcountll(__builtin_amdgcn_ballot_w64(m != 0));
+    }
+    wave_lds_sync();
+    // the largest tau that K chunks reach
+    uint32_t tau = 0;
+    if (valid > a.K) {
+      for (int b = 31; b >= 0; --b) {
+        const uint32_t t = tau | (1u << b);
+        int c = 0;
+        for (int q0 = 0; q0 < nq; q0 += 64)
+          c += __builtin_popcountll(__builtin_amdgcn_ballot_w64(q0 + lane < nq && mx[q0 + lane] >= t));
+        if (c >= a.K) tau = t;
+        if (c == a.K) break;
+      }
+    }
+    // the chunks above tau, then the first ones at tau
+    int np = 0;
+    for (int at = 0; at < 2; ++at)
+      for (int q0 = 0; q0 < nq && np < a.K; q0 += 64) {
+        const uint32_t m = q0 + lane < nq ? mx[q0 + lane] : 0;
+        const bool take = m != 0 && (at ? m == tau : m > tau);
+        const uint64_t mask = __builtin_amdgcn_ballot_w64(take);
+        const int p = np + __builtin_popcountll(mask & ((uint64_t(1) << lane) - 1));
+        if (take && p < a.K) picks[w][p] = q0 + lane;
+        np = min(a.K, np + __builtin_popcountll(mask));
+      }
+    uint64_t floor = (uint64_t)tau << 32;
+    if (!a.first) {
+      const uint64_t* b = a.best + (size_t)i * a.K;
+      for (int k = lane; k < a.K; k += 64) list[k] = b[k];
+      for (int k0 = 0; k0 < a.K; k0 += 64)
+        n += __builtin_popcountll(__builtin_amdgcn_ballot_w64(k0 + lane < a.K && b[k0 + lane] != 0));
+      if (n == a.K) floor = max(floor, b[a.K - 1]);
+    }
+    wave_lds_sync();
+    // their logits, two columns a lane, kAhead chunks in flight
+    constexpr int kAhead = 8;
+    const float* zr = a.z + (size_t)i * a.ldz;
+    const int np_c = np * a.R;
+    for (int p0 = 0; p0 < np_c; p0 += kAhead) {
+      float2 v[kAhead];
+      int col[kAhead], end[kAhead];  // first column of the chunk and end of its split
+#pragma unroll
+      for (int e = 0; e < kAhead; ++e) {
+        const int p = p0 + e;
+        const int c = p < np_c ? picks[w][p / a.R] * a.R + p % a.R : nch;
+        col[e] = end[e] = 0;
+        if (c < nch) {
+          const int sl = c / a.gm.cps, j = c - sl * a.gm.cps;
+          const int sbeg = (a.gm.s0 + sl) * a.gm.S;
+          col[e] = sbeg + j * kChunk;
+          end[e] = min(sbeg + a.gm.S, a.gm.V);
+          if (col[e] < end[e]) v[e] = *reinterpret_cast<const float2*>(zr + (size_t)c * kChunk + 2 * lane);
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < kAhead; ++e) {
+        if (col[e] >= end[e]) continue;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int id = col[e] + 2 * lane + h;
+          const float x = h ? v[e].y : v[e].x;
+          const uint64_t key = (uint64_t)ordered_bits(x) << 32 | (0xFFFFFFFFu - (uint32_t)id);
+          const bool take = id < end[e] && x == x && key >= floor;
+          const uint64_t mask = __builtin_amdgcn_ballot_w64(take);
+          if (!mask) continue;
+          if (n + __builtin_popcountll(mask) > kSelList) {
+            wave_lds_sync();
+            n = keep_best(list, n, a.K);
+            floor = max(floor, list[a.K - 1]);  // n == K: the list held more
+          }
+          if (take) list[n + __builtin_popcountll(mask & ((uint64_t(1) << lane) - 1))] = key;
+          n += __builtin_popcountll(mask);
+        }
+      }
+    }
+    wave_lds_sync();
+    n = keep_best(list, n, a.K);
+    if (!a.last)
+      for (int k = lane; k < a.K; k += 64) a.best[(size_t)i * a.K + k] = k < n ? list[k] : 0;
+  }
+  if (!a.last) return;
+  const MSU tot = fold_row<true>(a.rec, a.rec_u, a.rec_stride, i, a.gm);
+  const float m = __shfl(tot.m, 0), L = rlk_log(__shfl(tot.s, 0));
+  const int t = a.idx[i];
+  if (lane == 0) {
+    const int yt = a.y[t];
+    a.logp[t] = yt >= 0 && yt < a.gm.V ? (a.zt[i] - m) - L : __builtin_nanf("");
+    if (a.lse) a.lse[t] = m + L;
+    a.entropy[t] = L - tot.u / tot.s;
+  }
+  for (int k = lane; k < a.K; k += 64) {
+    const bool some = k < n;
+    const uint64_t key = some ? list[k] : 0;
+    a.top_ids[(size_t)t * a.K + k] = some ? (int32_t)(0xFFFFFFFFu - (uint32_t)key) : -1;
+    a.top_logp[(size_t)t * a.K + k] = some ? (from_ordered((uint32_t)(key >> 32)) - m) - L : -INFINITY;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// The divergence of a row: loss = sum_k q_k (log q_k - log p_k),
+// log p_k = (z_k - m) - log s of the teacher's tokens.  One wave per row.
+// ---------------------------------------------------------------------------
+struct DistillMergeArgs {
+  const float2* rec;
+  size_t rec_stride;
+  const int32_t* idx;
+  const int32_t* n_act;
+  SplitGeom gm;
+  int K;
+  float scale;
+  const int32_t* ids;
+  const float* logits;
+  const float* z_ids;  // [active row][K], scaled
+  float* loss;
+  float* lse;
+  float* logp_ids;
+};
+
+__global__ __launch_bounds__(256) void distill_merge(DistillMergeArgs a) {
+  const int lane = threadIdx.x & 63, i = blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (i >= *a.n_act) return;
+  const MSU tot = fold_row<false>(a.rec, nullptr, a.rec_stride, i, a.gm);
+  const float m = __shfl(tot.m, 0), L = rlk_log(__shfl(tot.s, 0));
+  const int t = a.idx[i];
+  const TeacherRow r = teacher_row(a.ids + (size_t)t * a.K, a.logits + (size_t)t * a.K, a.K, a.scale);
+  float sum = 0.f;
+#pragma unroll
+  for (int s = 0; s < kSlots2; ++s) {
+    const int k = lane + 64 * s;
+    if (k >= a.K) continue;
+    float lp = -INFINITY;
+    if (r.kept[s]) {
+      lp = r.id[s] < a.gm.V ? (a.z_ids[(size_t)i * a.K + k] - m) - L : __builtin_nanf("");
+      // a token that the teacher gives no weight adds nothing, whatever the student gives it
+      if (r.q[s] != 0.f || lp != lp) sum = sum + r.q[s] * (r.lq[s] - lp);
+    }
+    a.logp_ids[(size_t)t * a.K + k] = lp;
+  }
+  sum = wave_sum(sum);
+  if (lane == 0) {
+    a.loss[t] = sum;
+    a.lse[t] = m + L;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// dz of a group of splits from recomputed logits, bf16: tiles, staging and
+// stores as in dz_tiles;
+//     dz_v = g [v == target] - p_v (a + b (z_v - lse)),  p_v = e(z_v - lse),
+// z scaled by 1 / temperature.  fp32, each operation rounded once, then bf16
+// once: dz is an operand of the gradients' bf16 products.
+// kTop: with target and b; !kTop: a alone.
+// ---------------------------------------------------------------------------
+struct SoftDzArgs {
+  const uint16_t* hA;
+  const uint16_t* W;
+  const float4* rowinfo;  // {lse, a, b, target (bits)}
+  const float* rowg;      // g
+  const int32_t* n_act;
+  int H;
+  float scale;
+  SplitGeom gm;
+  TileGeom tg;
+  BwdGeom bg;
+  uint16_t* dZ;
+};
+
+template <bool kTop>
+__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(RLK_WAVES / 4, RLK_WAVES / 4))) void soft_dz_tiles(
+    SoftDzArgs a) {
+  __shared__ u32x4 lds[kLdsU4];
+  const int n_act = __builtin_amdgcn_readfirstlane(*a.n_act);
+  const int rtiles = (n_act + kBM - 1) / kBM;
+  const int C = a.bg.G * a.tg.tps;
+  const int id = xcd_tile(rtiles * C, blockIdx.x);
+  if (id < 0) return;
+  int rt, ct;
+  grouped_tile(id, rtiles, rt, ct, C, row_group(rtiles));
+  const int i0 = rt * kBM;
+  const int sc = ct / a.tg.tps, j = ct - sc * a.tg.tps;
+  const int sbeg = (a.bg.c_lo + sc) * a.gm.S;
+  const int valid_s = max(0, min(a.gm.S, a.gm.V - sbeg));  // columns of this split
+  const int c0 = sbeg + j * kBN;
+  const int c1 = sbeg + min(j * kBN + kBN, valid_s);
+  const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), wm = wave_m(w),
+            wn = wave_n(w);
+  float4 ri[kMI];  // loaded as in dz_tiles
+  const auto load_rows = [&]() {
+#pragma unroll
+    for (int mi = 0; mi < kTailRows; ++mi) ri[mi] = a.rowinfo[i0 + acc_row(wm, mi, lane)];
+  };
+  Acc acc;
+  acc_zero(acc);
+  {
+    // a tile past the vocabulary runs on W's first row and is written as zeros
+    const RowsK A = rows_k(a.hA + (size_t)i0 * a.H, kBM - 1, a.H);
+    const RowsK B = c0 < c1 ? rows_k(a.W + (size_t)c0 * a.H, c1 - 1 - c0, a.H) : rows_k(a.W, 0, a.H);
+    gemm256<false, false>(A, B, a.H / kBK, acc, lds, load_rows);
+  }
+  int le = lane;  // an opaque copy, see fwd_tiles
+  asm volatile("" : "+v"(le));
+#pragma unroll
+  for (int mi = kTailRows; mi < kMI; ++mi) ri[mi] = a.rowinfo[i0 + acc_row(wm, mi, le)];
+  uint16_t* dzs = a.dZ + (size_t)sc * a.bg.S_pad;
+  // staging in LDS as in dz_tiles: 256 rows x 512 bytes, 16-byte unit u of row r at r * 512 + 16 (u ^ (r & 31))
+  char* stage = reinterpret_cast<char*>(lds);
+  auto put = [&](int r, int c, const float (&d)[4]) {
+    const uint32_t off = 512u * r + 16u * ((c >> 3) ^ (r & 31)) + 8u * ((c >> 2) & 1);
+    *reinterpret_cast<uint2*>(stage + off) = make_uint2(pack_bf16x2(d[0], d[1]), pack_bf16x2(d[2], d[3]));
+  };
+  const auto minus_share = [&](float z, const float4& r) {  // -p (a + b d)
+    const float d = (kTop ? z : z * a.scale) - r.x;
+    const float p = rlk_exp(d);
+    if constexpr (kTop) return -(p * (r.y + r.z * fmaxf(d, kDeepest)));
+    else return -(p * r.y);
+  };
+  const int wc0 = j * kBN + 128 * wn;  // first column of the wave within the split
+  const bool full = i0 + kWaveRows * wm + kWaveRows <= n_act && wc0 + 128 <= valid_s;
+#pragma unroll
+  for (int mi = 0; mi < kMI; ++mi) {
+    const int r = acc_row(wm, mi, le);
+    const bool rvalid = i0 + r < n_act;
+    const int yl = kTop ? __float_as_int(ri[mi].w) - sbeg : -1;  // target column within the split
+    const int tl = yl - wc0;
+    const bool hit = kTop && tl >= 0 && tl < 128 && ((tl >> 2) & (kLPR - 1)) == row_lane(le);
+    if (full && !__builtin_amdgcn_ballot_w64(hit)) {
+#pragma unroll
+      for (int ni = 0; ni < kNI; ++ni)
+#pragma unroll
+        for (int q = 0; q < kQL; ++q) {
+          float d[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) d[e] = minus_share(acc.c[mi][ni][4 * q + e], ri[mi]);
+          put(r, acc_col4(wn, ni, q, le), d);
+        }
+    } else {
+      const float g = kTop ? a.rowg[i0 + r] : 0.f;
+#pragma unroll
+      for (int ni = 0; ni < kNI; ++ni)
+#pragma unroll
+        for (int q = 0; q < kQL; ++q) {
+          if (j * kBN + 128 * wn + kBlk * ni + 4 * kLPR * q >= a.bg.S_pad) continue;  // never stored
+          const int c = acc_col4(wn, ni, q, le);
+          float d[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int vl = j * kBN + c + e;
+            const float x = minus_share(acc.c[mi][ni][4 * q + e], ri[mi]);
+            d[e] = rvalid && vl < valid_s ? (kTop && vl == yl ? g + x : x) : 0.f;
+          }
+          put(r, c, d);
+        }
+    }
+  }
+  __syncthreads();
+  constexpr int kRowsW = kBM / kWaves;
+  const int u = le & 31;
+  const int col = j * kBN + 8 * u;  // column within the split
+  if (col < a.bg.S_pad) {
+#pragma unroll
+    for (int it = 0; it < kRowsW / 2; ++it) {
+      const int r = kRowsW * w + 2 * it + (le >> 5);
+      const u32x4 v = *reinterpret_cast<const u32x4*>(stage + 512u * r + 16u * (u ^ (r & 31)));
+      __builtin_nontemporal_store(v, reinterpret_cast<u32x4*>(dzs + (size_t)(i0 + r) * a.bg.ldz + col));
+    }
+  }
+}
+
+// dz at the teacher's tokens of the group: a (q - p) with a = -dL/dloss /
+// temperature and p = e(log p) of the forward.  A token in several slots of
+// a row has the sum of their q, in slot order, written by the first of them.
+// Block kMaxK, one thread per slot, rows strided over the grid.
+struct ScatterArgs {
+  const int32_t* ids;
+  const float* q;         // [T][K], 0 for slots that are not kept
+  const float* logp_ids;  // [T][K]
+  const float* logits;
+  const int32_t* idx;
+  const int32_t* n_act;
+  const float4* rowinfo;
+  int K;
+  SplitGeom gm;
+  BwdGeom bg;
+  uint16_t* dZ;
+};
+
+__global__ __launch_bounds__(kMaxK) void distill_scatter(ScatterArgs a) {
+  __shared__ int32_t id_s[kMaxK];
+  __shared__ float q_s[kMaxK];
+  const int k = threadIdx.x, n_act = *a.n_act;
+  for (int i = blockIdx.x; i < n_act; i += gridDim.x) {
+    const size_t at = (size_t)a.idx[i] * a.K + k;
+    int id = -1;
+    if (k < a.K && slot_kept(a.ids[at], a.logits[at])) id = a.ids[at];
+    if (id >= a.gm.V) id = -1;
+    __syncthreads();
+    id_s[k] = id;
+    q_s[k] = id >= 0 ? a.q[at] : 0.f;
+    __syncthreads();
+    if (id < 0) continue;
+    const int s = id / a.gm.S - a.bg.c_lo;
+    if (s < 0 || s >= a.bg.G) continue;
+    bool first = true;
+    float q = 0.f;
+    for (int j = 0; j < a.K; ++j) {
+      const bool same = id_s[j] == id;
+      first &= !(same && j < k);
+      if (same) q = q + q_s[j];
+    }
+    if (!first) continue;
+    const float p = rlk_exp(a.logp_ids[at]);
+    const float d = a.rowinfo[i].y * (q - p);
+    const int c = id - (s + a.bg.c_lo) * a.gm.S;
+    a.dZ[(size_t)i * a.bg.ldz + (size_t)s * a.bg.S_pad + c] = (uint16_t)pack_bf16x2(d, d);
+  }
+}
+
+// grad_W of the group as bf16, each fp32 sum rounded once (grad_tiles,
+// rlk_kernels.h, has it in fp32).
+__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(RLK_WAVES / 4, RLK_WAVES / 4))) void gradw_bf16_tiles(
+    GradWArgs a) {
+  __shared__ u32x4 lds[kLdsU4];
+  const int n_act = __builtin_amdgcn_readfirstlane(*a.n_act);
+  const int id = xcd_tile(a.n_tiles * a.bg.G * a.tps, blockIdx.x);
+  if (id >= 0) gradw_tile<true>(a, id, n_act, lds);
+}
+
+}  // namespace vocab
+}  // namespace rlk

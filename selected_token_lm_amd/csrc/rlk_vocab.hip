@@ -1,0 +1,592 @@
+// The operators of include/rlk/vocab_ops.h: their kernels, on the eight-wave
+// tile engine, and their C entry points.  Everything is enqueued on the
+// caller's stream; nothing here allocates device memory or synchronises.
+#ifdef RLK_WAVES
+#undef RLK_WAVES
+#endif
+#define RLK_WAVES 8
+#define RLK_ENGINE_W8
+#define RLK_ENGINE_PARTS
+#include "rlk/vocab_ops.h"
+
+#include "rlk_host.h"
+#include "rlk_rows.h"
+#include "rlk_vocab.h"
+
+namespace rlk {
+namespace vocab {
+
+// Zeroes n 16-byte words and the bytes after them (T == 0: grad_W).
+__global__ __launch_bounds__(256) void zero_bytes(u32x4* p, int64_t n16) {
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n16; i += (int64_t)gridDim.x * 256)
+    p[i] = u32x4{0u, 0u, 0u, 0u};
+}
+
+}  // namespace vocab
+}  // namespace rlk
+
+namespace {
+
+using namespace rlk::vocab;
+static_assert(RLK_MAX_K == kMaxK, "the header's limit");
+static_assert(rlk::kThreads == rlk::kThreadsW8, "eight-wave kernels");
+
+inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// Consecutive pieces of a workspace, each at a multiple of 256 bytes.
+struct Pieces {
+  size_t total = 0;
+  size_t take(size_t bytes) {
+    const size_t at = total;
+    total = align256(total + bytes);
+    return at;
+  }
+};
+
+inline int64_t padded_rows(int64_t T) { return ceil_div(std::max<int64_t>(T, 1), rlk::kBM) * rlk::kBM; }
+
+// linear_logp_top, forward: G splits of logits at a time.
+struct TopFwdWs {
+  size_t idx, yA, n_act, zt, hA, rec, rec_u, z, best, total;
+  int64_t T_pad, G, ldz;
+};
+
+inline TopFwdWs top_fwd_layout(int64_t T, int64_t H, int64_t V, int64_t K) {
+  const Geom g = geom_of(V);
+  TopFwdWs w;
+  w.T_pad = padded_rows(T);
+  w.G = rlk::kNSplit;
+  if (K > 0) {
+    const int64_t per_split = 4 * T * g.cps * rlk::kChunk, budget = dz_budget_bytes();
+    while (w.G > 1 && w.G * per_split > budget) w.G /= 2;
+  }
+  w.ldz = w.G * g.cps * rlk::kChunk;
+  Pieces p;
+  w.idx = p.take(sizeof(int32_t) * T);
+  w.yA = p.take(sizeof(int32_t) * T);
+  w.n_act = p.take(sizeof(int32_t));
+  w.zt = p.take(sizeof(float) * T);
+  w.hA = p.take(2 * (size_t)w.T_pad * H);
+  const size_t records = (size_t)rlk::kNSplit * g.cps * T;
+  w.rec = p.take(sizeof(float2) * records);
+  w.rec_u = p.take(sizeof(float) * records);
+  w.z = p.take(K > 0 ? sizeof(float) * (size_t)T * w.ldz : 0);
+  w.best = p.take(w.G < rlk::kNSplit ? sizeof(uint64_t) * (size_t)T * K : 0);
+  w.total = p.total;
+  return w;
+}
+
+struct DistillFwdWs {
+  size_t act, idx, n_act, hA, rec, off, ent, z_ids, total;
+  int64_t T_pad;
+};
+
+inline DistillFwdWs distill_fwd_layout(int64_t T, int64_t H, int64_t V, int64_t K) {
+  const Geom g = geom_of(V);
+  DistillFwdWs w;
+  w.T_pad = padded_rows(T);
+  Pieces p;
+  w.act = p.take(sizeof(int32_t) * T);
+  w.idx = p.take(sizeof(int32_t) * T);
+  w.n_act = p.take(sizeof(int32_t));
+  w.hA = p.take(2 * (size_t)w.T_pad * H);
+  w.rec = p.take(sizeof(float2) * (size_t)rlk::kNSplit * g.cps * T);
+  w.off = p.take(sizeof(int32_t) * (size_t)(w.T_pad / rlk::kBM) * (rlk::kNSplit * ceil_div(g.S, rlk::kBN) + 1));
+  w.ent = p.take(sizeof(uint32_t) * (size_t)w.T_pad * K);
+  w.z_ids = p.take(sizeof(float) * (size_t)T * K);
+  w.total = p.total;
+  return w;
+}
+
+// Both backwards: bwd_layout's pieces, the rows' g, and (distill, K > 0) the
+// teacher's rows.
+struct SoftBwdWs {
+  BwdWs core;
+  size_t rowg, act, q, total;
+};
+
+inline SoftBwdWs soft_bwd_layout(int64_t T, int64_t H, int64_t V, int64_t K) {
+  SoftBwdWs w;
+  w.core = bwd_layout(T, H, V);
+  Pieces p;
+  p.take(w.core.total);
+  w.rowg = p.take(sizeof(float) * w.core.T_pad);
+  w.act = p.take(K > 0 ? sizeof(int32_t) * T : 0);
+  w.q = p.take(sizeof(float) * (size_t)T * K);
+  w.total = p.total;
+  return w;
+}
+
+template <class T>
+T* at(void* ws, size_t off) {
+  return reinterpret_cast<T*>(static_cast<char*>(ws) + off);
+}
+
+inline rlk_status check_sizes(int64_t T, int64_t H, int64_t V, int64_t K, int64_t least_k) {
+  if (T < 0 || T > kMaxT) return fail(RLK_ERR_BAD_SHAPE, "T=%lld out of [0, 2^24]", (long long)T);
+  if (H <= 0 || H > kMaxH || H % 64 != 0)
+    return fail(RLK_ERR_BAD_SHAPE, "H=%lld must be a positive multiple of 64 up to 65536", (long long)H);
+  if (V <= 0 || V > kMaxV) return fail(RLK_ERR_BAD_SHAPE, "V=%lld out of [1, 8000000]", (long long)V);
+  if (K < least_k || K > kMaxK)
+    return fail(RLK_ERR_BAD_SHAPE, "K=%lld out of [%lld, %d]", (long long)K, (long long)least_k, kMaxK);
+  return RLK_OK;
+}
+
+// 1 / temperature; the kernels multiply by it.
+inline rlk_status check_temperature(float t, float* scale) {
+  *scale = 1.f / t;
+  if (!(t > 0.f) || !(t <= 3.402823466e38f) || !(*scale > 0.f && *scale <= 3.402823466e38f))
+    return fail(RLK_ERR_BAD_ARG, "temperature=%g must be positive and finite, and so its reciprocal", (double)t);
+  return RLK_OK;
+}
+
+inline rlk::SplitGeom split_geom(int64_t V) {
+  const Geom g = geom_of(V);
+  rlk::SplitGeom gm;
+  gm.V = (int)g.V;
+  gm.S = (int)g.S;
+  gm.cps = (int)g.cps;
+  gm.s0 = 0;
+  gm.vocab_start = 0;
+  return gm;
+}
+
+// The last split that holds columns.
+inline int last_split(const rlk::SplitGeom& gm) { return (gm.V - 1) / gm.S; }
+
+#define RLK_LAUNCH_V(kern, grid, block, st, ...) RLK_LAUNCH(vocab::kern, grid, block, st, __VA_ARGS__)
+
+inline rlk_status compact(hipStream_t st, const int32_t* y, int64_t T, int32_t ignore, int32_t* idx, int32_t* yA,
+                          int32_t* n_act, float* z0, float* z1, float* z2) {
+  {
+    ProfScope _ps("compact_rows", st);
+    rlk::launch_compact_rows(st, y, (int)T, ignore, idx, yA, n_act, z0, z1, z2);
+  }
+  return launched("compact_rows");
+}
+
+inline dim3 row_grid(int64_t rows) { return dim3((unsigned)std::min(rows, kRowBlocks)); }
+
+rlk_status run_top_fwd(const void* h, const void* W, const int32_t* y, int64_t T, int64_t H, int64_t V, int32_t ignore,
+                       int64_t K, float* logp, float* lse, float* entropy, float* top_logp, int32_t* top_ids, void* ws,
+                       hipStream_t st) {
+  const TopFwdWs L = top_fwd_layout(T, H, V, K);
+  int32_t* idx = at<int32_t>(ws, L.idx);
+  int32_t* yA = at<int32_t>(ws, L.yA);
+  int32_t* n_act = at<int32_t>(ws, L.n_act);
+  LogitArgs la{};
+  la.gm = split_geom(V);
+  la.tg.tps = (int)ceil_div(la.gm.S, rlk::kBN);
+  const int64_t blocks = 8 * ceil_div(ceil_div(T, rlk::kBM) * L.G * la.tg.tps, 8);
+  RLK_TRY(check_grid(blocks));
+  RLK_TRY(compact(st, y, T, ignore, idx, yA, n_act, logp, lse, entropy));
+  GatherArgs ga{};
+  ga.h = static_cast<const uint16_t*>(h);
+  ga.idx = idx;
+  ga.n_act = n_act;
+  ga.T = (int)T;
+  ga.rows = (int)L.T_pad;
+  ga.H = (int)H;
+  ga.hA = at<uint16_t>(ws, L.hA);
+  ga.act = y;
+  ga.ignore_index = ignore;
+  ga.K = (int)K;
+  ga.slot_logp = top_logp;
+  ga.slot_ids = top_ids;
+  RLK_LAUNCH_V(gather_rows_fill, row_grid(L.T_pad), dim3(256), st, ga);
+  la.hA = ga.hA;
+  la.W = static_cast<const uint16_t*>(W);
+  la.n_act = n_act;
+  la.H = (int)H;
+  la.G = (int)L.G;
+  la.rec_stride = (size_t)T;
+  la.rec = at<float2>(ws, L.rec);
+  la.yA = yA;
+  la.zt = at<float>(ws, L.zt);
+  la.rec_u = at<float>(ws, L.rec_u);
+  la.z = K > 0 ? at<float>(ws, L.z) : nullptr;
+  la.ldz = L.ldz;
+  TopMergeArgs ma{};
+  ma.rec = la.rec;
+  ma.rec_u = la.rec_u;
+  ma.rec_stride = la.rec_stride;
+  ma.zt = la.zt;
+  ma.idx = idx;
+  ma.n_act = n_act;
+  ma.y = y;
+  ma.G = (int)L.G;
+  ma.R = (int)ceil_div(L.G * la.gm.cps, kSelChunks);
+  ma.z = la.z;
+  ma.ldz = L.ldz;
+  ma.K = (int)K;
+  ma.best = at<uint64_t>(ws, L.best);
+  ma.logp = logp;
+  ma.lse = lse;
+  ma.entropy = entropy;
+  ma.top_logp = top_logp;
+  ma.top_ids = top_ids;
+  const int last = last_split(la.gm);
+  for (int c = 0; c <= last; c += (int)L.G) {
+    la.gm.s0 = c;
+    RLK_LAUNCH_FN("logit_tiles", (rlk::vocab::logit_tiles<true>), dim3((unsigned)blocks), dim3(rlk::kThreads), st, la);
+    ma.gm = la.gm;
+    ma.first = c == 0;
+    ma.last = c + L.G > last;
+    RLK_LAUNCH_V(top_merge, dim3((unsigned)ceil_div(T, kSelWaves)), dim3(64 * kSelWaves), st, ma);
+  }
+  return RLK_OK;
+}
+
+rlk_status run_distill_fwd(const void* h, const void* W, const int32_t* ids, const float* logits, int64_t T, int64_t H,
+                           int64_t V, int64_t K, float scale, float* loss, float* lse, float* logp_ids, void* ws,
+                           hipStream_t st) {
+  const DistillFwdWs L = distill_fwd_layout(T, H, V, K);
+  int32_t* act = at<int32_t>(ws, L.act);
+  int32_t* idx = at<int32_t>(ws, L.idx);
+  int32_t* n_act = at<int32_t>(ws, L.n_act);
+  LogitArgs la{};
+  la.gm = split_geom(V);
+  la.tg.tps = (int)ceil_div(la.gm.S, rlk::kBN);
+  const int64_t row_tiles = ceil_div(T, rlk::kBM);
+  const int64_t blocks = 8 * ceil_div(row_tiles * rlk::kNSplit * la.tg.tps, 8);
+  RLK_TRY(check_grid(blocks));
+  RLK_LAUNCH_V(distill_rows, row_grid(ceil_div(T, 4)), dim3(256), st, ids, logits, (int)T, (int)K, (int)V, scale, act,
+               nullptr);
+  RLK_TRY(compact(st, act, T, -100, idx, nullptr, n_act, loss, lse, nullptr));
+  GatherArgs ga{};
+  ga.h = static_cast<const uint16_t*>(h);
+  ga.idx = idx;
+  ga.n_act = n_act;
+  ga.T = (int)T;
+  ga.rows = (int)L.T_pad;
+  ga.H = (int)H;
+  ga.hA = at<uint16_t>(ws, L.hA);
+  ga.act = act;
+  ga.ignore_index = -100;
+  ga.K = (int)K;
+  ga.slot_logp = logp_ids;
+  RLK_LAUNCH_V(gather_rows_fill, row_grid(L.T_pad), dim3(256), st, ga);
+  la.ent_off = at<int32_t>(ws, L.off);
+  la.ent = at<uint32_t>(ws, L.ent);
+  RLK_LAUNCH_V(bucket_entries, dim3((unsigned)row_tiles), dim3(kBucketThreads), st, ids, logits, idx, n_act, (int)K,
+               la.gm, la.tg.tps, at<int32_t>(ws, L.off), at<uint32_t>(ws, L.ent));
+  la.hA = ga.hA;
+  la.W = static_cast<const uint16_t*>(W);
+  la.n_act = n_act;
+  la.H = (int)H;
+  la.G = rlk::kNSplit;
+  la.rec_stride = (size_t)T;
+  la.rec = at<float2>(ws, L.rec);
+  la.scale = scale;
+  la.K = (int)K;
+  la.z_ids = at<float>(ws, L.z_ids);
+  RLK_LAUNCH_FN("logit_tiles", (rlk::vocab::logit_tiles<false>), dim3((unsigned)blocks), dim3(rlk::kThreads), st, la);
+  DistillMergeArgs ma{};
+  ma.rec = la.rec;
+  ma.rec_stride = la.rec_stride;
+  ma.idx = idx;
+  ma.n_act = n_act;
+  ma.gm = la.gm;
+  ma.K = (int)K;
+  ma.scale = scale;
+  ma.ids = ids;
+  ma.logits = logits;
+  ma.z_ids = la.z_ids;
+  ma.loss = loss;
+  ma.lse = lse;
+  ma.logp_ids = logp_ids;
+  RLK_LAUNCH_V(distill_merge, dim3((unsigned)ceil_div(T, 4)), dim3(256), st, ma);
+  return RLK_OK;
+}
+
+// What the two backwards have in common: gradients of dz in groups of
+// splits; `act` marks the inactive rows with `ignore`.  ids != NULL: distill.
+struct SoftBwd {
+  const void *h, *W;
+  const int32_t* act;
+  int32_t ignore;
+  int64_t T, H, V, K;
+  float scale;
+  const float *lse, *g, *entropy, *g_entropy;
+  const int32_t* ids;
+  const float *logits, *logp_ids;
+  void *grad_h, *grad_W;
+  int32_t dtype;
+};
+
+rlk_status run_soft_bwd(const SoftBwd& b, const SoftBwdWs& S, void* ws, hipStream_t st) {
+  const BwdWs& L = S.core;
+  const bool top = b.ids == nullptr;
+  int32_t* idx = at<int32_t>(ws, L.idx);
+  int32_t* n_act = at<int32_t>(ws, L.n_act);
+  const rlk::SplitGeom gm = split_geom(b.V);
+  const int tps = (int)ceil_div(gm.S, rlk::kBN), n_tiles = (int)ceil_div(b.H, rlk::kBN), G = (int)L.G;
+  const int64_t row_tiles = ceil_div(b.T, rlk::kBM);
+  const int64_t dz_blocks = 8 * ceil_div(row_tiles * G * tps, 8);
+  const bool passes = b.grad_h && grad_h_passes(row_tiles, n_tiles);
+  const int64_t gh_blocks = b.grad_h ? 8 * ceil_div(row_tiles * n_tiles * (passes ? 2 : 1), 8) : 0;
+  const int64_t gw_blocks = b.grad_W ? 8 * ceil_div((int64_t)n_tiles * G * tps, 8) : 0;
+  RLK_TRY(check_grid(dz_blocks));
+  RLK_TRY(check_grid(gh_blocks + gw_blocks));
+  if (!top)
+    RLK_LAUNCH_V(distill_rows, row_grid(ceil_div(b.T, 4)), dim3(256), st, b.ids, b.logits, (int)b.T, (int)b.K,
+                 (int)b.V, b.scale, at<int32_t>(ws, S.act), at<float>(ws, S.q));
+  RLK_TRY(compact(st, b.act, b.T, b.ignore, idx, nullptr, n_act, nullptr, nullptr, nullptr));
+  GatherGradArgs ga{};
+  ga.h = static_cast<const uint16_t*>(b.h);
+  ga.idx = idx;
+  ga.n_act = n_act;
+  ga.rows = (int)L.T_pad;
+  ga.H = (int)b.H;
+  ga.V = (int)b.V;
+  ga.hA = at<uint16_t>(ws, L.hA);
+  ga.lse = b.lse;
+  ga.g = b.g;
+  ga.rowinfo = at<float4>(ws, L.rowinfo);
+  ga.rowg = at<float>(ws, S.rowg);
+  ga.y = top ? b.act : nullptr;
+  ga.entropy = b.entropy;
+  ga.g_entropy = b.g_entropy;
+  ga.act = b.act;
+  ga.scale = b.scale;
+  if (top)
+    RLK_LAUNCH_FN("gather_rows_grad", (rlk::vocab::gather_rows_grad<true>), row_grid(L.T_pad), dim3(256), st, ga);
+  else
+    RLK_LAUNCH_FN("gather_rows_grad", (rlk::vocab::gather_rows_grad<false>), row_grid(L.T_pad), dim3(256), st, ga);
+  if (b.grad_h) {
+    {
+      ProfScope _ps("zero_rows", st);
+      rlk::launch_zero_rows(st, b.act, (int)b.T, b.ignore, (int)b.H, static_cast<uint16_t*>(b.grad_h));
+    }
+    RLK_TRY(launched("zero_rows"));
+  }
+  const int last = last_split(gm);
+  for (int c = 0; c <= last; c += G) {
+    rlk::BwdGeom bg;
+    bg.c_lo = c;
+    bg.G = G;
+    bg.S_pad = (int)L.S_pad;
+    bg.ldz = (int)(G * L.S_pad);
+    bg.T_pad = (int)L.T_pad;
+    SoftDzArgs da{};
+    da.hA = ga.hA;
+    da.W = static_cast<const uint16_t*>(b.W);
+    da.rowinfo = ga.rowinfo;
+    da.rowg = ga.rowg;
+    da.n_act = n_act;
+    da.H = (int)b.H;
+    da.scale = b.scale;
+    da.gm = gm;
+    da.tg.tps = tps;
+    da.bg = bg;
+    da.dZ = at<uint16_t>(ws, L.dZ);
+    const dim3 grid((unsigned)dz_blocks), block(rlk::kThreads);
+    if (top) {
+      RLK_LAUNCH_FN("soft_dz_tiles", (rlk::vocab::soft_dz_tiles<true>), grid, block, st, da);
+    } else {
+      RLK_LAUNCH_FN("soft_dz_tiles", (rlk::vocab::soft_dz_tiles<false>), grid, block, st, da);
+      ScatterArgs sa{};
+      sa.ids = b.ids;
+      sa.q = at<float>(ws, S.q);
+      sa.logp_ids = b.logp_ids;
+      sa.logits = b.logits;
+      sa.idx = idx;
+      sa.n_act = n_act;
+      sa.rowinfo = ga.rowinfo;
+      sa.K = (int)b.K;
+      sa.gm = gm;
+      sa.bg = bg;
+      sa.dZ = da.dZ;
+      RLK_LAUNCH_V(distill_scatter, row_grid(b.T), dim3(kMaxK), st, sa);
+    }
+    rlk::GradWArgs wa{};
+    wa.dZ = da.dZ;
+    wa.hA = ga.hA;
+    wa.n_act = n_act;
+    wa.H = (int)b.H;
+    wa.gm = gm;
+    wa.bg = bg;
+    wa.tps = tps;
+    wa.n_tiles = n_tiles;
+    wa.grad_W = static_cast<float*>(b.grad_W);
+    rlk::GradHArgs ha{};
+    ha.dZ = da.dZ;
+    ha.W = da.W;
+    ha.idx = idx;
+    ha.n_act = n_act;
+    ha.H = (int)b.H;
+    ha.gm = gm;
+    ha.bg = bg;
+    ha.n_tiles = n_tiles;
+    ha.ghacc = at<float>(ws, L.ghacc);
+    ha.grad_h = static_cast<uint16_t*>(b.grad_h);
+    const bool first = c == 0, fin = c + G > last;
+    // fp32 gradients in one launch; a bf16 grad_W in one of its own
+    const bool bf16 = b.grad_W && b.dtype == RLK_DT_BF16;
+    if (bf16) {
+      wa.grad_W = nullptr;
+      rlk::GradWArgs wb = wa;
+      wb.grad_W = static_cast<float*>(b.grad_W);
+      RLK_LAUNCH_V(gradw_bf16_tiles, dim3((unsigned)gw_blocks), block, st, wb);
+    }
+    if (b.grad_h || !bf16) {
+      {
+        ProfScope _ps("grad_tiles", st);
+        rlk::launch_grad_tiles_w8(first, fin, passes, dim3((unsigned)(gh_blocks + (bf16 ? 0 : gw_blocks))), st, ha, wa);
+      }
+      RLK_TRY(launched("grad_tiles"));
+    }
+  }
+  return RLK_OK;
+}
+
+// Checks of the gradients' outputs; T == 0 zeroes grad_W (the sum over no
+// rows) and is done (*done).
+rlk_status check_grads(int64_t T, int64_t H, int64_t V, const void* grad_h, void* grad_W, int32_t dtype,
+                       hipStream_t st, bool* done) {
+  *done = false;
+  if (dtype != RLK_DT_F32 && dtype != RLK_DT_BF16) return fail(RLK_ERR_BAD_ARG, "grad_W_dtype=%d", dtype);
+  if ((grad_h && !aligned16(grad_h)) || (grad_W && !aligned16(grad_W)))
+    return fail(RLK_ERR_BAD_ALIGNMENT, "grad_h, grad_W must be 16-byte aligned");
+  if (T > 0) return RLK_OK;
+  *done = true;
+  if (!grad_W) return RLK_OK;
+  RLK_TRY(check_device());
+  const int64_t n16 = V * H * (dtype == RLK_DT_F32 ? 4 : 2) / 16;  // H % 64 == 0
+  RLK_LAUNCH_V(zero_bytes, row_grid(ceil_div(n16, 256)), dim3(256), st,
+               static_cast<rlk::u32x4*>(grad_W), n16);
+  return RLK_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t rlk_vocab_workspace_bytes(int32_t op, int64_t T, int64_t H, int64_t V, int64_t K) {
+  if (T < 0 || T > kMaxT || H <= 0 || H > kMaxH || H % 64 != 0 || V <= 0 || V > kMaxV || K < 0 || K > kMaxK) return 0;
+  switch (op) {
+    case RLK_VOP_TOP_FWD: return top_fwd_layout(T, H, V, K).total;
+    case RLK_VOP_TOP_BWD: return soft_bwd_layout(T, H, V, 0).total;
+    case RLK_VOP_DISTILL_FWD: return K > 0 ? distill_fwd_layout(T, H, V, K).total : 0;
+    case RLK_VOP_DISTILL_BWD: return K > 0 ? soft_bwd_layout(T, H, V, K).total : 0;
+    default: return 0;
+  }
+}
+
+rlk_status rlk_linear_logp_top_fwd(const void* h, const void* W, const int32_t* y, int64_t T, int64_t H, int64_t V,
+                                   int32_t ignore_index, int64_t K, float* logp, float* lse, float* entropy,
+                                   float* top_logp, int32_t* top_ids, void* ws, size_t ws_bytes, void* stream) {
+  RLK_TRY(check_sizes(T, H, V, K, 0));
+  if (T == 0) return ok();
+  if (!h || !W || !y || !logp || !entropy || !ws || (K > 0 && (!top_logp || !top_ids)))
+    return fail(RLK_ERR_NULL_ARG, "h, W, y, logp, entropy, ws (and top_logp, top_ids when K > 0) are required");
+  if (!aligned16(h) || !aligned16(W) || !aligned16(ws) || !aligned4(y) || !aligned4(logp) || !aligned4(lse) ||
+      !aligned4(entropy) || !aligned4(top_logp) || !aligned4(top_ids))
+    return fail(RLK_ERR_BAD_ALIGNMENT, "h, W, ws must be 16-byte aligned, the row arrays 4-byte");
+  const size_t need = top_fwd_layout(T, H, V, K).total;
+  if (ws_bytes < need) return fail(RLK_ERR_WORKSPACE_TOO_SMALL, "need %zu bytes, got %zu", need, ws_bytes);
+  RLK_TRY(check_device());
+  RLK_TRY(run_top_fwd(h, W, y, T, H, V, ignore_index, K, logp, lse, entropy, top_logp, top_ids, ws,
+                      static_cast<hipStream_t>(stream)));
+  return ok();
+}
+
+rlk_status rlk_linear_logp_top_bwd(const void* h, const void* W, const int32_t* y, const float* lse,
+                                   const float* entropy, const float* g, const float* g_entropy, int64_t T, int64_t H,
+                                   int64_t V, int32_t ignore_index, void* grad_h, void* grad_W, int32_t grad_W_dtype,
+                                   void* ws, size_t ws_bytes, void* stream) {
+  RLK_TRY(check_sizes(T, H, V, 0, 0));
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  bool done;
+  RLK_TRY(check_grads(T, H, V, grad_h, grad_W, grad_W_dtype, st, &done));
+  if (done) return ok();
+  if (!h || !W || !y || !lse || !entropy || !ws)
+    return fail(RLK_ERR_NULL_ARG, "h, W, y, lse, entropy and ws are required");
+  if (!aligned16(h) || !aligned16(W) || !aligned16(ws) || !aligned4(y) || !aligned4(lse) || !aligned4(entropy) ||
+      !aligned4(g) || !aligned4(g_entropy))
+    return fail(RLK_ERR_BAD_ALIGNMENT, "h, W, ws must be 16-byte aligned, the row arrays 4-byte");
+  const SoftBwdWs S = soft_bwd_layout(T, H, V, 0);
+  if (ws_bytes < S.total) return fail(RLK_ERR_WORKSPACE_TOO_SMALL, "need %zu bytes, got %zu", S.total, ws_bytes);
+  if (!grad_h && !grad_W) return ok();
+  RLK_TRY(check_device());
+  SoftBwd b{};
+  b.h = h;
+  b.W = W;
+  b.act = y;
+  b.ignore = ignore_index;
+  b.T = T;
+  b.H = H;
+  b.V = V;
+  b.scale = 1.f;
+  b.lse = lse;
+  b.g = g;
+  b.entropy = entropy;
+  b.g_entropy = g_entropy;
+  b.grad_h = grad_h;
+  b.grad_W = grad_W;
+  b.dtype = grad_W_dtype;
+  RLK_TRY(run_soft_bwd(b, S, ws, st));
+  return ok();
+}
+
+rlk_status rlk_linear_distill_fwd(const void* h, const void* W, const int32_t* ids, const float* logits, int64_t T,
+                                  int64_t H, int64_t V, int64_t K, float temperature, float* loss, float* lse,
+                                  float* logp_ids, void* ws, size_t ws_bytes, void* stream) {
+  RLK_TRY(check_sizes(T, H, V, K, 1));
+  float scale;
+  RLK_TRY(check_temperature(temperature, &scale));
+  if (T == 0) return ok();
+  if (!h || !W || !ids || !logits || !loss || !lse || !logp_ids || !ws)
+    return fail(RLK_ERR_NULL_ARG, "h, W, ids, logits, loss, lse, logp_ids and ws are required");
+  if (!aligned16(h) || !aligned16(W) || !aligned16(ws) || !aligned4(ids) || !aligned4(logits) || !aligned4(loss) ||
+      !aligned4(lse) || !aligned4(logp_ids))
+    return fail(RLK_ERR_BAD_ALIGNMENT, "h, W, ws must be 16-byte aligned, the row arrays 4-byte");
+  const size_t need = distill_fwd_layout(T, H, V, K).total;
+  if (ws_bytes < need) return fail(RLK_ERR_WORKSPACE_TOO_SMALL, "need %zu bytes, got %zu", need, ws_bytes);
+  RLK_TRY(check_device());
+  RLK_TRY(run_distill_fwd(h, W, ids, logits, T, H, V, K, scale, loss, lse, logp_ids, ws,
+                          static_cast<hipStream_t>(stream)));
+  return ok();
+}
+
+rlk_status rlk_linear_distill_bwd(const void* h, const void* W, const int32_t* ids, const float* logits,
+                                  const float* lse, const float* logp_ids, const float* g, int64_t T, int64_t H,
+                                  int64_t V, int64_t K, float temperature, void* grad_h, void* grad_W,
+                                  int32_t grad_W_dtype, void* ws, size_t ws_bytes, void* stream) {
+  RLK_TRY(check_sizes(T, H, V, K, 1));
+  SoftBwd b{};
+  RLK_TRY(check_temperature(temperature, &b.scale));
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  bool done;
+  RLK_TRY(check_grads(T, H, V, grad_h, grad_W, grad_W_dtype, st, &done));
+  if (done) return ok();
+  if (!h || !W || !ids || !logits || !lse || !logp_ids || !g || !ws)
+    return fail(RLK_ERR_NULL_ARG, "h, W, ids, logits, lse, logp_ids, g and ws are required");
+  if (!aligned16(h) || !aligned16(W) || !aligned16(ws) || !aligned4(ids) || !aligned4(logits) || !aligned4(lse) ||
+      !aligned4(logp_ids) || !aligned4(g))
+    return fail(RLK_ERR_BAD_ALIGNMENT, "h, W, ws must be 16-byte aligned, the row arrays 4-byte");
+  const SoftBwdWs S = soft_bwd_layout(T, H, V, K);
+  if (ws_bytes < S.total) return fail(RLK_ERR_WORKSPACE_TOO_SMALL, "need %zu bytes, got %zu", S.total, ws_bytes);
+  if (!grad_h && !grad_W) return ok();
+  RLK_TRY(check_device());
+  b.h = h;
+  b.W = W;
+  b.act = at<int32_t>(ws, S.act);
+  b.ignore = -100;
+  b.T = T;
+  b.H = H;
+  b.V = V;
+  b.K = K;
+  b.lse = lse;
+  b.g = g;
+  b.ids = ids;
+  b.logits = logits;
+  b.logp_ids = logp_ids;
+  b.grad_h = grad_h;
+  b.grad_W = grad_W;
+  b.dtype = grad_W_dtype;
+  RLK_TRY(run_soft_bwd(b, S, ws, st));
+  return ok();
+}
+
+}  // extern "C"
