@@ -14,11 +14,6 @@ void launch_compact_rows(hipStream_t st, const int32_t* y, int T, int ignore_ind
                      nullptr, zero2, nullptr);
 }
 
-void launch_zero_rows(hipStream_t st, const int32_t* y, int T, int ignore_index, int H, uint16_t* rows) {
-  hipLaunchKernelGGL(zero_rows, dim3((unsigned)std::min((int64_t)T, kRowBlocks)), dim3(256), 0, st, y, T, ignore_index,
-                     H, rows);
-}
-
 }  // namespace rlk
 
 namespace {

@@ -18,8 +18,6 @@
 //   gemm_tiles         C = A B^T, one MFMA chain per element
 #pragma once
 
-#include <type_traits>
-
 #include "rlk_args.h"
 #include "rlk_gemm.h"
 
@@ -760,9 +758,7 @@ struct WRowsMN {
 // in groups of 4 H tiles: an XCD's ~32 running tiles are then 4 H tiles x 8
 // v tiles, and the h columns it keeps re-reading (4 tiles of all active
 // rows) stay small (measured against groups of 2, 8 and 16: the fastest).
-// kBf16: grad_W holds bf16, each fp32 sum rounded once, instead of fp32.
 constexpr int kGradWGroup = 4;
-template <bool kBf16 = false>
 __device__ __forceinline__ void gradw_tile(GradWArgs a, int id, int n_act, u32x4* lds) {
   int nt, vt;
   grouped_tile(id, a.n_tiles, nt, vt, a.bg.G * a.tps, min(kGradWGroup, a.n_tiles));
@@ -785,8 +781,7 @@ __device__ __forceinline__ void gradw_tile(GradWArgs a, int id, int n_act, u32x4
   // no active rows: grad_W is zero
   if (n_act > 0) gemm256<true, true>(A, B, (n_act + kBK - 1) / kBK, acc, lds);
   const int lane = tid & 63, w = tid >> 6, wm = wave_m(w), wn = wave_n(w);
-  using Out = std::conditional_t<kBf16, uint16_t, float>;
-  Out* out = reinterpret_cast<Out*>(a.grad_W) + (size_t)sbeg * a.H;
+  float* out = a.grad_W + (size_t)sbeg * a.H;
 #pragma unroll
   for (int mi = 0; mi < kMI; ++mi) {
     const int v = v0 + acc_row(wm, mi, lane);
@@ -797,12 +792,8 @@ __device__ __forceinline__ void gradw_tile(GradWArgs a, int id, int n_act, u32x4
       for (int q = 0; q < kQL; ++q) {
         if (n0 + 128 * wn + kBlk * ni + 4 * kLPR * q >= a.H) continue;  // wave-uniform
         const AccBlk& c = acc.c[mi][ni];
-        Out* to = out + (size_t)v * a.H + n0 + acc_col4(wn, ni, q, lane);
-        if constexpr (kBf16)
-          *reinterpret_cast<uint2*>(to) =
-              make_uint2(pack_bf16x2(c[4 * q], c[4 * q + 1]), pack_bf16x2(c[4 * q + 2], c[4 * q + 3]));
-        else
-          *reinterpret_cast<float4*>(to) = make_float4(c[4 * q], c[4 * q + 1], c[4 * q + 2], c[4 * q + 3]);
+        *reinterpret_cast<float4*>(out + (size_t)v * a.H + n0 + acc_col4(wn, ni, q, lane)) =
+            make_float4(c[4 * q], c[4 * q + 1], c[4 * q + 2], c[4 * q + 3]);
       }
   }
 }
@@ -941,7 +932,7 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(RLK_WA
   // nh_blocks is a multiple of 8: block bid - nh_blocks runs on the same XCD
   const int nw = wa.grad_W ? wa.n_tiles * wa.bg.G * wa.tps : 0;
   const int id = xcd_tile(nw, bid - nh_blocks);
-  if (id >= 0) gradw_tile<>(wa, id, n_act, lds);
+  if (id >= 0) gradw_tile(wa, id, n_act, lds);
 }
 
 

@@ -16,8 +16,4 @@ __attribute__((visibility("hidden"))) void launch_compact_rows(hipStream_t st, c
                                                               int32_t* n_act, float* zero0, float* zero1,
                                                               float* zero2);
 
-// zero_rows: the rows of a bf16 [T, H] array with y[t] == ignore_index.
-__attribute__((visibility("hidden"))) void launch_zero_rows(hipStream_t st, const int32_t* y, int T, int ignore_index,
-                                                           int H, uint16_t* rows);
-
 }  // namespace rlk

@@ -16,7 +16,8 @@
 //   gather_rows_grad   compacted hidden rows and the rows' coefficients
 //   soft_dz_tiles      recomputed logits -> dz, bf16
 //   distill_scatter    dz at the teacher's tokens
-//   gradw_bf16_tiles   grad_W as bf16
+//   part_grad_tiles    grad_h in parts of the vocabulary, grad_W
+//   grad_h_sum         the parts together (after the last group)
 #pragma once
 
 #include "rlk_kernels.h"
@@ -442,17 +443,42 @@ __global__ __launch_bounds__(kBucketThreads) void bucket_entries(const int32_t* 
   const int C = kNSplit * tps;
   for (int c = tid; c < C; c += kBucketThreads) cnt[c] = 0;
   __syncthreads();
-  const auto each = [&](auto&& f) {
-    for (int e = tid; e < n * K; e += kBucketThreads) {
-      const int r = e / K, k = e - r * K;
+  // thread tid takes slot tid % kp of rows tid / kp, + kBucketThreads / kp,
+  // ... (kp: the power of two at or above K), all loads in flight at once
+  const int kp = 1 << (32 - __builtin_clz(max(K - 1, 1))), shift = __builtin_ctz(kp);
+  const int k = tid & (kp - 1), r0 = tid >> shift, step = kBucketThreads >> shift;
+  constexpr int kPer = kBM * kMaxK / kBucketThreads;  // rows of a thread
+  int id[kPer], bin[kPer];
+  float lg[kPer];
+#pragma unroll
+  for (int e = 0; e < kPer; ++e) {
+    const int r = r0 + e * step;
+    id[e] = -1;
+    lg[e] = 0.f;
+    if (r < n && k < K) {
       const size_t at = (size_t)idx[i0 + r] * K + k;
-      const int id = ids[at];
-      if (id >= gm.V || !slot_kept(id, logits[at])) continue;
-      const int s = id / gm.S, c = id - s * gm.S;
-      f(s * tps + (c >> 8), entry_of(c & 255, r, k));
+      id[e] = ids[at];
+      lg[e] = logits[at];
     }
-  };
-  each([&](int c, uint32_t) { atomicAdd(&cnt[c], 1); });
+  }
+  const uint32_t rcp = (uint32_t)(((uint64_t(1) << 32) - 1) / (uint32_t)gm.S);
+  uint32_t ent_e[kPer];
+#pragma unroll
+  for (int e = 0; e < kPer; ++e) {
+    bin[e] = -1;
+    ent_e[e] = 0;
+    if (id[e] < gm.V && slot_kept(id[e], lg[e])) {
+      // id / S: the truncated reciprocal's quotient is short by at most one
+      int q = (int)__umulhi((uint32_t)id[e], rcp), c = id[e] - q * gm.S;
+      if (c >= gm.S) {
+        c -= gm.S;
+        ++q;
+      }
+      bin[e] = q * tps + (c >> 8);
+      ent_e[e] = entry_of(c & 255, r0 + e * step, k);
+      atomicAdd(&cnt[bin[e]], 1);
+    }
+  }
   __syncthreads();
   // exclusive scan: thread tid takes `per` consecutive tiles
   const int per = (C + kBucketThreads - 1) / kBucketThreads;
@@ -479,53 +505,92 @@ __global__ __launch_bounds__(kBucketThreads) void bucket_entries(const int32_t* 
   if (tid == kBucketThreads - 1) o[C] = pos;
   __syncthreads();
   uint32_t* e0 = ent + (size_t)rt * kBM * K;
-  each([&](int c, uint32_t x) { e0[atomicAdd(&cnt[c], 1)] = x; });
+#pragma unroll
+  for (int e = 0; e < kPer; ++e)
+    if (bin[e] >= 0) e0[atomicAdd(&cnt[bin[e]], 1)] = ent_e[e];
 }
 
 // ---------------------------------------------------------------------------
-// Folds.  Lane s < 32 folds split s of active row i (chunks left to right);
-// the splits then meet in a pairwise tree over the lanes (lane 2w j takes
-// lane 2w j + w): the order, and for m and s the bits, of merge_splits.
-// The result is valid in lane 0.
+// Row kernels after the logits: one wave (a block) per row.  With one row
+// they are latency alone, and most of that is instruction fetch: unrolled
+// forms of these loops, which run through their code once, took 54 us where
+// the rolled ones below take 17 (20 alternatives, V = 151936).  So loops stay
+// rolled, what is loaded ahead goes through LDS, and only the loads are
+// unrolled.  A chunk's records of neighbouring rows share cache lines, so a
+// die takes consecutive rows (xcd_tile).
 // ---------------------------------------------------------------------------
+// The lanes of a wave see one another's LDS writes.
+__device__ __forceinline__ void wave_lds_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
+// Chunks of split `s` that hold columns.
+__device__ __forceinline__ int chunks_of(const SplitGeom& gm, int s) {
+  const int cols = min(gm.S, gm.V - s * gm.S);
+  return cols > 0 ? (cols + kChunk - 1) / kChunk : 0;
+}
+
+// Fold of active row i.  Lane s < 32 folds split s (chunks left to right);
+// the splits then meet in a pairwise tree over the lanes (lane 2w j takes
+// lane 2w j + w): the order, and for m and s the bits, of merge_splits.  All
+// lanes load, kFoldAhead chunks of every split at a time, the next ones while
+// these are folded.  The result is valid in lane 0.  buf: kFoldFloats floats.
+constexpr int kFoldAhead = 16;
+constexpr int kFoldFloats = 3 * kFoldAhead * kNSplit;
 template <bool kMoment>
 __device__ __forceinline__ MSU fold_row(const float2* rec, const float* rec_u, size_t stride, int i,
-                                        const SplitGeom& gm) {
-  const int lane = threadIdx.x & 63;
-  MSU r = msu_identity();
-  if (lane < kNSplit) {
-    const int c0 = lane * gm.S, send = min(c0 + gm.S, gm.V);
-    const int nj = send > c0 ? (send - c0 + kChunk - 1) / kChunk : 0;
-    const size_t base = (size_t)lane * gm.cps * stride + i;
-    constexpr int kBatch = 8;
-    for (int j0 = 0; j0 < nj; j0 += kBatch) {
-      float2 ms[kBatch];
-      float u[kBatch];
+                                        const SplitGeom& gm, float* buf) {
+  const int lane = threadIdx.x & 63, s = lane & (kNSplit - 1), half = lane / kNSplit;
+  constexpr int kEach = kFoldAhead / 2;
+  const int nj = chunks_of(gm, s);
+  const size_t base = (size_t)s * gm.cps * stride + i;
+  float2* b_ms = reinterpret_cast<float2*>(buf);
+  float* b_u = buf + 2 * kFoldAhead * kNSplit;
+  float2 ms[kEach];
+  float u[kEach];
+  const auto load = [&](int j0) {
 #pragma unroll
-      for (int b = 0; b < kBatch; ++b)
-        if (j0 + b < nj) {
-          ms[b] = rec[base + (size_t)(j0 + b) * stride];
-          u[b] = kMoment ? rec_u[base + (size_t)(j0 + b) * stride] : 0.f;
-        }
-#pragma unroll
-      for (int b = 0; b < kBatch; ++b)
-        if (j0 + b < nj) {
-          if constexpr (kMoment) {
-            r = msu_combine(r, MSU{ms[b].x, ms[b].y, u[b]});
-          } else {
-            const MS t = ms_combine(MS{r.m, r.s}, MS{ms[b].x, ms[b].y});
-            r.m = t.m;
-            r.s = t.s;
-          }
-        }
+    for (int b = 0; b < kEach; ++b) {
+      const int j = j0 + half * kEach + b;
+      if (j < nj) {
+        ms[b] = rec[base + (size_t)j * stride];
+        if (kMoment) u[b] = rec_u[base + (size_t)j * stride];
+      }
     }
-  }
+  };
+  MSU r = msu_identity();
+  load(0);
+#pragma unroll 1
+  for (int j0 = 0; j0 < gm.cps; j0 += kFoldAhead) {
 #pragma unroll
+    for (int b = 0; b < kEach; ++b) {
+      b_ms[(half * kEach + b) * kNSplit + s] = ms[b];
+      if (kMoment) b_u[(half * kEach + b) * kNSplit + s] = u[b];
+    }
+    wave_lds_sync();
+    load(j0 + kFoldAhead);
+    const int n = half ? 0 : min(kFoldAhead, nj - j0);
+#pragma unroll 1
+    for (int j = 0; j < n; ++j) {
+      const float2 x = b_ms[j * kNSplit + s];
+      if constexpr (kMoment) {
+        r = msu_combine(r, MSU{x.x, x.y, b_u[j * kNSplit + s]});
+      } else {
+        const MS t = ms_combine(MS{r.m, r.s}, MS{x.x, x.y});
+        r.m = t.m;
+        r.s = t.s;
+      }
+    }
+    wave_lds_sync();
+  }
+#pragma unroll 1
   for (int w = 1; w < kNSplit; w <<= 1) {
     MSU b;
     b.m = __shfl_down(r.m, w);
     b.s = __shfl_down(r.s, w);
-    b.u = __shfl_down(r.u, w);
+    b.u = kMoment ? __shfl_down(r.u, w) : 0.f;
     if constexpr (kMoment) {
       r = msu_combine(r, b);
     } else {
@@ -542,20 +607,26 @@ __device__ __forceinline__ MSU fold_row(const float2* rec, const float* rec_u, s
 //
 // A logit and its id make one 64-bit key (the logit's bits in an order that
 // integers keep, -0 as +0, then the id's complement): all keys of a row
-// differ, and a larger key is a better alternative.  Every one of the K best
-// lies in one of the K chunks with the largest (max, then lowest number):
-// of a chunk that is not among them, each of those K holds a better logit.
-// So: tau = the K-th largest chunk max (bit by bit, counting the chunks at or
-// above), the chunks above tau and then the first ones at tau, K in all; of
-// their logits those at or above tau go to a list; the list's K best by
-// counting.  When the list fills up it is cut to its K best, and tau to the
-// last of them (ties in number: the cut keeps the lowest ids).
-// Vocabularies of more than kSelChunks chunks take runs of R chunks as one.
+// differ, and a larger key is a better alternative.  The chunks are dealt
+// into 256 groups; tau = the K-th largest of the groups' maxima (bit by bit,
+// counting the groups at or above).  K logits at least are >= tau, so the K
+// best are, and they lie in the chunks whose max is >= tau: about
+// -256 log(1 - K / 256) of them.  Their logits at or above tau go to a list,
+// its K best come out by counting.  When the list fills up it is cut to its K
+// best, and what is accepted to what beats the last of them.
+//
+// Lanes l and l + 32 hold the two halves of split l's chunks, at most
+// kSelPer each; splits of more than 2 kSelPer chunks (vocabularies past
+// 262144) take runs of R chunks as one.
 // ---------------------------------------------------------------------------
-constexpr int kSelWaves = 4;      // rows per block, one wave each
-constexpr int kSelChunks = 2048;  // chunk maxima of a row in LDS
-constexpr int kSelList = 512;     // keys of a row in LDS
+constexpr int kSelPer = 32;                // runs per lane
+constexpr int kSelGroups = 4;              // groups per lane
+constexpr int kSelRuns = 64 * kSelPer;
+constexpr int kSelList = 512;              // keys of a row in LDS
+constexpr int kSelAhead = 16;              // chunks whose logits are loaded together
 static_assert(kSelList >= kMaxK + 64, "room for a step after a cut");
+static_assert(64 * kSelGroups >= kMaxK, "K groups");
+static_assert(kSelAhead * kChunk <= kSelRuns && kFoldFloats <= kSelRuns, "one LDS array serves all three");
 
 __device__ __forceinline__ uint32_t ordered_bits(float x) {
   const uint32_t b = __float_as_uint(x + 0.f);
@@ -563,13 +634,6 @@ __device__ __forceinline__ uint32_t ordered_bits(float x) {
 }
 __device__ __forceinline__ float from_ordered(uint32_t o) {
   return __uint_as_float(o ^ ((o >> 31) ? 0x80000000u : 0xFFFFFFFFu));
-}
-
-// The lanes of a wave see one another's LDS writes.
-__device__ __forceinline__ void wave_lds_sync() {
-  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-  __builtin_amdgcn_wave_barrier();
-  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
 // list[0..n) -> its min(n, K) best in descending order; returns their number.
@@ -583,11 +647,14 @@ __device__ __forceinline__ int keep_best(uint64_t* list, int n, int K) {
     x[e] = 64 * e + lane < n ? list[64 * e + lane] : 0;
     rank[e] = 0;
   }
+#pragma unroll 1
   for (int j = 0; j < n; ++j) {
     const uint64_t b = list[j];
+    rank[0] += b > x[0];
+    if (n > 64) {
 #pragma unroll
-    for (int e = 0; e < kPer; ++e)
-      if (64 * e < n) rank[e] += b > x[e];
+      for (int e = 1; e < kPer; ++e) rank[e] += b > x[e];
+    }
   }
   wave_lds_sync();
 #pragma unroll
@@ -620,56 +687,61 @@ struct TopMergeArgs {
   int32_t* top_ids;
 };
 
-__global__ __launch_bounds__(64 * kSelWaves) void top_merge(TopMergeArgs a) {
-  __shared__ uint32_t maxima[kSelWaves][kSelChunks];
-  __shared__ uint64_t lists[kSelWaves][kSelList];
-  __shared__ int32_t picks[kSelWaves][kMaxK];
-  const int w = threadIdx.x >> 6, lane = threadIdx.x & 63;
-  const int i = blockIdx.x * kSelWaves + w;
-  if (i >= *a.n_act) return;  // (a wave's rows are its own: no block barrier below)
-  uint64_t* list = lists[w];
+__global__ __launch_bounds__(64) void top_merge(TopMergeArgs a) {
+  __shared__ uint32_t pool[kSelRuns];  // run maxima; then logits; then the fold's records
+  __shared__ uint64_t list[kSelList];
+  __shared__ uint16_t picks[kSelRuns];
+  const int lane = threadIdx.x, i = xcd_tile(*a.n_act, blockIdx.x);
+  if (i < 0) return;
   int n = 0;
   if (a.K > 0) {
-    uint32_t* mx = maxima[w];
-    // maxima of the group's chunks (0: no columns)
-    const int nch = a.G * a.gm.cps, nq = (nch + a.R - 1) / a.R;
-    int valid = 0;
-    for (int q0 = 0; q0 < nq; q0 += 64) {
-      const int q = q0 + lane;
-      uint32_t m = 0;
-      for (int c = q * a.R; q < nq && c < min((q + 1) * a.R, nch); ++c) {
-        const int sl = c / a.gm.cps, j = c - sl * a.gm.cps;
-        const int sbeg = (a.gm.s0 + sl) * a.gm.S;
-        if (sbeg + j * kChunk >= min(sbeg + a.gm.S, a.gm.V)) continue;
-        m = max(m, ordered_bits(a.rec[((size_t)a.gm.s0 * a.gm.cps + c) * a.rec_stride + i].x));
+    // this lane's runs of R chunks: run e is chunks j0 + e R .. of split s0 + sl
+    const int sl = lane & (kNSplit - 1), hs = ((a.gm.cps + a.R - 1) / a.R + 1) / 2;
+    const int nj = sl < a.G ? chunks_of(a.gm, a.gm.s0 + sl) : 0;
+    const int j0 = lane / kNSplit * hs * a.R;
+    const float2* rec = a.rec + (size_t)(a.gm.s0 + sl) * a.gm.cps * a.rec_stride + i;
+    uint32_t top[kSelGroups] = {0, 0, 0, 0};  // groups' maxima (0: no columns)
+    constexpr int kLoads = 16;
+#pragma unroll 1
+    for (int e0 = 0; e0 < hs; e0 += kLoads) {
+      float m[kLoads];
+#pragma unroll
+      for (int e = 0; e < kLoads; ++e) {
+        const int j = j0 + (e0 + e) * a.R;
+        if (e0 + e < hs && j < nj) m[e] = rec[(size_t)j * a.rec_stride].x;
       }
-      if (q < nq) mx[q] = m;
-      valid += __builtin_popcountll(__builtin_amdgcn_ballot_w64(m != 0));
+#pragma unroll
+      for (int e = 0; e < kLoads; ++e) {
+        const int j = j0 + (e0 + e) * a.R;
+        if (e0 + e >= hs) continue;
+        uint32_t x = j < nj ? ordered_bits(m[e]) : 0;
+        for (int r = 1; r < a.R; ++r)
+          if (j + r < nj) x = max(x, ordered_bits(rec[(size_t)(j + r) * a.rec_stride].x));
+        pool[(e0 + e) * 64 + lane] = x;
+        top[e % kSelGroups] = max(top[e % kSelGroups], x);
+      }
     }
-    wave_lds_sync();
-    // the largest tau that K chunks reach
+    // the largest tau that K groups reach (1, any logit, if fewer hold columns)
     uint32_t tau = 0;
-    if (valid > a.K) {
-      for (int b = 31; b >= 0; --b) {
-        const uint32_t t = tau | (1u << b);
-        int c = 0;
-        for (int q0 = 0; q0 < nq; q0 += 64)
-          c += __builtin_popcountll(__builtin_amdgcn_ballot_w64(q0 + lane < nq && mx[q0 + lane] >= t));
-        if (c >= a.K) tau = t;
-        if (c == a.K) break;
-      }
+#pragma unroll 1
+    for (int b = 31; b >= 0; --b) {
+      const uint32_t t = tau | (1u << b);
+      int c = 0;
+#pragma unroll
+      for (int e = 0; e < kSelGroups; ++e) c += __builtin_popcountll(__builtin_amdgcn_ballot_w64(top[e] >= t));
+      if (c >= a.K) tau = t;
+      if (c == a.K) break;
     }
-    // the chunks above tau, then the first ones at tau
+    tau = max(tau, 1u);
+    // the runs that reach it
     int np = 0;
-    for (int at = 0; at < 2; ++at)
-      for (int q0 = 0; q0 < nq && np < a.K; q0 += 64) {
-        const uint32_t m = q0 + lane < nq ? mx[q0 + lane] : 0;
-        const bool take = m != 0 && (at ? m == tau : m > tau);
-        const uint64_t mask = __builtin_amdgcn_ballot_w64(take);
-        const int p = np + __builtin_popcountll(mask & ((uint64_t(1) << lane) - 1));
-        if (take && p < a.K) picks[w][p] = q0 + lane;
-        np = min(a.K, np + __builtin_popcountll(mask));
-      }
+#pragma unroll 1
+    for (int e = 0; e < hs; ++e) {
+      const bool take = pool[e * 64 + lane] >= tau;
+      const uint64_t mask = __builtin_amdgcn_ballot_w64(take);
+      if (take) picks[np + __builtin_popcountll(mask & ((uint64_t(1) << lane) - 1))] = (uint16_t)(e * 64 + lane);
+      np += __builtin_popcountll(mask);
+    }
     uint64_t floor = (uint64_t)tau << 32;
     if (!a.first) {
       const uint64_t* b = a.best + (size_t)i * a.K;
@@ -679,35 +751,43 @@ __global__ __launch_bounds__(64 * kSelWaves) void top_merge(TopMergeArgs a) {
       if (n == a.K) floor = max(floor, b[a.K - 1]);
     }
     wave_lds_sync();
-    // their logits, two columns a lane, kAhead chunks in flight
-    constexpr int kAhead = 8;
+    // their logits, two columns a lane
     const float* zr = a.z + (size_t)i * a.ldz;
+    float2* stage = reinterpret_cast<float2*>(pool);
     const int np_c = np * a.R;
-    for (int p0 = 0; p0 < np_c; p0 += kAhead) {
-      float2 v[kAhead];
-      int col[kAhead], end[kAhead];  // first column of the chunk and end of its split
+    // chunk p of the picked runs: its split (of the group) and number there
+    const auto chunk_at = [&](int p, int& ps, int& j) {
+      const int q = __builtin_amdgcn_readfirstlane(picks[a.R == 1 ? p : p / a.R]);
+      ps = q & (kNSplit - 1);
+      j = ((q & 63) / kNSplit * hs + (q >> 6)) * a.R + (a.R == 1 ? 0 : p % a.R);
+    };
+#pragma unroll 1
+    for (int p0 = 0; p0 < np_c; p0 += kSelAhead) {
+      float2 v[kSelAhead];
 #pragma unroll
-      for (int e = 0; e < kAhead; ++e) {
-        const int p = p0 + e;
-        const int c = p < np_c ? picks[w][p / a.R] * a.R + p % a.R : nch;
-        col[e] = end[e] = 0;
-        if (c < nch) {
-          const int sl = c / a.gm.cps, j = c - sl * a.gm.cps;
-          const int sbeg = (a.gm.s0 + sl) * a.gm.S;
-          col[e] = sbeg + j * kChunk;
-          end[e] = min(sbeg + a.gm.S, a.gm.V);
-          if (col[e] < end[e]) v[e] = *reinterpret_cast<const float2*>(zr + (size_t)c * kChunk + 2 * lane);
-        }
+      for (int e = 0; e < kSelAhead; ++e) {
+        if (p0 + e >= np_c) continue;
+        int ps, j;
+        chunk_at(p0 + e, ps, j);
+        if (j < a.gm.cps)
+          v[e] = *reinterpret_cast<const float2*>(zr + (size_t)(ps * a.gm.cps + j) * kChunk + 2 * lane);
       }
 #pragma unroll
-      for (int e = 0; e < kAhead; ++e) {
-        if (col[e] >= end[e]) continue;
-#pragma unroll
+      for (int e = 0; e < kSelAhead; ++e) stage[64 * e + lane] = v[e];
+      wave_lds_sync();
+#pragma unroll 1
+      for (int e = 0; e < min(kSelAhead, np_c - p0); ++e) {
+        int ps, j;
+        chunk_at(p0 + e, ps, j);
+        const int sbeg = (a.gm.s0 + ps) * a.gm.S;
+        const int id0 = sbeg + j * kChunk + 2 * lane, end = min(sbeg + a.gm.S, a.gm.V);
+        const float2 x2 = stage[64 * e + lane];
+#pragma unroll 1
         for (int h = 0; h < 2; ++h) {
-          const int id = col[e] + 2 * lane + h;
-          const float x = h ? v[e].y : v[e].x;
+          const int id = id0 + h;
+          const float x = h ? x2.y : x2.x;
           const uint64_t key = (uint64_t)ordered_bits(x) << 32 | (0xFFFFFFFFu - (uint32_t)id);
-          const bool take = id < end[e] && x == x && key >= floor;
+          const bool take = id < end && x == x && key >= floor;
           const uint64_t mask = __builtin_amdgcn_ballot_w64(take);
           if (!mask) continue;
           if (n + __builtin_popcountll(mask) > kSelList) {
@@ -719,14 +799,14 @@ __global__ __launch_bounds__(64 * kSelWaves) void top_merge(TopMergeArgs a) {
           n += __builtin_popcountll(mask);
         }
       }
+      wave_lds_sync();
     }
-    wave_lds_sync();
     n = keep_best(list, n, a.K);
     if (!a.last)
       for (int k = lane; k < a.K; k += 64) a.best[(size_t)i * a.K + k] = k < n ? list[k] : 0;
   }
   if (!a.last) return;
-  const MSU tot = fold_row<true>(a.rec, a.rec_u, a.rec_stride, i, a.gm);
+  const MSU tot = fold_row<true>(a.rec, a.rec_u, a.rec_stride, i, a.gm, reinterpret_cast<float*>(pool));
   const float m = __shfl(tot.m, 0), L = rlk_log(__shfl(tot.s, 0));
   const int t = a.idx[i];
   if (lane == 0) {
@@ -763,10 +843,11 @@ struct DistillMergeArgs {
   float* logp_ids;
 };
 
-__global__ __launch_bounds__(256) void distill_merge(DistillMergeArgs a) {
-  const int lane = threadIdx.x & 63, i = blockIdx.x * 4 + (threadIdx.x >> 6);
-  if (i >= *a.n_act) return;
-  const MSU tot = fold_row<false>(a.rec, nullptr, a.rec_stride, i, a.gm);
+__global__ __launch_bounds__(64) void distill_merge(DistillMergeArgs a) {
+  __shared__ float buf[kFoldFloats];
+  const int lane = threadIdx.x, i = xcd_tile(*a.n_act, blockIdx.x);
+  if (i < 0) return;
+  const MSU tot = fold_row<false>(a.rec, nullptr, a.rec_stride, i, a.gm, buf);
   const float m = __shfl(tot.m, 0), L = rlk_log(__shfl(tot.s, 0));
   const int t = a.idx[i];
   const TeacherRow r = teacher_row(a.ids + (size_t)t * a.K, a.logits + (size_t)t * a.K, a.K, a.scale);
@@ -962,14 +1043,203 @@ __global__ __launch_bounds__(kMaxK) void distill_scatter(ScatterArgs a) {
   }
 }
 
-// grad_W of the group as bf16, each fp32 sum rounded once (grad_tiles,
-// rlk_kernels.h, has it in fp32).
-__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(RLK_WAVES / 4, RLK_WAVES / 4))) void gradw_bf16_tiles(
-    GradWArgs a) {
+// ---------------------------------------------------------------------------
+// Gradients of a group of splits.
+//
+// grad_h: the sum over the vocabulary is cut into kParts parts of
+// kPartSplits splits each, whatever the batch; a part's sum is one fp32 MFMA
+// chain per element, vocabulary ascending (it continues across groups through
+// its place in `part`), and grad_h_sum adds the parts in order.  One chain
+// over the whole vocabulary leaves most compute units without a grad_h tile
+// where rows are few: at 257 rows, H = 4096, V = 151936 its tiles take 1.97
+// ms.  (linear_logp_bwd keeps the one chain: its bits are its contract.)
+// Four parts: both gradients of that batch in 0.98 ms, of 4096 rows (3482
+// active) in 6.63 ms with grad_h_sum; two parts 1.68 and 6.49, eight 0.99 and
+// 6.73 (the parts' sums pass through HBM).
+// ---------------------------------------------------------------------------
+constexpr int kPartSplits = 8, kParts = kNSplit / kPartSplits;
+
+struct PartGradHArgs {
+  const uint16_t* dZ;
+  const uint16_t* W;
+  int H;
+  SplitGeom gm;
+  BwdGeom bg;
+  int n_tiles;         // 256-column tiles of H
+  int part0, parts;    // parts of the group: part0 .. part0 + parts - 1
+  float* part;         // [kParts][T][H], rows in active order; NULL: not wanted
+  size_t part_stride;  // T * H
+};
+
+// kCont: the group starts inside its (one) part.
+template <bool kCont>
+__device__ __forceinline__ void gradh_part_tile(const PartGradHArgs& a, int id, int rtiles, int n_act, u32x4* lds) {
+  const int per = rtiles * a.n_tiles;
+  const int q = id / per;  // part within the group
+  int rt, nt;
+  grouped_tile(id - q * per, rtiles, rt, nt, a.n_tiles, row_group(rtiles));
+  const int i0 = rt * kBM, n0 = nt * kBN;
+  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, wm = wave_m(w), wn = wave_n(w);
+  float* part = a.part + (size_t)(a.part0 + q) * a.part_stride;
+  Acc acc;
+  acc_zero(acc);
+  if (kCont) {  // (clamped addresses outside the problem; never stored)
+#pragma unroll
+    for (int mi = 0; mi < kMI; ++mi) {
+      const float* src = part + (size_t)min(i0 + acc_row(wm, mi, lane), n_act - 1) * a.H;
+#pragma unroll
+      for (int ni = 0; ni < kNI; ++ni)
+#pragma unroll
+        for (int p = 0; p < kQL; ++p) {
+          const float4 v = *reinterpret_cast<const float4*>(src + min(n0 + acc_col4(wn, ni, p, lane), a.H - 4));
+          acc.c[mi][ni][4 * p] = v.x;
+          acc.c[mi][ni][4 * p + 1] = v.y;
+          acc.c[mi][ni][4 * p + 2] = v.z;
+          acc.c[mi][ni][4 * p + 3] = v.w;
+        }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  }
+  // the accumulators enter the engine in accumulator registers (see gradh_tile)
+#pragma unroll
+  for (int mi = 0; mi < kMI; ++mi)
+#pragma unroll
+    for (int ni = 0; ni < kNI; ++ni) asm volatile("" : "+a"(acc.c[mi][ni]));
+  const int s0 = q * kPartSplits, splits = min(kPartSplits, a.bg.G - s0);  // of the group
+  const RowsK A = rows_k(a.dZ + (size_t)i0 * a.bg.ldz + (size_t)s0 * a.bg.S_pad, kBM - 1, a.bg.ldz);
+  WRowsMN B;
+  B.base = reinterpret_cast<const char*>(a.W + n0);
+  B.H = a.H;
+  B.S = a.gm.S;
+  B.kbps = a.bg.S_pad / kBK;
+  B.rcp = ((uint64_t(1) << 32) + (uint64_t)B.kbps - 1) / (uint64_t)B.kbps;
+  B.c_lo = a.bg.c_lo + s0;
+  B.V = a.gm.V;
+#pragma unroll
+  for (int i = 0; i < kDma; ++i) {
+    B.col2[i] = 2 * (min(n0 + dma_mn_piece(dma_mn_krow(i)) * 8, a.H - 8) - n0);
+    B.krow[i] = (uint32_t)dma_mn_krow(i);
+  }
+  gemm256<false, true>(A, B, splits * B.kbps, acc, lds);
+#pragma unroll
+  for (int mi = 0; mi < kMI; ++mi) {
+    const int i = i0 + acc_row(wm, mi, lane);
+    if (i >= n_act) continue;
+#pragma unroll
+    for (int ni = 0; ni < kNI; ++ni)
+#pragma unroll
+      for (int p = 0; p < kQL; ++p) {
+        if (n0 + 128 * wn + kBlk * ni + 4 * kLPR * p >= a.H) continue;  // wave-uniform
+        const AccBlk& c = acc.c[mi][ni];
+        *reinterpret_cast<float4*>(part + (size_t)i * a.H + n0 + acc_col4(wn, ni, p, lane)) =
+            make_float4(c[4 * p], c[4 * p + 1], c[4 * p + 2], c[4 * p + 3]);
+      }
+  }
+}
+
+// gradw_tile (rlk_kernels.h) with a bf16 grad_W, each fp32 sum rounded once.
+// The tile goes through LDS as dz does: straight from the accumulators a
+// store would write 32-byte pieces of 16 rows.
+__device__ __forceinline__ void gradw_bf16_tile(const GradWArgs& a, int id, int n_act, u32x4* lds) {
+  int nt, vt;
+  grouped_tile(id, a.n_tiles, nt, vt, a.bg.G * a.tps, min(kGradWGroup, a.n_tiles));
+  const int sc = vt / a.tps, j = vt - sc * a.tps;
+  const int sbeg = (a.bg.c_lo + sc) * a.gm.S;
+  const int valid_s = max(0, min(a.gm.S, a.gm.V - sbeg));
+  const int v0 = j * kBM;  // within the split
+  if (v0 >= valid_s) return;
+  const int n0 = nt * kBN;
+  const int tid = threadIdx.x;
+  const ColsMN A = cols_mn(a.dZ + (size_t)sc * a.bg.S_pad, v0, a.bg.S_pad, a.bg.ldz);
+  const ColsMN B = cols_mn(a.hA, n0, a.H, a.H);
+  Acc acc;
+  acc_zero(acc);
+#pragma unroll
+  for (int mi = 0; mi < kMI; ++mi)
+#pragma unroll
+    for (int ni = 0; ni < kNI; ++ni) asm volatile("" : "+a"(acc.c[mi][ni]));
+  if (n_act > 0) gemm256<true, true>(A, B, (n_act + kBK - 1) / kBK, acc, lds);
+  int le = tid & 63;  // an opaque copy, see fwd_tiles
+  asm volatile("" : "+v"(le));
+  const int w = __builtin_amdgcn_readfirstlane(tid >> 6), wm = wave_m(w), wn = wave_n(w);
+  char* stage = reinterpret_cast<char*>(lds);  // as in dz_tiles
+#pragma unroll
+  for (int mi = 0; mi < kMI; ++mi) {
+    const int r = acc_row(wm, mi, le);
+#pragma unroll
+    for (int ni = 0; ni < kNI; ++ni)
+#pragma unroll
+      for (int q = 0; q < kQL; ++q) {
+        const AccBlk& c = acc.c[mi][ni];
+        const int col = acc_col4(wn, ni, q, le);
+        *reinterpret_cast<uint2*>(stage + 512u * r + 16u * ((col >> 3) ^ (r & 31)) + 8u * ((col >> 2) & 1)) =
+            make_uint2(pack_bf16x2(c[4 * q], c[4 * q + 1]), pack_bf16x2(c[4 * q + 2], c[4 * q + 3]));
+      }
+  }
+  __syncthreads();
+  constexpr int kRowsW = kBM / kWaves;
+  const int u = le & 31, col = n0 + 8 * u;
+  if (col < a.H) {
+    uint16_t* out = reinterpret_cast<uint16_t*>(a.grad_W) + (size_t)sbeg * a.H + col;
+#pragma unroll
+    for (int it = 0; it < kRowsW / 2; ++it) {
+      const int r = kRowsW * w + 2 * it + (le >> 5);
+      if (v0 + r < valid_s)
+        *reinterpret_cast<u32x4*>(out + (size_t)(v0 + r) * a.H) =
+            *reinterpret_cast<const u32x4*>(stage + 512u * r + 16u * (u ^ (r & 31)));
+    }
+  }
+}
+
+// The group's grad_h tiles (long chains, first) and grad_W tiles in one
+// launch, as in grad_tiles.
+template <bool kBf16, bool kCont>
+__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(RLK_WAVES / 4, RLK_WAVES / 4))) void part_grad_tiles(
+    PartGradHArgs ha, GradWArgs wa) {
   __shared__ u32x4 lds[kLdsU4];
-  const int n_act = __builtin_amdgcn_readfirstlane(*a.n_act);
-  const int id = xcd_tile(a.n_tiles * a.bg.G * a.tps, blockIdx.x);
-  if (id >= 0) gradw_tile<true>(a, id, n_act, lds);
+  const int n_act = __builtin_amdgcn_readfirstlane(*wa.n_act);
+  const int rtiles = (n_act + kBM - 1) / kBM;
+  const int nh = ha.part ? rtiles * ha.n_tiles * ha.parts : 0;
+  const int nh_blocks = 8 * ((nh + 7) >> 3);
+  const int bid = blockIdx.x;
+  if (bid < nh_blocks) {
+    const int id = xcd_tile(nh, bid);
+    if (id >= 0) gradh_part_tile<kCont>(ha, id, rtiles, n_act, lds);
+    return;
+  }
+  const int nw = wa.grad_W ? wa.n_tiles * wa.bg.G * wa.tps : 0;
+  const int id = xcd_tile(nw, bid - nh_blocks);
+  if (id < 0) return;
+  if constexpr (kBf16) gradw_bf16_tile(wa, id, n_act, lds);
+  else gradw_tile(wa, id, n_act, lds);
+}
+
+// grad_h[idx[i]] = the parts' sum, left to right, rounded to bf16 once; zero
+// rows for inactive rows.  Block b takes active row b and row b of the batch.
+__global__ __launch_bounds__(256) void grad_h_sum(const float* __restrict__ part, size_t part_stride, int parts,
+                                                  const int32_t* __restrict__ idx,
+                                                  const int32_t* __restrict__ n_act_p, const int32_t* __restrict__ act,
+                                                  int ignore_index, int T, int H, uint16_t* __restrict__ grad_h) {
+  const int n_act = *n_act_p;
+  for (int i = blockIdx.x; i < T; i += gridDim.x) {
+    if (act[i] == ignore_index)
+      for (int c = 4 * threadIdx.x; c < H; c += 1024)
+        *reinterpret_cast<uint2*>(grad_h + (size_t)i * H + c) = make_uint2(0u, 0u);
+    if (i >= n_act) continue;
+    uint16_t* out = grad_h + (size_t)idx[i] * H;
+    for (int c = 4 * threadIdx.x; c < H; c += 1024) {
+      const float* src = part + (size_t)i * H + c;
+      float4 v[kParts];
+#pragma unroll
+      for (int q = 0; q < kParts; ++q)
+        if (q < parts) v[q] = *reinterpret_cast<const float4*>(src + q * part_stride);
+      float4 s = v[0];
+#pragma unroll
+      for (int q = 1; q < kParts; ++q)
+        if (q < parts) s = make_float4(s.x + v[q].x, s.y + v[q].y, s.z + v[q].z, s.w + v[q].w);
+      *reinterpret_cast<uint2*>(out + c) = make_uint2(pack_bf16x2(s.x, s.y), pack_bf16x2(s.z, s.w));
+    }
+  }
 }
 
 }  // namespace vocab

@@ -98,19 +98,27 @@ inline DistillFwdWs distill_fwd_layout(int64_t T, int64_t H, int64_t V, int64_t 
   return w;
 }
 
-// Both backwards: bwd_layout's pieces, the rows' g, and (distill, K > 0) the
-// teacher's rows.
+// Both backwards: G splits of dz at a time, grad_h's parts, and (distill,
+// K > 0) the teacher's rows.
 struct SoftBwdWs {
-  BwdWs core;
-  size_t rowg, act, q, total;
+  size_t idx, n_act, rowinfo, rowg, hA, dZ, part, act, q, total;
+  int64_t T_pad, S_pad, G;
 };
 
 inline SoftBwdWs soft_bwd_layout(int64_t T, int64_t H, int64_t V, int64_t K) {
+  const BwdWs b = bwd_layout(T, H, V);
   SoftBwdWs w;
-  w.core = bwd_layout(T, H, V);
+  w.T_pad = b.T_pad;
+  w.S_pad = b.S_pad;
+  w.G = b.G;
   Pieces p;
-  p.take(w.core.total);
-  w.rowg = p.take(sizeof(float) * w.core.T_pad);
+  w.idx = p.take(sizeof(int32_t) * T);
+  w.n_act = p.take(sizeof(int32_t));
+  w.rowinfo = p.take(16 * (size_t)w.T_pad);
+  w.rowg = p.take(sizeof(float) * w.T_pad);
+  w.hA = p.take(2 * (size_t)w.T_pad * H);
+  w.dZ = p.take(2 * (size_t)w.T_pad * w.G * w.S_pad);
+  w.part = p.take(sizeof(float) * (size_t)kParts * T * H);
   w.act = p.take(K > 0 ? sizeof(int32_t) * T : 0);
   w.q = p.take(sizeof(float) * (size_t)T * K);
   w.total = p.total;
@@ -215,7 +223,7 @@ rlk_status run_top_fwd(const void* h, const void* W, const int32_t* y, int64_t T
   ma.n_act = n_act;
   ma.y = y;
   ma.G = (int)L.G;
-  ma.R = (int)ceil_div(L.G * la.gm.cps, kSelChunks);
+  ma.R = (int)ceil_div(la.gm.cps, 2 * kSelPer);
   ma.z = la.z;
   ma.ldz = L.ldz;
   ma.K = (int)K;
@@ -232,7 +240,7 @@ rlk_status run_top_fwd(const void* h, const void* W, const int32_t* y, int64_t T
     ma.gm = la.gm;
     ma.first = c == 0;
     ma.last = c + L.G > last;
-    RLK_LAUNCH_V(top_merge, dim3((unsigned)ceil_div(T, kSelWaves)), dim3(64 * kSelWaves), st, ma);
+    RLK_LAUNCH_V(top_merge, dim3((unsigned)(8 * ceil_div(T, 8))), dim3(64), st, ma);
   }
   return RLK_OK;
 }
@@ -295,7 +303,7 @@ rlk_status run_distill_fwd(const void* h, const void* W, const int32_t* ids, con
   ma.loss = loss;
   ma.lse = lse;
   ma.logp_ids = logp_ids;
-  RLK_LAUNCH_V(distill_merge, dim3((unsigned)ceil_div(T, 4)), dim3(256), st, ma);
+  RLK_LAUNCH_V(distill_merge, dim3((unsigned)(8 * ceil_div(T, 8))), dim3(64), st, ma);
   return RLK_OK;
 }
 
@@ -314,23 +322,23 @@ struct SoftBwd {
   int32_t dtype;
 };
 
-rlk_status run_soft_bwd(const SoftBwd& b, const SoftBwdWs& S, void* ws, hipStream_t st) {
-  const BwdWs& L = S.core;
+rlk_status run_soft_bwd(const SoftBwd& b, const SoftBwdWs& L, void* ws, hipStream_t st) {
   const bool top = b.ids == nullptr;
   int32_t* idx = at<int32_t>(ws, L.idx);
   int32_t* n_act = at<int32_t>(ws, L.n_act);
+  float* part = at<float>(ws, L.part);
   const rlk::SplitGeom gm = split_geom(b.V);
   const int tps = (int)ceil_div(gm.S, rlk::kBN), n_tiles = (int)ceil_div(b.H, rlk::kBN), G = (int)L.G;
   const int64_t row_tiles = ceil_div(b.T, rlk::kBM);
   const int64_t dz_blocks = 8 * ceil_div(row_tiles * G * tps, 8);
-  const bool passes = b.grad_h && grad_h_passes(row_tiles, n_tiles);
-  const int64_t gh_blocks = b.grad_h ? 8 * ceil_div(row_tiles * n_tiles * (passes ? 2 : 1), 8) : 0;
+  const int group_parts = (int)ceil_div(G, kPartSplits);
+  const int64_t gh_blocks = b.grad_h ? 8 * ceil_div(row_tiles * n_tiles * group_parts, 8) : 0;
   const int64_t gw_blocks = b.grad_W ? 8 * ceil_div((int64_t)n_tiles * G * tps, 8) : 0;
   RLK_TRY(check_grid(dz_blocks));
   RLK_TRY(check_grid(gh_blocks + gw_blocks));
   if (!top)
     RLK_LAUNCH_V(distill_rows, row_grid(ceil_div(b.T, 4)), dim3(256), st, b.ids, b.logits, (int)b.T, (int)b.K,
-                 (int)b.V, b.scale, at<int32_t>(ws, S.act), at<float>(ws, S.q));
+                 (int)b.V, b.scale, at<int32_t>(ws, L.act), at<float>(ws, L.q));
   RLK_TRY(compact(st, b.act, b.T, b.ignore, idx, nullptr, n_act, nullptr, nullptr, nullptr));
   GatherGradArgs ga{};
   ga.h = static_cast<const uint16_t*>(b.h);
@@ -343,7 +351,7 @@ rlk_status run_soft_bwd(const SoftBwd& b, const SoftBwdWs& S, void* ws, hipStrea
   ga.lse = b.lse;
   ga.g = b.g;
   ga.rowinfo = at<float4>(ws, L.rowinfo);
-  ga.rowg = at<float>(ws, S.rowg);
+  ga.rowg = at<float>(ws, L.rowg);
   ga.y = top ? b.act : nullptr;
   ga.entropy = b.entropy;
   ga.g_entropy = b.g_entropy;
@@ -353,13 +361,6 @@ rlk_status run_soft_bwd(const SoftBwd& b, const SoftBwdWs& S, void* ws, hipStrea
     RLK_LAUNCH_FN("gather_rows_grad", (rlk::vocab::gather_rows_grad<true>), row_grid(L.T_pad), dim3(256), st, ga);
   else
     RLK_LAUNCH_FN("gather_rows_grad", (rlk::vocab::gather_rows_grad<false>), row_grid(L.T_pad), dim3(256), st, ga);
-  if (b.grad_h) {
-    {
-      ProfScope _ps("zero_rows", st);
-      rlk::launch_zero_rows(st, b.act, (int)b.T, b.ignore, (int)b.H, static_cast<uint16_t*>(b.grad_h));
-    }
-    RLK_TRY(launched("zero_rows"));
-  }
   const int last = last_split(gm);
   for (int c = 0; c <= last; c += G) {
     rlk::BwdGeom bg;
@@ -387,7 +388,7 @@ rlk_status run_soft_bwd(const SoftBwd& b, const SoftBwdWs& S, void* ws, hipStrea
       RLK_LAUNCH_FN("soft_dz_tiles", (rlk::vocab::soft_dz_tiles<false>), grid, block, st, da);
       ScatterArgs sa{};
       sa.ids = b.ids;
-      sa.q = at<float>(ws, S.q);
+      sa.q = at<float>(ws, L.q);
       sa.logp_ids = b.logp_ids;
       sa.logits = b.logits;
       sa.idx = idx;
@@ -409,34 +410,30 @@ rlk_status run_soft_bwd(const SoftBwd& b, const SoftBwdWs& S, void* ws, hipStrea
     wa.tps = tps;
     wa.n_tiles = n_tiles;
     wa.grad_W = static_cast<float*>(b.grad_W);
-    rlk::GradHArgs ha{};
+    PartGradHArgs ha{};
     ha.dZ = da.dZ;
     ha.W = da.W;
-    ha.idx = idx;
-    ha.n_act = n_act;
     ha.H = (int)b.H;
     ha.gm = gm;
     ha.bg = bg;
     ha.n_tiles = n_tiles;
-    ha.ghacc = at<float>(ws, L.ghacc);
-    ha.grad_h = static_cast<uint16_t*>(b.grad_h);
-    const bool first = c == 0, fin = c + G > last;
-    // fp32 gradients in one launch; a bf16 grad_W in one of its own
-    const bool bf16 = b.grad_W && b.dtype == RLK_DT_BF16;
-    if (bf16) {
-      wa.grad_W = nullptr;
-      rlk::GradWArgs wb = wa;
-      wb.grad_W = static_cast<float*>(b.grad_W);
-      RLK_LAUNCH_V(gradw_bf16_tiles, dim3((unsigned)gw_blocks), block, st, wb);
-    }
-    if (b.grad_h || !bf16) {
-      {
-        ProfScope _ps("grad_tiles", st);
-        rlk::launch_grad_tiles_w8(first, fin, passes, dim3((unsigned)(gh_blocks + (bf16 ? 0 : gw_blocks))), st, ha, wa);
-      }
-      RLK_TRY(launched("grad_tiles"));
+    ha.part0 = c / kPartSplits;
+    ha.parts = std::min(group_parts, last / kPartSplits + 1 - ha.part0);
+    ha.part = b.grad_h ? part : nullptr;
+    ha.part_stride = (size_t)b.T * b.H;
+    const dim3 gg((unsigned)(gh_blocks + gw_blocks));
+    const bool cont = c % kPartSplits != 0;
+    if (b.dtype == RLK_DT_BF16) {
+      if (cont) RLK_LAUNCH_FN("part_grad_tiles", (rlk::vocab::part_grad_tiles<true, true>), gg, block, st, ha, wa);
+      else RLK_LAUNCH_FN("part_grad_tiles", (rlk::vocab::part_grad_tiles<true, false>), gg, block, st, ha, wa);
+    } else {
+      if (cont) RLK_LAUNCH_FN("part_grad_tiles", (rlk::vocab::part_grad_tiles<false, true>), gg, block, st, ha, wa);
+      else RLK_LAUNCH_FN("part_grad_tiles", (rlk::vocab::part_grad_tiles<false, false>), gg, block, st, ha, wa);
     }
   }
+  if (b.grad_h)
+    RLK_LAUNCH_V(grad_h_sum, row_grid(b.T), dim3(256), st, part, (size_t)b.T * b.H, last / kPartSplits + 1, idx, n_act,
+                 b.act, b.ignore, (int)b.T, (int)b.H, static_cast<uint16_t*>(b.grad_h));
   return RLK_OK;
 }
 
