@@ -27,6 +27,9 @@ namespace vocab {
 
 constexpr int kMaxK = 128;  // alternatives, or teacher's tokens, of a row
 
+// Target of a row that has no dz (rowinfo of the few-row kernels).
+constexpr int kNoRow = INT32_MIN;
+
 // A product e^d * d is 0 where e^d is (d may be -inf there): d is cut off
 // where e^d rounds to 0 in fp32 (e^-103.98 is half the least denormal).
 constexpr float kDeepest = -104.f;
@@ -104,10 +107,14 @@ struct LogitArgs {
   // !kTop
   float scale;
   int K;
-  const int32_t* ent_off;  // [row tile][32 tps + 1]
-  const uint32_t* ent;     // [row tile][256 K]
+  const int32_t* ent_off;  // [row group][32 tps + 1]
+  const uint32_t* ent;     // [row group][kBucketRows K]
   float* z_ids;            // [active row][K]
 };
+
+// Teacher's tokens are sorted in groups of kBucketRows rows (bucket_entries).
+constexpr int kBucketRows = 32;
+static_assert(kWaveRows % kBucketRows == 0 && kBucketRows % kBlk == 0, "a row group is whole row blocks of one wave");
 
 // An entry: column and row within the tile, slot of the row.
 __device__ __forceinline__ uint32_t entry_of(int col, int row, int k) { return (uint32_t)(col | row << 8 | k << 16); }
@@ -158,15 +165,15 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(RLK_WA
   const int lim = width - 4 * rl;  // value k is valid iff chunk_col(k) < lim
 #pragma unroll
   for (int mi = kTailRows; mi < kMI; ++mi) load_row(mi, le);
-  // the tile's entries
+  // the entries of row group rg in this tile
   int e0 = 0, e1 = 0;
   const uint32_t* ent = nullptr;
-  if constexpr (!kTop) {
-    const int32_t* off = a.ent_off + (size_t)rt * (kNSplit * a.tg.tps + 1) + (a.gm.s0 + sl) * a.tg.tps + j;
+  const auto entries = [&](int rg) {
+    const int32_t* off = a.ent_off + (size_t)rg * (kNSplit * a.tg.tps + 1) + (a.gm.s0 + sl) * a.tg.tps + j;
     e0 = __builtin_amdgcn_readfirstlane(off[0]);
     e1 = __builtin_amdgcn_readfirstlane(off[1]);
-    ent = a.ent + (size_t)rt * kBM * a.K;
-  }
+    ent = a.ent + (size_t)rg * kBucketRows * a.K;
+  };
 #pragma unroll
   for (int mi = 0; mi < kMI; ++mi) {
     const int i = i0 + acc_row(wm, mi, le);
@@ -205,6 +212,9 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(RLK_WA
       }
     } else {
       bool staged = false;
+      const int i_mi = i0 + kWaveRows * wm + kBlk * mi;  // first row of the block
+      if (i_mi >= n_act) continue;
+      if (mi * kBlk % kBucketRows == 0) entries(i_mi / kBucketRows);
       for (int eb = e0; eb < e1; eb += 64) {
         const uint32_t x = eb + le < e1 ? ent[eb + le] : 0u;
         const int row = (x >> 8) & 255, col = x & 255;
@@ -245,6 +255,180 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(RLK_WA
     }
   }
 }
+
+// -p (a + b (z - lse)), the softmax's share of dz; z already scaled.
+// rowinfo = {lse, a, b, target}; b counts in the kTop instances only.
+template <bool kTop>
+__device__ __forceinline__ float minus_share(float z, const float4& r) {
+  const float d = z - r.x;
+  const float p = rlk_exp(d);
+  if constexpr (kTop) return -(p * (r.y + r.z * fmaxf(d, kDeepest)));
+  else return -(p * r.y);
+}
+
+#if RLK_MFMA == 16
+// ---------------------------------------------------------------------------
+// Few rows (T <= kFewRows): the same logits, statistics and dz with W streamed
+// straight from HBM into registers.
+//
+// A tile of 256 rows reads W through LDS at one tile per compute unit; with
+// few rows its 608 tiles come in 2.4 rounds, and the last one half empty
+// costs a third of the time.  Here a wave, a block of its own, owns a chunk
+// of 128 columns and all rows: 1216 blocks, all of them resident at once.  W's fragments go from memory to the MFMA's registers,
+// a stage of 32 or 64 k ahead of the one in use; h's come from L2.  Every
+// logit is the engine's MFMA chain (k ascending in steps of 32) in the
+// engine's layout, so the statistics are the same bits.  Rows are those of
+// the batch, in place: no compaction.
+// ---------------------------------------------------------------------------
+constexpr int kFewRows = 64;
+
+struct FewArgs {
+  const uint16_t* h;  // [T, H]
+  const uint16_t* W;
+  int T, H;
+  SplitGeom gm;
+  float scale;  // 1 / temperature; not applied by the kTop instances
+  // logits
+  size_t rec_stride;
+  float2* rec;
+  float* rec_u;
+  float* z;     // row t, chunk c of the vocabulary at t * ldz + 128 c
+  int64_t ldz;
+  // dz
+  const float4* rowinfo;  // [kFewRows] as for soft_dz_tiles; target kNoRow: zeros
+  const float* rowg;
+  BwdGeom bg;
+  uint16_t* dZ;  // rows 0 .. kFewRows - 1 are written
+};
+
+struct FewShape {
+  int rb, steps;  // 16-row blocks, k steps of 32 of a stage
+};
+// up to 16, 32 and 64 rows.  A stage of 64 k asks for whole cache lines and
+// keeps 16 KB in flight per wave; at 64 rows only one of 32 k fits the
+// registers beside the accumulators.  us at H = 4096, V = 151936: 230 (1
+// row), 242 (32), 335 (64); with 64 columns a wave, three waves per SIMD, 237,
+// 270 and 392; with the 64 rows as two waves of 32, 465 to 500; non-temporal
+// loads of W 260, 310, 415; the 256-row tiles 300 for any.
+constexpr FewShape kFewShapes[3] = {{1, 2}, {2, 2}, {4, 1}};
+constexpr int few_shape(int64_t T) { return T <= 16 ? 0 : T <= 32 ? 1 : 2; }
+
+template <bool kTop, bool kDz, int kShape>
+__global__ __launch_bounds__(64) __attribute__((amdgpu_waves_per_eu(2))) void few_tiles(FewArgs a) {
+  constexpr int kRB = kFewShapes[kShape].rb, kSteps = kFewShapes[kShape].steps, kDepth = 2;
+  constexpr int kCB = kChunk / 16;
+  // block -> chunk j of split s (of the group, for dz)
+  const int s = blockIdx.x / a.gm.cps, j = blockIdx.x - s * a.gm.cps;
+  const int sbeg = (a.gm.s0 + s) * a.gm.S, valid_s = max(0, min(a.gm.S, a.gm.V - sbeg));
+  const int width = min(kChunk, valid_s - j * kChunk);  // columns of the chunk
+  if (!kDz && width <= 0) return;
+  const int lane = threadIdx.x, r16 = lane & 15, rl = lane >> 4;
+  float acc_v[kRB][kCB][4];
+  {
+    // lane l: row l % 16 of a block, k = 8 (l / 16) .. + 7 of a step
+    const int c0 = sbeg + j * kChunk, last = max(width, 1) - 1;
+    const char* wb = reinterpret_cast<const char*>(a.W + (size_t)(width > 0 ? c0 : 0) * a.H);
+    const char* hb = reinterpret_cast<const char*>(a.h);
+    uint32_t wo[kCB], ho[kRB];
+#pragma unroll
+    for (int n = 0; n < kCB; ++n) wo[n] = 2u * ((uint32_t)min(16 * n + r16, last) * a.H + 8 * rl);
+#pragma unroll
+    for (int m = 0; m < kRB; ++m) ho[m] = 2u * ((uint32_t)min(16 * m + r16, a.T - 1) * a.H + 8 * rl);
+    struct Stage {
+      bf16x8 w[kSteps][kCB], h[kSteps][kRB];
+    } st[kDepth];
+    const int ns = a.H / (32 * kSteps);
+    const auto load = [&](Stage& x, int i) {  // (past the end: the last stage again)
+      const size_t k2 = (size_t)min(i, ns - 1) * (64 * kSteps);
+#pragma unroll
+      for (int q = 0; q < kSteps; ++q) {
+#pragma unroll
+        for (int n = 0; n < kCB; ++n) x.w[q][n] = *reinterpret_cast<const bf16x8*>(wb + k2 + 64 * q + wo[n]);
+#pragma unroll
+        for (int m = 0; m < kRB; ++m) x.h[q][m] = *reinterpret_cast<const bf16x8*>(hb + k2 + 64 * q + ho[m]);
+      }
+    };
+    AccBlk acc[kRB][kCB];
+#pragma unroll
+    for (int m = 0; m < kRB; ++m)
+#pragma unroll
+      for (int n = 0; n < kCB; ++n) acc[m][n] = AccBlk{};
+#pragma unroll
+    for (int d = 0; d + 1 < kDepth; ++d) load(st[d], d);
+#pragma unroll 1
+    for (int i = 0; i < ns; i += kDepth) {
+#pragma unroll
+      for (int d = 0; d < kDepth; ++d) {
+        if (i + d >= ns) break;
+        load(st[(d + kDepth - 1) % kDepth], i + d + kDepth - 1);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int q = 0; q < kSteps; ++q)
+#pragma unroll
+          for (int m = 0; m < kRB; ++m)
+#pragma unroll
+            for (int n = 0; n < kCB; ++n)
+              acc[m][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(st[d].w[q][n], st[d].h[q][m], acc[m][n], 0, 0, 0);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+#pragma unroll
+    for (int m = 0; m < kRB; ++m)
+#pragma unroll
+      for (int n = 0; n < kCB; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc_v[m][n][e] = kTop ? acc[m][n][e] : acc[m][n][e] * a.scale;
+  }
+  // lane l holds row 16 m + l % 16, columns 16 n + 4 (l / 16) + e
+  if constexpr (kDz) {
+#pragma unroll
+    for (int m = 0; m < kFewRows / 16; ++m) {  // (zeros below the rows at hand)
+      const int t = 16 * m + r16;
+      const float4 ri = a.rowinfo[t];
+      const int target = __float_as_int(ri.w), yl = target - sbeg - j * kChunk;
+      const bool on = m < kRB && target != kNoRow;
+      const float g = kTop && on ? a.rowg[t] : 0.f;
+#pragma unroll
+      for (int n = 0; n < kCB; ++n) {
+        const int c = 16 * n + 4 * rl;
+        if (j * kChunk + c >= a.bg.S_pad) continue;  // the next split's columns
+        float d[4] = {0.f, 0.f, 0.f, 0.f};
+        if (m < kRB && on) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (c + e < width) {
+              const float x = minus_share<kTop>(acc_v[m < kRB ? m : 0][n][e], ri);
+              d[e] = kTop && c + e == yl ? g + x : x;
+            }
+        }
+        *reinterpret_cast<uint2*>(a.dZ + (size_t)t * a.bg.ldz + (size_t)s * a.bg.S_pad + j * kChunk + c) =
+            make_uint2(pack_bf16x2(d[0], d[1]), pack_bf16x2(d[2], d[3]));
+      }
+    }
+  } else {
+    const int g = (a.gm.s0 + s) * a.gm.cps + j;
+#pragma unroll
+    for (int m = 0; m < kRB; ++m) {
+      const int t = 16 * m + r16;
+      float v[4 * kCB];
+#pragma unroll
+      for (int n = 0; n < kCB; ++n) {
+        const int c = 16 * n + 4 * rl;
+        if (t < a.T)  // whole chunks: what lies past the split's end is not read
+          *reinterpret_cast<float4*>(a.z + (size_t)t * a.ldz + (size_t)g * kChunk + c) =
+              make_float4(acc_v[m][n][0], acc_v[m][n][1], acc_v[m][n][2], acc_v[m][n][3]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[4 * n + e] = c + e < width ? acc_v[m][n][e] : -INFINITY;
+      }
+      const MSU st = chunk_stats_moment(v);
+      if (rl == 0 && t < a.T) {
+        a.rec[(size_t)g * a.rec_stride + t] = make_float2(st.m, st.s);
+        if (kTop) a.rec_u[(size_t)g * a.rec_stride + t] = st.u;
+      }
+    }
+  }
+}
+#endif  // RLK_MFMA == 16
 
 // ---------------------------------------------------------------------------
 // Row gathers
@@ -291,8 +475,7 @@ __global__ __launch_bounds__(256) void gather_rows_fill(GatherArgs a) {
 
 // hA as above, and per active row the coefficients of
 //     dz_v = g [v == target] - p_v (a + b (z_v - lse)),  p_v = e(z_v - lse):
-// rowinfo = {lse, a, b, target (bits)}, rowg = g; {0, 0, 0, -1} and 0 past
-// n_act.  top: a = g + b entropy, b = dL/dentropy.  distill: a = -(dL/dloss
+// rowinfo = {lse, a, b, target (bits)}, rowg = g; {0, 0, 0, -1} past n_act.  top: a = g + b entropy, b = dL/dentropy.  distill: a = -(dL/dloss
 // / temperature), b = 0, no target; the teacher's share of dz comes from
 // distill_scatter.  A row without a defined loss (a target, or a kept
 // teacher's token, outside the vocabulary) gets NaN coefficients.
@@ -316,30 +499,46 @@ struct GatherGradArgs {
 };
 
 template <bool kTop>
+__device__ __forceinline__ float4 grad_row(const GatherGradArgs& a, int t, float* g_out) {
+  float4 ri = make_float4(a.lse[t], 0.f, 0.f, __int_as_float(-1));
+  float gt = 0.f;
+  if constexpr (kTop) {
+    const int yt = a.y[t];
+    gt = a.g ? a.g[t] : 0.f;
+    if (yt < 0 || yt >= a.V) gt = __builtin_nanf("");
+    ri.z = a.g_entropy ? a.g_entropy[t] : 0.f;
+    ri.y = gt + ri.z * a.entropy[t];
+    ri.w = __int_as_float(yt);
+  } else {
+    ri.y = a.act[t] == 1 ? __builtin_nanf("") : -(a.g[t] * a.scale);
+  }
+  *g_out = gt;
+  return ri;
+}
+
+template <bool kTop>
 __global__ __launch_bounds__(256) void gather_rows_grad(GatherGradArgs a) {
   const int n_act = *a.n_act;
   for (int i = blockIdx.x; i < a.rows; i += gridDim.x) {
     gather_row(a.h, a.idx, n_act, i, a.H, a.hA);
-    if (threadIdx.x == 0) {
-      float4 ri = make_float4(0.f, 0.f, 0.f, __int_as_float(-1));
-      float gt = 0.f;
-      if (i < n_act) {
-        const int t = a.idx[i];
-        ri.x = a.lse[t];
-        if constexpr (kTop) {
-          const int yt = a.y[t];
-          gt = a.g ? a.g[t] : 0.f;
-          if (yt < 0 || yt >= a.V) gt = __builtin_nanf("");
-          ri.z = a.g_entropy ? a.g_entropy[t] : 0.f;
-          ri.y = gt + ri.z * a.entropy[t];
-          ri.w = __int_as_float(yt);
-        } else {
-          ri.y = a.act[t] == 1 ? __builtin_nanf("") : -(a.g[t] * a.scale);
-        }
-      }
-      a.rowinfo[i] = ri;
-      a.rowg[i] = gt;
-    }
+    if (threadIdx.x == 0)
+      a.rowinfo[i] = i < n_act ? grad_row<kTop>(a, a.idx[i], a.rowg + i) : make_float4(0.f, 0.f, 0.f, __int_as_float(-1));
+  }
+}
+
+// Few rows: the batch's rows in place.  hA[t] = h[t], zeros for inactive rows
+// and past T (they meet dz = 0 in grad_W, and may hold anything in h);
+// n_act = T.  Grid: `rows` blocks.
+template <bool kTop>
+__global__ __launch_bounds__(256) void few_rows_grad(GatherGradArgs a, int T, int ignore_index, int32_t* n_act) {
+  const int t = blockIdx.x;
+  const bool on = t < T && a.act[t] != ignore_index;
+  u32x4* dst = reinterpret_cast<u32x4*>(a.hA + (size_t)t * a.H);
+  const u32x4* src = reinterpret_cast<const u32x4*>(a.h + (size_t)t * a.H);
+  for (int p = threadIdx.x; p < a.H / 8; p += 256) dst[p] = on ? src[p] : u32x4{0u, 0u, 0u, 0u};
+  if (threadIdx.x == 0) {
+    a.rowinfo[t] = on ? grad_row<kTop>(a, t, a.rowg + t) : make_float4(0.f, 0.f, 0.f, __int_as_float(kNoRow));
+    if (t == 0) *n_act = T;
   }
 }
 
@@ -423,62 +622,68 @@ __global__ __launch_bounds__(256) void distill_rows(const int32_t* __restrict__ 
   }
 }
 
-// The entries of each row tile (256 active rows), grouped by the vocabulary
-// tile their token lies in: off[rt][c] .. off[rt][c + 1] are those of tile c
+// The entries of every kBucketRows active rows, grouped by the vocabulary
+// tile their token lies in: off[rb][c] .. off[rb][c + 1] are those of tile c
 // (= split * tps + tile of the split).  Within a tile the order is left open:
-// every entry writes a place of its own.  One block per row tile.
-constexpr int kBucketThreads = 1024;
+// every entry writes a place of its own.  One block per row group: small
+// groups, since a teacher's tokens crowd in few tiles, whose counters take
+// their entries one after the other (256 rows of 128 in one block: 38 us).
+constexpr int kBucketThreads = 256;
 constexpr int kMaxVTiles = 32768;  // 32 tps for the largest vocabulary: 31264
+template <int kTiles>
 __global__ __launch_bounds__(kBucketThreads) void bucket_entries(const int32_t* __restrict__ ids,
                                                                  const float* __restrict__ logits,
                                                                  const int32_t* __restrict__ idx,
                                                                  const int32_t* __restrict__ n_act_p, int K,
                                                                  SplitGeom gm, int tps, int32_t* __restrict__ off,
                                                                  uint32_t* __restrict__ ent) {
-  __shared__ int32_t cnt[kMaxVTiles];
+  __shared__ int32_t cnt[kTiles];
+  __shared__ int32_t row_s[kBucketRows];
   __shared__ int32_t wave_tot[kBucketThreads / 64];
-  const int rt = blockIdx.x, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int i0 = rt * kBM, n = min(kBM, *n_act_p - i0);
+  const int rg = blockIdx.x, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int i0 = rg * kBucketRows, n = min(kBucketRows, *n_act_p - i0);
   if (n <= 0) return;
   const int C = kNSplit * tps;
   for (int c = tid; c < C; c += kBucketThreads) cnt[c] = 0;
+  if (tid < n) row_s[tid] = idx[i0 + tid];
   __syncthreads();
   // thread tid takes slot tid % kp of rows tid / kp, + kBucketThreads / kp,
-  // ... (kp: the power of two at or above K), all loads in flight at once
+  // ... (kp: the power of two at or above K), kAhead of them at a time: the
+  // loads unrolled, the loop not (see the row kernels below)
   const int kp = 1 << (32 - __builtin_clz(max(K - 1, 1))), shift = __builtin_ctz(kp);
   const int k = tid & (kp - 1), r0 = tid >> shift, step = kBucketThreads >> shift;
-  constexpr int kPer = kBM * kMaxK / kBucketThreads;  // rows of a thread
-  int id[kPer], bin[kPer];
-  float lg[kPer];
-#pragma unroll
-  for (int e = 0; e < kPer; ++e) {
-    const int r = r0 + e * step;
-    id[e] = -1;
-    lg[e] = 0.f;
-    if (r < n && k < K) {
-      const size_t at = (size_t)idx[i0 + r] * K + k;
-      id[e] = ids[at];
-      lg[e] = logits[at];
-    }
-  }
   const uint32_t rcp = (uint32_t)(((uint64_t(1) << 32) - 1) / (uint32_t)gm.S);
-  uint32_t ent_e[kPer];
+  constexpr int kAhead = 8;
+  const auto each = [&](auto&& f) {
+#pragma unroll 1
+    for (int rb = r0; rb - r0 < n; rb += kAhead * step) {
+      int id[kAhead];
+      float lg[kAhead];
 #pragma unroll
-  for (int e = 0; e < kPer; ++e) {
-    bin[e] = -1;
-    ent_e[e] = 0;
-    if (id[e] < gm.V && slot_kept(id[e], lg[e])) {
-      // id / S: the truncated reciprocal's quotient is short by at most one
-      int q = (int)__umulhi((uint32_t)id[e], rcp), c = id[e] - q * gm.S;
-      if (c >= gm.S) {
-        c -= gm.S;
-        ++q;
+      for (int e = 0; e < kAhead; ++e) {
+        const int r = rb + e * step;
+        id[e] = -1;
+        lg[e] = 0.f;
+        if (r < n && k < K) {
+          const size_t at = (size_t)row_s[r] * K + k;
+          id[e] = ids[at];
+          lg[e] = logits[at];
+        }
       }
-      bin[e] = q * tps + (c >> 8);
-      ent_e[e] = entry_of(c & 255, r0 + e * step, k);
-      atomicAdd(&cnt[bin[e]], 1);
+#pragma unroll
+      for (int e = 0; e < kAhead; ++e) {
+        if (id[e] >= gm.V || !slot_kept(id[e], lg[e])) continue;
+        // id / S: the truncated reciprocal's quotient is short by at most one
+        int q = (int)__umulhi((uint32_t)id[e], rcp), c = id[e] - q * gm.S;
+        if (c >= gm.S) {
+          c -= gm.S;
+          ++q;
+        }
+        f(q * tps + (c >> 8), entry_of(c & 255, i0 % kBM + rb + e * step, k));
+      }
     }
-  }
+  };
+  each([&](int bin, uint32_t) { atomicAdd(&cnt[bin], 1); });
   __syncthreads();
   // exclusive scan: thread tid takes `per` consecutive tiles
   const int per = (C + kBucketThreads - 1) / kBucketThreads;
@@ -495,7 +700,7 @@ __global__ __launch_bounds__(kBucketThreads) void bucket_entries(const int32_t* 
   __syncthreads();
   int pos = incl - sum;
   for (int w = 0; w < wave; ++w) pos += wave_tot[w];
-  int32_t* o = off + (size_t)rt * (C + 1);
+  int32_t* o = off + (size_t)rg * (C + 1);
   for (int c = lo; c < hi; ++c) {
     const int v = cnt[c];
     o[c] = pos;
@@ -504,10 +709,8 @@ __global__ __launch_bounds__(kBucketThreads) void bucket_entries(const int32_t* 
   }
   if (tid == kBucketThreads - 1) o[C] = pos;
   __syncthreads();
-  uint32_t* e0 = ent + (size_t)rt * kBM * K;
-#pragma unroll
-  for (int e = 0; e < kPer; ++e)
-    if (bin[e] >= 0) e0[atomicAdd(&cnt[bin[e]], 1)] = ent_e[e];
+  uint32_t* e0 = ent + (size_t)rg * kBucketRows * K;
+  each([&](int bin, uint32_t x) { e0[atomicAdd(&cnt[bin], 1)] = x; });
 }
 
 // ---------------------------------------------------------------------------
@@ -524,6 +727,12 @@ __device__ __forceinline__ void wave_lds_sync() {
   __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
   __builtin_amdgcn_wave_barrier();
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
+// Place of token v's logit in a row of all chunks' logits.
+__device__ __forceinline__ int logit_at(const SplitGeom& gm, int v) {
+  const int s = v / gm.S;
+  return s * gm.cps * kChunk + (v - s * gm.S);
 }
 
 // Chunks of split `s` that hold columns.
@@ -668,9 +877,10 @@ struct TopMergeArgs {
   const float2* rec;
   const float* rec_u;
   size_t rec_stride;
-  const float* zt;
-  const int32_t* idx;
+  const float* zt;       // NULL: the target's logit is in z
+  const int32_t* idx;    // NULL: every row of the batch, in place
   const int32_t* n_act;
+  int T, ignore_index;
   const int32_t* y;
   SplitGeom gm;    // gm.s0: first split of the group
   int G;           // splits of the group whose logits z holds
@@ -691,8 +901,20 @@ __global__ __launch_bounds__(64) void top_merge(TopMergeArgs a) {
   __shared__ uint32_t pool[kSelRuns];  // run maxima; then logits; then the fold's records
   __shared__ uint64_t list[kSelList];
   __shared__ uint16_t picks[kSelRuns];
-  const int lane = threadIdx.x, i = xcd_tile(*a.n_act, blockIdx.x);
+  const int lane = threadIdx.x, i = xcd_tile(a.idx ? *a.n_act : a.T, blockIdx.x);
   if (i < 0) return;
+  const int t = a.idx ? a.idx[i] : i, yt = a.y[t];
+  if (!a.idx && yt == a.ignore_index) {
+    if (lane == 0) {
+      a.logp[t] = a.entropy[t] = 0.f;
+      if (a.lse) a.lse[t] = 0.f;
+    }
+    for (int k = lane; k < a.K; k += 64) {
+      a.top_ids[(size_t)t * a.K + k] = -1;
+      a.top_logp[(size_t)t * a.K + k] = -INFINITY;
+    }
+    return;
+  }
   int n = 0;
   if (a.K > 0) {
     // this lane's runs of R chunks: run e is chunks j0 + e R .. of split s0 + sl
@@ -808,10 +1030,13 @@ __global__ __launch_bounds__(64) void top_merge(TopMergeArgs a) {
   if (!a.last) return;
   const MSU tot = fold_row<true>(a.rec, a.rec_u, a.rec_stride, i, a.gm, reinterpret_cast<float*>(pool));
   const float m = __shfl(tot.m, 0), L = rlk_log(__shfl(tot.s, 0));
-  const int t = a.idx[i];
   if (lane == 0) {
-    const int yt = a.y[t];
-    a.logp[t] = yt >= 0 && yt < a.gm.V ? (a.zt[i] - m) - L : __builtin_nanf("");
+    float lp = __builtin_nanf("");
+    if (yt >= 0 && yt < a.gm.V) {
+      const float zt = a.zt ? a.zt[i] : a.z[(size_t)i * a.ldz + logit_at(a.gm, yt)];
+      lp = (zt - m) - L;
+    }
+    a.logp[t] = lp;
     if (a.lse) a.lse[t] = m + L;
     a.entropy[t] = L - tot.u / tot.s;
   }
@@ -837,7 +1062,10 @@ struct DistillMergeArgs {
   float scale;
   const int32_t* ids;
   const float* logits;
-  const float* z_ids;  // [active row][K], scaled
+  const float* z_ids;  // [active row][K], scaled; NULL: they are in z
+  const float* z;      // (idx, n_act NULL: every row of the batch, in place)
+  int64_t ldz;
+  int T;
   float* loss;
   float* lse;
   float* logp_ids;
@@ -845,12 +1073,22 @@ struct DistillMergeArgs {
 
 __global__ __launch_bounds__(64) void distill_merge(DistillMergeArgs a) {
   __shared__ float buf[kFoldFloats];
-  const int lane = threadIdx.x, i = xcd_tile(*a.n_act, blockIdx.x);
+  const int lane = threadIdx.x, i = xcd_tile(a.idx ? *a.n_act : a.T, blockIdx.x);
   if (i < 0) return;
+  const int t = a.idx ? a.idx[i] : i;
+  const TeacherRow r = teacher_row(a.ids + (size_t)t * a.K, a.logits + (size_t)t * a.K, a.K, a.scale);
+  if (!a.idx) {
+    bool any = false;
+#pragma unroll
+    for (int s = 0; s < kSlots2; ++s) any |= r.kept[s];
+    if (!__builtin_amdgcn_ballot_w64(any)) {
+      if (lane == 0) a.loss[t] = a.lse[t] = 0.f;
+      for (int k = lane; k < a.K; k += 64) a.logp_ids[(size_t)t * a.K + k] = -INFINITY;
+      return;
+    }
+  }
   const MSU tot = fold_row<false>(a.rec, nullptr, a.rec_stride, i, a.gm, buf);
   const float m = __shfl(tot.m, 0), L = rlk_log(__shfl(tot.s, 0));
-  const int t = a.idx[i];
-  const TeacherRow r = teacher_row(a.ids + (size_t)t * a.K, a.logits + (size_t)t * a.K, a.K, a.scale);
   float sum = 0.f;
 #pragma unroll
   for (int s = 0; s < kSlots2; ++s) {
@@ -858,7 +1096,11 @@ __global__ __launch_bounds__(64) void distill_merge(DistillMergeArgs a) {
     if (k >= a.K) continue;
     float lp = -INFINITY;
     if (r.kept[s]) {
-      lp = r.id[s] < a.gm.V ? (a.z_ids[(size_t)i * a.K + k] - m) - L : __builtin_nanf("");
+      lp = __builtin_nanf("");
+      if (r.id[s] < a.gm.V) {
+        const float z = a.z_ids ? a.z_ids[(size_t)i * a.K + k] : a.z[(size_t)i * a.ldz + logit_at(a.gm, r.id[s])];
+        lp = (z - m) - L;
+      }
       // a token that the teacher gives no weight adds nothing, whatever the student gives it
       if (r.q[s] != 0.f || lp != lp) sum = sum + r.q[s] * (r.lq[s] - lp);
     }
@@ -936,12 +1178,7 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(RLK_WA
     const uint32_t off = 512u * r + 16u * ((c >> 3) ^ (r & 31)) + 8u * ((c >> 2) & 1);
     *reinterpret_cast<uint2*>(stage + off) = make_uint2(pack_bf16x2(d[0], d[1]), pack_bf16x2(d[2], d[3]));
   };
-  const auto minus_share = [&](float z, const float4& r) {  // -p (a + b d)
-    const float d = (kTop ? z : z * a.scale) - r.x;
-    const float p = rlk_exp(d);
-    if constexpr (kTop) return -(p * (r.y + r.z * fmaxf(d, kDeepest)));
-    else return -(p * r.y);
-  };
+  const auto share = [&](float z, const float4& r) { return minus_share<kTop>(kTop ? z : z * a.scale, r); };
   const int wc0 = j * kBN + 128 * wn;  // first column of the wave within the split
   const bool full = i0 + kWaveRows * wm + kWaveRows <= n_act && wc0 + 128 <= valid_s;
 #pragma unroll
@@ -958,7 +1195,7 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(RLK_WA
         for (int q = 0; q < kQL; ++q) {
           float d[4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) d[e] = minus_share(acc.c[mi][ni][4 * q + e], ri[mi]);
+          for (int e = 0; e < 4; ++e) d[e] = share(acc.c[mi][ni][4 * q + e], ri[mi]);
           put(r, acc_col4(wn, ni, q, le), d);
         }
     } else {
@@ -973,7 +1210,7 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(RLK_WA
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const int vl = j * kBN + c + e;
-            const float x = minus_share(acc.c[mi][ni][4 * q + e], ri[mi]);
+            const float x = share(acc.c[mi][ni][4 * q + e], ri[mi]);
             d[e] = rvalid && vl < valid_s ? (kTop && vl == yl ? g + x : x) : 0.f;
           }
           put(r, c, d);
@@ -1003,7 +1240,7 @@ struct ScatterArgs {
   const float* q;         // [T][K], 0 for slots that are not kept
   const float* logp_ids;  // [T][K]
   const float* logits;
-  const int32_t* idx;
+  const int32_t* idx;  // NULL: every row of the batch, in place
   const int32_t* n_act;
   const float4* rowinfo;
   int K;
@@ -1017,7 +1254,7 @@ __global__ __launch_bounds__(kMaxK) void distill_scatter(ScatterArgs a) {
   __shared__ float q_s[kMaxK];
   const int k = threadIdx.x, n_act = *a.n_act;
   for (int i = blockIdx.x; i < n_act; i += gridDim.x) {
-    const size_t at = (size_t)a.idx[i] * a.K + k;
+    const size_t at = (size_t)(a.idx ? a.idx[i] : i) * a.K + k;
     int id = -1;
     if (k < a.K && slot_kept(a.ids[at], a.logits[at])) id = a.ids[at];
     if (id >= a.gm.V) id = -1;
@@ -1075,9 +1312,11 @@ struct PartGradHArgs {
 template <bool kCont>
 __device__ __forceinline__ void gradh_part_tile(const PartGradHArgs& a, int id, int rtiles, int n_act, u32x4* lds) {
   const int per = rtiles * a.n_tiles;
-  const int q = id / per;  // part within the group
+  const int q = __builtin_amdgcn_readfirstlane(id / per);  // part within the group
   int rt, nt;
   grouped_tile(id - q * per, rtiles, rt, nt, a.n_tiles, row_group(rtiles));
+  rt = __builtin_amdgcn_readfirstlane(rt);  // (tile addresses derive from them)
+  nt = __builtin_amdgcn_readfirstlane(nt);
   const int i0 = rt * kBM, n0 = nt * kBN;
   const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, wm = wave_m(w), wn = wave_n(w);
   float* part = a.part + (size_t)(a.part0 + q) * a.part_stride;
@@ -1143,7 +1382,9 @@ __device__ __forceinline__ void gradh_part_tile(const PartGradHArgs& a, int id, 
 __device__ __forceinline__ void gradw_bf16_tile(const GradWArgs& a, int id, int n_act, u32x4* lds) {
   int nt, vt;
   grouped_tile(id, a.n_tiles, nt, vt, a.bg.G * a.tps, min(kGradWGroup, a.n_tiles));
-  const int sc = vt / a.tps, j = vt - sc * a.tps;
+  nt = __builtin_amdgcn_readfirstlane(nt);  // (tile addresses derive from them)
+  vt = __builtin_amdgcn_readfirstlane(vt);
+  const int sc = __builtin_amdgcn_readfirstlane(vt / a.tps), j = vt - sc * a.tps;
   const int sbeg = (a.bg.c_lo + sc) * a.gm.S;
   const int valid_s = max(0, min(a.gm.S, a.gm.V - sbeg));
   const int v0 = j * kBM;  // within the split
@@ -1214,19 +1455,323 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(RLK_WA
   else gradw_tile(wa, id, n_act, lds);
 }
 
+#if RLK_MFMA == 16
+// ---------------------------------------------------------------------------
+// Gradients of few rows.  Both are bound by W's traffic (grad_h reads it,
+// grad_W has its size), and the 256 x 256 tiles leave that far off: 64 of
+// them for grad_h at H = 4096, each as long as its part, and for grad_W one
+// tile at a time per compute unit, loads, MFMAs and stores in turn.  Together
+// they took 0.92 ms at 64 rows (V = 151936).
+// ---------------------------------------------------------------------------
+// Waves wait for their own direct loads, all but the n issued last, and then
+// for one another.
+template <int n>
+__device__ __forceinline__ void loads_then_barrier() {
+  asm volatile("s_waitcnt vmcnt(%0)" : : "n"(n) : "memory");
+  wait_lds();
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_sched_barrier(0);
+}
+
+// Eight k of one column for each lane, from two transposing reads: `base` is
+// where the lane's 4 columns of k-row 8 (l / 16) + (l % 16) / 4 lie, kr the
+// bytes of 4 k-rows (which keep the swizzle; see frag_at).
+__device__ __forceinline__ bf16x8 tr_frag(const char* base, uint32_t kr4) {
+  const lds_bf16x4* p0 = (const lds_bf16x4*)base;
+  const lds_bf16x4* p1 = (const lds_bf16x4*)(base + kr4);
+  const bf16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4bf16(const_cast<lds_bf16x4*>(p0));
+  const bf16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4bf16(const_cast<lds_bf16x4*>(p1));
+  return bf16x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+}
+
+// grad_h of up to 128 rows: a block takes 64 columns of one part and streams
+// the part's W through a ring of kSlots LDS stages of 64 vocabulary rows
+// (8 KB, and the dz block they meet), kSlots - 1 in flight.  Its four waves
+// take 16 columns each, or (above 64 rows, where reading dz from LDS counts)
+// 32 columns and half of the rows.  The same chains as
+// gradh_part_tile.
+// A stage: W as 64 k-rows of 128 bytes, 32-byte units xor-ed with
+// (row >> 1 & 1) + 2 (row >> 3 & 1): the 8 k-rows of a transposing pass fall
+// on distinct banks; dz as rows of 128 bytes in the engine's K layout (slot_k).
+struct FewGradHArgs {
+  const uint16_t* dZ;  // 16 kRB rows at least
+  const uint16_t* W;
+  const int32_t* n_act;
+  int H;
+  SplitGeom gm;
+  BwdGeom bg;
+  int part0, parts;
+  float* part;         // as in PartGradHArgs
+  size_t part_stride;
+};
+
+template <int kRB, bool kCont>
+__global__ __launch_bounds__(256) void few_grad_h(FewGradHArgs a) {
+  constexpr int kRows = 16 * (kRB < 2 ? 2 : kRB);  // dz rows of a stage (32 at least: every wave loads as many)
+  constexpr uint32_t kWBytes = 64 * 128, kStage = kWBytes + kRows * 128;
+  constexpr int kSlots = (160 << 10) / kStage, kLoads = 2 + kRows / 32;
+  static_assert((kSlots - 2) * kLoads < 64, "vmcnt");
+  constexpr int kC = kRB >= 8 ? 2 : 1, kR = kRB / kC;  // 16-column and 16-row blocks of a wave
+  __shared__ u32x4 lds[kSlots * kStage / 16];
+  const int n_act = __builtin_amdgcn_readfirstlane(*a.n_act);
+  const int n_tiles = a.H / 64;
+  const int id = n_act > 0 ? xcd_tile(n_tiles * a.parts, blockIdx.x) : -1;
+  if (id < 0) return;
+  const int q = __builtin_amdgcn_readfirstlane(id / n_tiles), n0 = 64 * (id - q * n_tiles);
+  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int r16 = lane & 15, rl = lane >> 4;
+  const int wc = kC == 1 ? 16 * w : 32 * (w & 1), wr = kC == 1 ? 0 : 16 * kR * (w >> 1);  // first column, row
+  const int s0 = q * kPartSplits, splits = min(kPartSplits, a.bg.G - s0), kbps = a.bg.S_pad / kBK;
+  const int nk = splits * kbps;
+  // direct loads of this lane: W rows 16 w + 8 i + lane / 8, dz rows 8 (w + 4 i) + lane / 8
+  uint32_t w_row[2], w_col[2], dz_off[kRows / 32];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int row = 16 * w + 8 * i + (lane >> 3), p = lane & 7;
+    const int f = ((row >> 1) & 1) | ((row >> 2) & 2);
+    w_row[i] = row;
+    w_col[i] = 2 * n0 + 16 * ((((p >> 1) ^ f) << 1) | (p & 1));
+  }
+#pragma unroll
+  for (int i = 0; i < kRows / 32; ++i) {
+    const int row = 8 * (w + 4 * i) + (lane >> 3);
+    dz_off[i] = 2u * ((uint32_t)row * (uint32_t)a.bg.ldz) + 16u * ((lane & 7) ^ ((row >> 1) & 7));
+  }
+  const char* dz = reinterpret_cast<const char*>(a.dZ + (size_t)s0 * a.bg.S_pad);
+  const uint32_t lds0 = lds_addr(lds);
+  int l_sc = 0, l_kb = 0, l_kt = 0;  // the stage loaded next: split, k-block of it, k-block of the part
+  const auto load = [&](int slot) {
+    const uint32_t m0 = lds0 + kStage * slot;
+    const int r0 = min((a.bg.c_lo + s0 + l_sc) * a.gm.S + kBK * l_kb, a.gm.V - 1);
+    const uint32_t last = (uint32_t)(a.gm.V - 1 - r0);  // (rows past it meet dz = 0)
+    const char* wb = reinterpret_cast<const char*>(a.W) + (size_t)r0 * (2 * a.H);
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      dma16(wb, min(w_row[i], last) * (uint32_t)(2 * a.H) + w_col[i], m0 + 1024u * (2 * w + i));
+#pragma unroll
+    for (int i = 0; i < kRows / 32; ++i)
+      dma16(dz + (size_t)l_kt * (2 * kBK), dz_off[i], m0 + kWBytes + 1024u * (w + 4 * i));
+    if (l_kt + 1 < nk) {  // (past the end: the last stage again, into a free slot)
+      ++l_kt;
+      if (++l_kb == kbps) {
+        l_kb = 0;
+        ++l_sc;
+      }
+    }
+  };
+  AccBlk acc[kR][kC];
+  float* part = a.part + (size_t)(a.part0 + q) * a.part_stride + n0 + wc + 4 * rl;
+#pragma unroll
+  for (int m = 0; m < kR; ++m)
+#pragma unroll
+    for (int c = 0; c < kC; ++c) {
+      acc[m][c] = AccBlk{};
+      if (kCont) {
+        const float4 v = *reinterpret_cast<const float4*>(part + (size_t)min(wr + 16 * m + r16, n_act - 1) * a.H + 16 * c);
+        acc[m][c] = AccBlk{v.x, v.y, v.z, v.w};
+      }
+    }
+  // this lane's W fragments within a stage: k step kk 32 k-rows further (the swizzle stays, as for k-rows + 4)
+  const int krow = 8 * rl + (r16 >> 2), f = ((krow >> 1) & 1) | ((krow >> 2) & 2);
+  uint32_t w_at[kC];
+#pragma unroll
+  for (int c = 0; c < kC; ++c) w_at[c] = 128u * krow + 32u * (((wc >> 4) + c) ^ f) + 8u * (r16 & 3);
+  if (kCont) asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // (the loads below are counted)
+#pragma unroll 1
+  for (int i = 0; i + 1 < kSlots; ++i) load(i);
+  int slot = 0;
+#pragma unroll 1
+  for (int kt = 0; kt < nk; ++kt) {
+    loads_then_barrier<(kSlots - 2) * kLoads>();
+    load(slot == 0 ? kSlots - 1 : slot - 1);  // the slot read last time
+    const char* st = reinterpret_cast<const char*>(lds) + kStage * slot;
+#pragma unroll
+    for (int kk = 0; kk < 2; ++kk) {
+      bf16x8 y[kC];
+#pragma unroll
+      for (int c = 0; c < kC; ++c) y[c] = tr_frag(st + w_at[c] + 128u * 32 * kk, 128u * 4);
+#pragma unroll
+      for (int m = 0; m < kR; ++m) {
+        const bf16x8 x = __builtin_bit_cast(
+            bf16x8, *reinterpret_cast<const u32x4*>(st + kWBytes + 16u * slot_k(wr + 16 * m + r16, 4 * kk + rl)));
+#pragma unroll
+        for (int c = 0; c < kC; ++c) acc[m][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(y[c], x, acc[m][c], 0, 0, 0);
+      }
+    }
+    slot = slot + 1 == kSlots ? 0 : slot + 1;
+  }
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // nothing is loaded into LDS past the block's end
+#pragma unroll
+  for (int m = 0; m < kR; ++m) {
+    const int t = wr + 16 * m + r16;
+    if (t >= n_act) continue;
+#pragma unroll
+    for (int c = 0; c < kC; ++c)
+      *reinterpret_cast<float4*>(part + (size_t)t * a.H + 16 * c) =
+          make_float4(acc[m][c][0], acc[m][c][1], acc[m][c][2], acc[m][c][3]);
+  }
+}
+
+// grad_W of up to 64 kKB rows: a block takes a chunk of 128 vocabulary rows
+// and all of H, 128 columns at a time; its four waves take 64 x 64 of that
+// each.  dz's fragments are read once, through LDS, and stay in registers
+// (32 kKB of them); h comes in stages of 64 rows x 128 columns, two LDS slots.
+// Several blocks per compute unit overlap one's stores with another's loads
+// and MFMAs.  The same chains as gradw_tile (rows ascending).
+// A lane's columns of an MFMA block are free to choose, four by four.  For a
+// bf16 grad_W block n of a wave's four takes, in lanes r = l / 16, columns
+// 32 (n / 2) + 8 r + 4 (n % 2) .. + 3: two blocks make 8 consecutive columns
+// of a lane and 32 (64 bytes) of a row's four lanes, one store.
+// LDS: rows (k) of 256 bytes, their 32-byte units xor-ed with
+// (row & 3) + 4 (row >> 3 & 1), as in mn_pos; with the columns so chosen h's
+// 64-byte units with row & 3 instead (two lanes then meet at a bank, the
+// least there is: each lane of a pass reads the same half of a piece).
+struct FewGradWArgs {
+  const uint16_t* dZ;
+  const uint16_t* hA;  // zero rows past the active ones, to a multiple of 64 at least
+  const int32_t* n_act;  // <= 64 kKB
+  int H;
+  SplitGeom gm;
+  BwdGeom bg;
+  void* grad_W;
+};
+
+template <int kKB, bool kBf16>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2))) void few_grad_w(FewGradWArgs a) {
+  constexpr uint32_t kTile = 64 * 256;
+  __shared__ u32x4 lds[2 * kTile / 16];
+  const int s = blockIdx.x / a.gm.cps, j = blockIdx.x - s * a.gm.cps;
+  const int sbeg = (a.bg.c_lo + s) * a.gm.S, v0 = kChunk * j;
+  const int rows = min(kChunk, min(a.gm.S, a.gm.V - sbeg) - v0);  // vocabulary rows of the chunk
+  if (rows <= 0) return;
+  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int r16 = lane & 15, rl = lane >> 4, wv = 64 * (w & 1), wc = 64 * (w >> 1);
+  const int n_act = __builtin_amdgcn_readfirstlane(*a.n_act);
+  const int kb = (n_act + 63) / 64;  // k-blocks (none: grad_W is zero)
+  const uint32_t lds0 = lds_addr(lds);
+  // direct loads: k-rows 16 w + 4 i + lane / 16 of a 64-row tile, piece lane % 16
+  uint32_t dz_off[4], h_off[4];
+  int h_piece[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int row = 16 * w + 4 * i + rl, p = r16;
+    const int f = (row & 3) | ((row >> 1) & 4);
+    const int pd = (((p >> 1) ^ f) << 1) | (p & 1);
+    dz_off[i] = 2u * ((uint32_t)row * (uint32_t)a.bg.ldz + (uint32_t)min(v0 + 8 * pd, a.bg.S_pad - 8));
+    h_off[i] = 2u * (uint32_t)row * (uint32_t)a.H;
+    h_piece[i] = kBf16 ? p ^ ((row & 3) << 2) : pd;
+  }
+  const char* dz = reinterpret_cast<const char*>(a.dZ + (size_t)s * a.bg.S_pad);
+  const char* hb = reinterpret_cast<const char*>(a.hA);
+  // this lane's fragments: k-row 8 rl + r16 / 4, k step kk 32 rows further
+  const int krow = 8 * rl + (r16 >> 2), q4 = r16 & 3, f_row = (krow & 3) | ((krow >> 1) & 4);
+  bf16x8 x[kKB][2][4];
+#pragma unroll
+  for (int k = 0; k < kKB; ++k) {
+    if (k < kb) {
+      const uint32_t slot = lds0 + kTile * (k & 1);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) dma16(dz + (size_t)k * 128 * a.bg.ldz, dz_off[i], slot + 1024u * (4 * w + i));
+      loads_then_barrier<0>();
+#pragma unroll
+      for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+          const uint32_t at = 256u * (krow + 32 * kk) + 32u * (((wv >> 4) + m) ^ f_row) + 8u * q4;
+          x[k][kk][m] = tr_frag(reinterpret_cast<const char*>(lds) + kTile * (k & 1) + at, 256u * 4);
+        }
+    } else {
+#pragma unroll
+      for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+        for (int m = 0; m < 4; ++m) x[k][kk][m] = bf16x8{};
+    }
+  }
+  loads_then_barrier<0>();  // every wave has its fragments: the slots are free
+  const int steps = (a.H + 127) / 128;
+  int l_n = 0, l_k = 0;
+  const auto load = [&](uint32_t slot) {
+    const char* base = hb + (size_t)l_k * 128 * a.H;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      dma16(base, h_off[i] + 2u * (uint32_t)min(128 * l_n + 8 * h_piece[i], a.H - 8), slot + 1024u * (4 * w + i));
+    if (++l_k >= kb) {
+      l_k = 0;
+      if (l_n + 1 < steps) ++l_n;
+    }
+  };
+  load(lds0);
+  using Out = std::conditional_t<kBf16, uint16_t, float>;
+  Out* out = reinterpret_cast<Out*>(a.grad_W) + (size_t)(sbeg + v0) * a.H;
+  uint32_t slot = 0;
+#pragma unroll 1
+  for (int n = 0; n < steps; ++n) {
+    AccBlk acc[4][4];
+#pragma unroll
+    for (int m = 0; m < 4; ++m)
+#pragma unroll
+      for (int b = 0; b < 4; ++b) acc[m][b] = AccBlk{};
+#pragma unroll
+    for (int k = 0; k < kKB; ++k) {
+      if (k >= kb) break;
+      loads_then_barrier<0>();
+      load(lds0 + (slot ^ kTile));
+      const char* th = reinterpret_cast<const char*>(lds) + slot;
+#pragma unroll
+      for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+          // this lane's four columns of block b, k-row krow
+          const int c64 = wc >> 6;
+          const uint32_t in_row = kBf16 ? 16u * ((8 * c64 + 4 * (b >> 1) + q4) ^ ((krow & 3) << 2)) + 8u * (b & 1)
+                                        : 32u * ((4 * c64 + b) ^ f_row) + 8u * q4;
+          const bf16x8 y = tr_frag(th + 256u * (krow + 32 * kk) + in_row, 256u * 4);
+#pragma unroll
+          for (int m = 0; m < 4; ++m)
+            acc[m][b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(y, x[k][kk][m], acc[m][b], 0, 0, 0);
+        }
+      slot ^= kTile;
+    }
+    const int c0 = 128 * n + wc;
+    if (c0 >= a.H) continue;  // (H % 128 == 64: the last step's second half)
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+      const int v = wv + 16 * m + r16;
+      if (v >= rows) continue;
+      if constexpr (kBf16) {
+        Out* to = out + (size_t)v * a.H + c0 + 8 * rl;
+#pragma unroll
+        for (int b = 0; b < 4; b += 2)
+          *reinterpret_cast<u32x4*>(to + 16 * b) =
+              u32x4{pack_bf16x2(acc[m][b][0], acc[m][b][1]), pack_bf16x2(acc[m][b][2], acc[m][b][3]),
+                    pack_bf16x2(acc[m][b + 1][0], acc[m][b + 1][1]), pack_bf16x2(acc[m][b + 1][2], acc[m][b + 1][3])};
+      } else {
+        Out* to = out + (size_t)v * a.H + c0 + 4 * rl;
+#pragma unroll
+        for (int b = 0; b < 4; ++b)
+          *reinterpret_cast<float4*>(to + 16 * b) = make_float4(acc[m][b][0], acc[m][b][1], acc[m][b][2], acc[m][b][3]);
+      }
+    }
+  }
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // nothing is loaded into LDS past the block's end
+}
+#endif  // RLK_MFMA == 16
+
 // grad_h[idx[i]] = the parts' sum, left to right, rounded to bf16 once; zero
-// rows for inactive rows.  Block b takes active row b and row b of the batch.
+// rows for inactive rows.  Block b takes active row b and row b of the batch
+// (idx NULL: they are the same).
 __global__ __launch_bounds__(256) void grad_h_sum(const float* __restrict__ part, size_t part_stride, int parts,
                                                   const int32_t* __restrict__ idx,
                                                   const int32_t* __restrict__ n_act_p, const int32_t* __restrict__ act,
                                                   int ignore_index, int T, int H, uint16_t* __restrict__ grad_h) {
   const int n_act = *n_act_p;
   for (int i = blockIdx.x; i < T; i += gridDim.x) {
-    if (act[i] == ignore_index)
+    const bool off = act[i] == ignore_index;
+    if (off)
       for (int c = 4 * threadIdx.x; c < H; c += 1024)
         *reinterpret_cast<uint2*>(grad_h + (size_t)i * H + c) = make_uint2(0u, 0u);
-    if (i >= n_act) continue;
-    uint16_t* out = grad_h + (size_t)idx[i] * H;
+    if (i >= n_act || (!idx && off)) continue;
+    uint16_t* out = grad_h + (size_t)(idx ? idx[i] : i) * H;
     for (int c = 4 * threadIdx.x; c < H; c += 1024) {
       const float* src = part + (size_t)i * H + c;
       float4 v[kParts];

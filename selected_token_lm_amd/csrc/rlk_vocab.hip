@@ -45,6 +45,15 @@ struct Pieces {
 
 inline int64_t padded_rows(int64_t T) { return ceil_div(std::max<int64_t>(T, 1), rlk::kBM) * rlk::kBM; }
 
+// Few rows: every logit of the batch is kept (in fp32, within the budget).
+#if RLK_MFMA == 16
+inline int64_t few_ldz(int64_t V) { return rlk::kNSplit * geom_of(V).cps * rlk::kChunk; }
+inline bool few_rows(int64_t T, int64_t V) { return T <= kFewRows && 4 * T * few_ldz(V) <= dz_budget_bytes(); }
+#else
+inline int64_t few_ldz(int64_t) { return 0; }
+inline bool few_rows(int64_t, int64_t) { return false; }
+#endif
+
 // linear_logp_top, forward: G splits of logits at a time.
 struct TopFwdWs {
   size_t idx, yA, n_act, zt, hA, rec, rec_u, z, best, total;
@@ -70,14 +79,14 @@ inline TopFwdWs top_fwd_layout(int64_t T, int64_t H, int64_t V, int64_t K) {
   const size_t records = (size_t)rlk::kNSplit * g.cps * T;
   w.rec = p.take(sizeof(float2) * records);
   w.rec_u = p.take(sizeof(float) * records);
-  w.z = p.take(K > 0 ? sizeof(float) * (size_t)T * w.ldz : 0);
+  w.z = p.take(K > 0 || few_rows(T, V) ? sizeof(float) * (size_t)T * w.ldz : 0);
   w.best = p.take(w.G < rlk::kNSplit ? sizeof(uint64_t) * (size_t)T * K : 0);
   w.total = p.total;
   return w;
 }
 
 struct DistillFwdWs {
-  size_t act, idx, n_act, hA, rec, off, ent, z_ids, total;
+  size_t act, idx, n_act, hA, rec, off, ent, z_ids, z, total;
   int64_t T_pad;
 };
 
@@ -91,9 +100,10 @@ inline DistillFwdWs distill_fwd_layout(int64_t T, int64_t H, int64_t V, int64_t 
   w.n_act = p.take(sizeof(int32_t));
   w.hA = p.take(2 * (size_t)w.T_pad * H);
   w.rec = p.take(sizeof(float2) * (size_t)rlk::kNSplit * g.cps * T);
-  w.off = p.take(sizeof(int32_t) * (size_t)(w.T_pad / rlk::kBM) * (rlk::kNSplit * ceil_div(g.S, rlk::kBN) + 1));
+  w.off = p.take(sizeof(int32_t) * (size_t)(w.T_pad / kBucketRows) * (rlk::kNSplit * ceil_div(g.S, rlk::kBN) + 1));
   w.ent = p.take(sizeof(uint32_t) * (size_t)w.T_pad * K);
   w.z_ids = p.take(sizeof(float) * (size_t)T * K);
+  w.z = p.take(few_rows(T, V) ? sizeof(float) * (size_t)T * few_ldz(V) : 0);
   w.total = p.total;
   return w;
 }
@@ -175,6 +185,36 @@ inline rlk_status compact(hipStream_t st, const int32_t* y, int64_t T, int32_t i
 
 inline dim3 row_grid(int64_t rows) { return dim3((unsigned)std::min(rows, kRowBlocks)); }
 
+#if RLK_MFMA == 16
+template <bool kTop, bool kDz>
+rlk_status launch_few(const FewArgs& a, int64_t blocks, hipStream_t st) {
+  typedef void (*Fn)(FewArgs);
+  static constexpr Fn fns[3] = {few_tiles<kTop, kDz, 0>, few_tiles<kTop, kDz, 1>, few_tiles<kTop, kDz, 2>};
+  const int f = few_shape(a.T);
+  RLK_LAUNCH_FN(kDz ? "few_tiles (dz)" : "few_tiles", fns[f], dim3((unsigned)blocks), dim3(64), st, a);
+  return RLK_OK;
+}
+
+// The logits, and chunk statistics, of a few rows.
+template <bool kTop>
+rlk_status few_logits(const void* h, const void* W, int64_t T, int64_t H, int64_t V, float scale, float2* rec,
+                      float* rec_u, float* z, hipStream_t st) {
+  FewArgs a{};
+  a.h = static_cast<const uint16_t*>(h);
+  a.W = static_cast<const uint16_t*>(W);
+  a.T = (int)T;
+  a.H = (int)H;
+  a.gm = split_geom(V);
+  a.scale = scale;
+  a.rec_stride = (size_t)T;
+  a.rec = rec;
+  a.rec_u = rec_u;
+  a.z = z;
+  a.ldz = few_ldz(V);
+  return launch_few<kTop, false>(a, (int64_t)(last_split(a.gm) + 1) * a.gm.cps, st);
+}
+#endif
+
 rlk_status run_top_fwd(const void* h, const void* W, const int32_t* y, int64_t T, int64_t H, int64_t V, int32_t ignore,
                        int64_t K, float* logp, float* lse, float* entropy, float* top_logp, int32_t* top_ids, void* ws,
                        hipStream_t st) {
@@ -187,6 +227,34 @@ rlk_status run_top_fwd(const void* h, const void* W, const int32_t* y, int64_t T
   la.tg.tps = (int)ceil_div(la.gm.S, rlk::kBN);
   const int64_t blocks = 8 * ceil_div(ceil_div(T, rlk::kBM) * L.G * la.tg.tps, 8);
   RLK_TRY(check_grid(blocks));
+  TopMergeArgs ma{};
+  ma.rec = at<float2>(ws, L.rec);
+  ma.rec_u = at<float>(ws, L.rec_u);
+  ma.rec_stride = (size_t)T;
+  ma.T = (int)T;
+  ma.ignore_index = ignore;
+  ma.y = y;
+  ma.gm = la.gm;
+  ma.G = (int)L.G;
+  ma.first = ma.last = 1;
+  ma.R = (int)ceil_div(la.gm.cps, 2 * kSelPer);
+  ma.z = at<float>(ws, L.z);
+  ma.ldz = L.ldz;
+  ma.K = (int)K;
+  ma.best = at<uint64_t>(ws, L.best);
+  ma.logp = logp;
+  ma.lse = lse;
+  ma.entropy = entropy;
+  ma.top_logp = top_logp;
+  ma.top_ids = top_ids;
+  const dim3 merge_grid((unsigned)(8 * ceil_div(T, 8)));
+#if RLK_MFMA == 16
+  if (few_rows(T, V)) {
+    RLK_TRY(few_logits<true>(h, W, T, H, V, 1.f, at<float2>(ws, L.rec), at<float>(ws, L.rec_u), at<float>(ws, L.z), st));
+    RLK_LAUNCH_V(top_merge, merge_grid, dim3(64), st, ma);
+    return RLK_OK;
+  }
+#endif
   RLK_TRY(compact(st, y, T, ignore, idx, yA, n_act, logp, lse, entropy));
   GatherArgs ga{};
   ga.h = static_cast<const uint16_t*>(h);
@@ -214,25 +282,9 @@ rlk_status run_top_fwd(const void* h, const void* W, const int32_t* y, int64_t T
   la.rec_u = at<float>(ws, L.rec_u);
   la.z = K > 0 ? at<float>(ws, L.z) : nullptr;
   la.ldz = L.ldz;
-  TopMergeArgs ma{};
-  ma.rec = la.rec;
-  ma.rec_u = la.rec_u;
-  ma.rec_stride = la.rec_stride;
   ma.zt = la.zt;
   ma.idx = idx;
   ma.n_act = n_act;
-  ma.y = y;
-  ma.G = (int)L.G;
-  ma.R = (int)ceil_div(la.gm.cps, 2 * kSelPer);
-  ma.z = la.z;
-  ma.ldz = L.ldz;
-  ma.K = (int)K;
-  ma.best = at<uint64_t>(ws, L.best);
-  ma.logp = logp;
-  ma.lse = lse;
-  ma.entropy = entropy;
-  ma.top_logp = top_logp;
-  ma.top_ids = top_ids;
   const int last = last_split(la.gm);
   for (int c = 0; c <= last; c += (int)L.G) {
     la.gm.s0 = c;
@@ -240,7 +292,7 @@ rlk_status run_top_fwd(const void* h, const void* W, const int32_t* y, int64_t T
     ma.gm = la.gm;
     ma.first = c == 0;
     ma.last = c + L.G > last;
-    RLK_LAUNCH_V(top_merge, dim3((unsigned)(8 * ceil_div(T, 8))), dim3(64), st, ma);
+    RLK_LAUNCH_V(top_merge, merge_grid, dim3(64), st, ma);
   }
   return RLK_OK;
 }
@@ -258,6 +310,28 @@ rlk_status run_distill_fwd(const void* h, const void* W, const int32_t* ids, con
   const int64_t row_tiles = ceil_div(T, rlk::kBM);
   const int64_t blocks = 8 * ceil_div(row_tiles * rlk::kNSplit * la.tg.tps, 8);
   RLK_TRY(check_grid(blocks));
+  DistillMergeArgs ma{};
+  ma.rec = at<float2>(ws, L.rec);
+  ma.rec_stride = (size_t)T;
+  ma.gm = la.gm;
+  ma.K = (int)K;
+  ma.T = (int)T;
+  ma.scale = scale;
+  ma.ids = ids;
+  ma.logits = logits;
+  ma.loss = loss;
+  ma.lse = lse;
+  ma.logp_ids = logp_ids;
+  const dim3 merge_grid((unsigned)(8 * ceil_div(T, 8)));
+#if RLK_MFMA == 16
+  if (few_rows(T, V)) {
+    ma.z = at<float>(ws, L.z);
+    ma.ldz = few_ldz(V);
+    RLK_TRY(few_logits<false>(h, W, T, H, V, scale, at<float2>(ws, L.rec), nullptr, at<float>(ws, L.z), st));
+    RLK_LAUNCH_V(distill_merge, merge_grid, dim3(64), st, ma);
+    return RLK_OK;
+  }
+#endif
   RLK_LAUNCH_V(distill_rows, row_grid(ceil_div(T, 4)), dim3(256), st, ids, logits, (int)T, (int)K, (int)V, scale, act,
                nullptr);
   RLK_TRY(compact(st, act, T, -100, idx, nullptr, n_act, loss, lse, nullptr));
@@ -276,8 +350,9 @@ rlk_status run_distill_fwd(const void* h, const void* W, const int32_t* ids, con
   RLK_LAUNCH_V(gather_rows_fill, row_grid(L.T_pad), dim3(256), st, ga);
   la.ent_off = at<int32_t>(ws, L.off);
   la.ent = at<uint32_t>(ws, L.ent);
-  RLK_LAUNCH_V(bucket_entries, dim3((unsigned)row_tiles), dim3(kBucketThreads), st, ids, logits, idx, n_act, (int)K,
-               la.gm, la.tg.tps, at<int32_t>(ws, L.off), at<uint32_t>(ws, L.ent));
+  const auto bucket = rlk::kNSplit * la.tg.tps <= 4096 ? rlk::vocab::bucket_entries<4096> : rlk::vocab::bucket_entries<kMaxVTiles>;
+  RLK_LAUNCH_FN("bucket_entries", bucket, dim3((unsigned)ceil_div(T, kBucketRows)), dim3(kBucketThreads), st, ids, logits,
+                idx, n_act, (int)K, la.gm, la.tg.tps, at<int32_t>(ws, L.off), at<uint32_t>(ws, L.ent));
   la.hA = ga.hA;
   la.W = static_cast<const uint16_t*>(W);
   la.n_act = n_act;
@@ -289,23 +364,38 @@ rlk_status run_distill_fwd(const void* h, const void* W, const int32_t* ids, con
   la.K = (int)K;
   la.z_ids = at<float>(ws, L.z_ids);
   RLK_LAUNCH_FN("logit_tiles", (rlk::vocab::logit_tiles<false>), dim3((unsigned)blocks), dim3(rlk::kThreads), st, la);
-  DistillMergeArgs ma{};
-  ma.rec = la.rec;
-  ma.rec_stride = la.rec_stride;
   ma.idx = idx;
   ma.n_act = n_act;
-  ma.gm = la.gm;
-  ma.K = (int)K;
-  ma.scale = scale;
-  ma.ids = ids;
-  ma.logits = logits;
   ma.z_ids = la.z_ids;
-  ma.loss = loss;
-  ma.lse = lse;
-  ma.logp_ids = logp_ids;
-  RLK_LAUNCH_V(distill_merge, dim3((unsigned)(8 * ceil_div(T, 8))), dim3(64), st, ma);
+  RLK_LAUNCH_V(distill_merge, merge_grid, dim3(64), st, ma);
   return RLK_OK;
 }
+
+#if RLK_MFMA == 16
+// Both gradients in their few-row kernels up to kFewGrad rows: 0.66 ms
+// together at 128 rows (H = 4096, V = 151936) against the tiles' 0.94; of 256
+// rows 1.09 against 0.95.
+constexpr int64_t kFewGrad = 128;
+rlk_status launch_few_grad_h(const FewGradHArgs& a, int64_t T, bool cont, hipStream_t st) {
+  typedef void (*Fn)(FewGradHArgs);
+  static constexpr Fn fns[2][4] = {
+      {few_grad_h<1, false>, few_grad_h<2, false>, few_grad_h<4, false>, few_grad_h<8, false>},
+      {few_grad_h<1, true>, few_grad_h<2, true>, few_grad_h<4, true>, few_grad_h<8, true>}};
+  const int64_t blocks = 8 * ceil_div(a.H / 64 * a.parts, 8);
+  int f = 0;
+  while ((int64_t)16 << f < T) ++f;
+  RLK_LAUNCH_FN("few_grad_h", fns[cont][f], dim3((unsigned)blocks), dim3(256), st, a);
+  return RLK_OK;
+}
+
+rlk_status launch_few_grad_w(const FewGradWArgs& a, int64_t T, bool bf16, int64_t blocks, hipStream_t st) {
+  typedef void (*Fn)(FewGradWArgs);
+  static constexpr Fn fns[2][2] = {{few_grad_w<1, false>, few_grad_w<2, false>},
+                                   {few_grad_w<1, true>, few_grad_w<2, true>}};
+  RLK_LAUNCH_FN("few_grad_w", fns[bf16][T <= 64 ? 0 : 1], dim3((unsigned)blocks), dim3(256), st, a);
+  return RLK_OK;
+}
+#endif
 
 // What the two backwards have in common: gradients of dz in groups of
 // splits; `act` marks the inactive rows with `ignore`.  ids != NULL: distill.
@@ -339,7 +429,13 @@ rlk_status run_soft_bwd(const SoftBwd& b, const SoftBwdWs& L, void* ws, hipStrea
   if (!top)
     RLK_LAUNCH_V(distill_rows, row_grid(ceil_div(b.T, 4)), dim3(256), st, b.ids, b.logits, (int)b.T, (int)b.K,
                  (int)b.V, b.scale, at<int32_t>(ws, L.act), at<float>(ws, L.q));
-  RLK_TRY(compact(st, b.act, b.T, b.ignore, idx, nullptr, n_act, nullptr, nullptr, nullptr));
+#if RLK_MFMA == 16
+  const bool few = b.T <= kFewRows;
+#else
+  const bool few = false;
+#endif
+  if (few) idx = nullptr;  // the batch's rows in place
+  else RLK_TRY(compact(st, b.act, b.T, b.ignore, idx, nullptr, n_act, nullptr, nullptr, nullptr));
   GatherGradArgs ga{};
   ga.h = static_cast<const uint16_t*>(b.h);
   ga.idx = idx;
@@ -357,6 +453,16 @@ rlk_status run_soft_bwd(const SoftBwd& b, const SoftBwdWs& L, void* ws, hipStrea
   ga.g_entropy = b.g_entropy;
   ga.act = b.act;
   ga.scale = b.scale;
+#if RLK_MFMA == 16
+  const dim3 few_grid(kFewRows);
+  if (few && top)
+    RLK_LAUNCH_FN("few_rows_grad", (rlk::vocab::few_rows_grad<true>), few_grid, dim3(256), st, ga, (int)b.T, b.ignore,
+                  n_act);
+  else if (few)
+    RLK_LAUNCH_FN("few_rows_grad", (rlk::vocab::few_rows_grad<false>), few_grid, dim3(256), st, ga, (int)b.T, b.ignore,
+                  n_act);
+  else
+#endif
   if (top)
     RLK_LAUNCH_FN("gather_rows_grad", (rlk::vocab::gather_rows_grad<true>), row_grid(L.T_pad), dim3(256), st, ga);
   else
@@ -382,10 +488,29 @@ rlk_status run_soft_bwd(const SoftBwd& b, const SoftBwdWs& L, void* ws, hipStrea
     da.bg = bg;
     da.dZ = at<uint16_t>(ws, L.dZ);
     const dim3 grid((unsigned)dz_blocks), block(rlk::kThreads);
-    if (top) {
+#if RLK_MFMA == 16
+    if (few) {
+      FewArgs fa{};
+      fa.h = ga.h;
+      fa.W = da.W;
+      fa.T = (int)b.T;
+      fa.H = (int)b.H;
+      fa.gm = gm;
+      fa.gm.s0 = c;
+      fa.scale = b.scale;
+      fa.rowinfo = ga.rowinfo;
+      fa.rowg = ga.rowg;
+      fa.bg = bg;
+      fa.dZ = da.dZ;
+      if (top) RLK_TRY((launch_few<true, true>(fa, (int64_t)G * gm.cps, st)));
+      else RLK_TRY((launch_few<false, true>(fa, (int64_t)G * gm.cps, st)));
+    } else
+#endif
+    if (top)
       RLK_LAUNCH_FN("soft_dz_tiles", (rlk::vocab::soft_dz_tiles<true>), grid, block, st, da);
-    } else {
+    else
       RLK_LAUNCH_FN("soft_dz_tiles", (rlk::vocab::soft_dz_tiles<false>), grid, block, st, da);
+    if (!top) {
       ScatterArgs sa{};
       sa.ids = b.ids;
       sa.q = at<float>(ws, L.q);
@@ -421,8 +546,38 @@ rlk_status run_soft_bwd(const SoftBwd& b, const SoftBwdWs& L, void* ws, hipStrea
     ha.parts = std::min(group_parts, last / kPartSplits + 1 - ha.part0);
     ha.part = b.grad_h ? part : nullptr;
     ha.part_stride = (size_t)b.T * b.H;
-    const dim3 gg((unsigned)(gh_blocks + gw_blocks));
     const bool cont = c % kPartSplits != 0;
+#if RLK_MFMA == 16
+    if (b.grad_h && b.T <= kFewGrad) {
+      FewGradHArgs fh{};
+      fh.dZ = da.dZ;
+      fh.W = da.W;
+      fh.n_act = n_act;
+      fh.H = (int)b.H;
+      fh.gm = gm;
+      fh.bg = bg;
+      fh.part0 = ha.part0;
+      fh.parts = ha.parts;
+      fh.part = part;
+      fh.part_stride = ha.part_stride;
+      RLK_TRY(launch_few_grad_h(fh, b.T, cont, st));
+      ha.part = nullptr;
+    }
+    if (b.grad_W && b.T <= kFewGrad) {
+      FewGradWArgs fw{};
+      fw.dZ = da.dZ;
+      fw.hA = ga.hA;
+      fw.n_act = n_act;
+      fw.H = (int)b.H;
+      fw.gm = gm;
+      fw.bg = bg;
+      fw.grad_W = b.grad_W;
+      RLK_TRY(launch_few_grad_w(fw, b.T, b.dtype == RLK_DT_BF16, (int64_t)G * gm.cps, st));
+      wa.grad_W = nullptr;
+    }
+    if (!ha.part && !wa.grad_W) continue;
+#endif
+    const dim3 gg((unsigned)((ha.part ? gh_blocks : 0) + (wa.grad_W ? gw_blocks : 0)));
     if (b.dtype == RLK_DT_BF16) {
       if (cont) RLK_LAUNCH_FN("part_grad_tiles", (rlk::vocab::part_grad_tiles<true, true>), gg, block, st, ha, wa);
       else RLK_LAUNCH_FN("part_grad_tiles", (rlk::vocab::part_grad_tiles<true, false>), gg, block, st, ha, wa);

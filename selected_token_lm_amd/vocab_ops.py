@@ -16,6 +16,7 @@ which mark empty slots.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 
 import torch
@@ -42,6 +43,15 @@ SIGNATURES = {
 def vocab_workspace_bytes(op: int, T: int, H: int, V: int, K: int) -> int:
     """Workspace bytes of one of the operators (VOP_*); 0 for invalid sizes."""
     return int(lib().rlk_vocab_workspace_bytes(op, T, H, V, K))
+
+
+_SAME = contextlib.nullcontext()
+
+
+def _on(device):
+    """`device` as the current one (the library works on the current device's
+    stream); free where it already is."""
+    return _SAME if device.index == torch.cuda.current_device() else torch.cuda.device(device)
 
 
 def _ws(ws, op, T, H, V, K, device):
@@ -83,12 +93,16 @@ def _slot_values(T, K, device, **named):
 
 
 def _head(h, W):
-    """_prep without targets."""
-    if h.dim() != 2:
+    """The checks of _prep for h and W alone."""
+    if h.dtype != torch.bfloat16 or W.dtype != torch.bfloat16:
+        raise TypeError("h and W must be bfloat16")
+    if h.dim() != 2 or W.dim() != 2 or h.shape[1] != W.shape[1]:
         raise ValueError("h must be [T, H] and W [V, H]")
-    rows = torch.empty(h.shape[0], dtype=torch.int32, device=h.device)
-    h, W, _ = _prep(h, W, rows)
-    return h, W
+    if not (h.is_cuda and W.is_cuda):
+        raise ValueError("h and W must be device tensors")
+    if W.device != h.device:
+        raise ValueError("h and W must be on one device")
+    return h.contiguous(), W.contiguous()
 
 
 def _grads(h, W, need_grad_h, need_grad_W, grad_W_dtype):
@@ -113,7 +127,7 @@ def linear_logp_top_fwd(h, W, y, top_k: int, ignore_index: int = IGNORE_INDEX, w
     h, W, y = _prep(h, W, y)
     T, H = h.shape
     V = W.shape[0]
-    with torch.cuda.device(h.device):
+    with _on(h.device):
         logp, lse, entropy = (torch.empty(T, dtype=torch.float32, device=h.device) for _ in range(3))
         top_logp = torch.empty((T, top_k), dtype=torch.float32, device=h.device)
         top_ids = torch.empty((T, top_k), dtype=torch.int32, device=h.device)
@@ -135,7 +149,7 @@ def linear_logp_top_bwd(h, W, y, lse, entropy, g, g_entropy=None, ignore_index: 
     named = dict(lse=lse, entropy=entropy, g=g, g_entropy=g_entropy)
     named = {k: v for k, v in named.items() if v is not None or k in ("lse", "entropy")}
     rows = dict(zip(named, _rows(T, h.device, **named)))
-    with torch.cuda.device(h.device):
+    with _on(h.device):
         grad_h, grad_W, code = _grads(h, W, need_grad_h, need_grad_W, grad_W_dtype)
         ws, n = _ws(ws, VOP_TOP_BWD, T, H, V, 0, h.device)
         _check(lib().rlk_linear_logp_top_bwd(_ptr(h), _ptr(W), _ptr(y), _ptr(rows["lse"]), _ptr(rows["entropy"]),
@@ -157,7 +171,7 @@ def linear_distill_fwd(h, W, ids, logits, temperature: float = 1.0, ws=None):
     V = W.shape[0]
     ids, logits = _slots(T, h.device, ids, logits)
     K = ids.shape[1]
-    with torch.cuda.device(h.device):
+    with _on(h.device):
         loss, lse = (torch.empty(T, dtype=torch.float32, device=h.device) for _ in range(2))
         logp_ids = torch.empty((T, K), dtype=torch.float32, device=h.device)
         ws, n = _ws(ws, VOP_DISTILL_FWD, T, H, V, K, h.device)
@@ -177,7 +191,7 @@ def linear_distill_bwd(h, W, ids, logits, lse, logp_ids, g, temperature: float =
     K = ids.shape[1]
     lse, g = _rows(T, h.device, lse=lse, g=g)
     logp_ids, = _slot_values(T, K, h.device, logp_ids=logp_ids)
-    with torch.cuda.device(h.device):
+    with _on(h.device):
         grad_h, grad_W, code = _grads(h, W, need_grad_h, need_grad_W, grad_W_dtype)
         ws, n = _ws(ws, VOP_DISTILL_BWD, T, H, V, K, h.device)
         _check(lib().rlk_linear_distill_bwd(_ptr(h), _ptr(W), _ptr(ids), _ptr(logits), _ptr(lse), _ptr(logp_ids),

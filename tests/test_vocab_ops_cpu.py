@@ -144,6 +144,7 @@ def host_as_device(monkeypatch):
     """CPU tensors get past the checks of h and W; those of the other
     arguments must still fire first."""
     monkeypatch.setattr(vo, "_prep", lambda h, W, y: (h, W, y))
+    monkeypatch.setattr(vo, "_head", lambda h, W: (h, W))
 
 
 @pytest.mark.parametrize("bad", [-1, 129, 2.0, True, None])
