@@ -93,6 +93,7 @@ struct LogitArgs {
   const uint16_t* W;
   const int32_t* n_act;
   int H;
+  int cus;      // see tile_of_block
   int G;        // splits of this launch: [gm.s0, gm.s0 + G)
   SplitGeom gm;
   TileGeom tg;
@@ -112,6 +113,22 @@ struct LogitArgs {
   float* z_ids;            // [active row][K]
 };
 
+// Tile of block `bid` when n tiles run on `cus` compute units one at a time:
+// whole tiles for whole rounds; the tiles of a last round that would leave
+// half of the units idle are cut into their two 128-column halves (half = 0,
+// 1; -1: whole), which take half as long.  At up to 256 rows of V = 151936
+// that is 2.5 rounds instead of 3.  Waves of a half's other columns only load.
+__device__ __forceinline__ bool tile_of_block(int n, int cus, int bid, int& id, int& half) {
+  const int full = n / cus * cus, rest = n - full;
+  const bool cut = 2 * rest <= cus;
+  const int k = bid < full ? xcd_tile(full, bid) : xcd_tile(cut ? 2 * rest : rest, bid - full);
+  if (k < 0) return false;
+  const bool h = cut && bid >= full;
+  id = __builtin_amdgcn_readfirstlane(bid < full ? k : full + (cut ? k >> 1 : k));
+  half = __builtin_amdgcn_readfirstlane(h ? k & 1 : -1);
+  return true;
+}
+
 // Teacher's tokens are sorted in groups of kBucketRows rows (bucket_entries).
 constexpr int kBucketRows = 32;
 static_assert(kWaveRows % kBucketRows == 0 && kBucketRows % kBlk == 0, "a row group is whole row blocks of one wave");
@@ -126,17 +143,19 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(RLK_WA
   const int n_act = __builtin_amdgcn_readfirstlane(*a.n_act);
   const int rtiles = (n_act + kBM - 1) / kBM;
   const int C = a.G * a.tg.tps;
-  const int id = xcd_tile(rtiles * C, blockIdx.x);
-  if (id < 0) return;
+  int id, half;
+  if (!tile_of_block(rtiles * C, a.cus, blockIdx.x, id, half)) return;
   int rt, ct;
   grouped_tile(id, rtiles, rt, ct, C, row_group(rtiles));
+  rt = __builtin_amdgcn_readfirstlane(rt);  // (tile addresses derive from them)
+  ct = __builtin_amdgcn_readfirstlane(ct);
   const int i0 = rt * kBM;
-  const int sl = ct / a.tg.tps, j = ct - sl * a.tg.tps;
+  const int sl = __builtin_amdgcn_readfirstlane(ct / a.tg.tps), j = ct - sl * a.tg.tps;
   const int sbeg = (a.gm.s0 + sl) * a.gm.S;
   const int send = min(sbeg + a.gm.S, a.gm.V);
-  const int c0 = sbeg + j * kBN;
+  const int c0 = sbeg + j * kBN + kChunk * max(half, 0);
   if (c0 >= send) return;
-  const int c1 = min(c0 + kBN, send);
+  const int c1 = min(c0 + (half < 0 ? kBN : kChunk), send);
   const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), wm = wave_m(w),
             wn = wave_n(w);
   // this lane's rows' targets, loaded as in fwd_tiles
@@ -152,12 +171,16 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(RLK_WA
   const RowsK B = rows_k(a.W + (size_t)c0 * a.H, c1 - 1 - c0, a.H);
   Acc acc;
   acc_zero(acc);
-  gemm_kk<0>(A, B, a.H / kBK, acc, lds, load_rows);
+  if (half >= 0 && wn == 1) {
+    gemm256<false, false, 0>(A, B, a.H / kBK, acc, lds);
+    return;
+  }
+  gemm256<false, false>(A, B, a.H / kBK, acc, lds, load_rows);
 
   const int cc0 = c0 + kChunk * wn;  // this wave's chunk
   const int width = min(cc0 + kChunk, c1) - cc0;
   if (width <= 0) return;
-  const int jc = 2 * j + wn;  // its number in the split
+  const int ch = half < 0 ? wn : half, jc = 2 * j + ch;  // its number in the tile, in the split
   const int g = (a.gm.s0 + sl) * a.gm.cps + jc;
   int le = lane;  // an opaque copy, see fwd_tiles
   asm volatile("" : "+v"(le));
@@ -218,7 +241,7 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(RLK_WA
       for (int eb = e0; eb < e1; eb += 64) {
         const uint32_t x = eb + le < e1 ? ent[eb + le] : 0u;
         const int row = (x >> 8) & 255, col = x & 255;
-        const bool mine = eb + le < e1 && row / kBlk == kMI * wm + mi && (col >> 7) == wn;
+        const bool mine = eb + le < e1 && row / kBlk == kMI * wm + mi && (col >> 7) == ch;
         if (!__builtin_amdgcn_ballot_w64(mine)) continue;
         if (!staged) {
           stage();
@@ -1128,6 +1151,7 @@ struct SoftDzArgs {
   const float* rowg;      // g
   const int32_t* n_act;
   int H;
+  int cus;                // see tile_of_block
   float scale;
   SplitGeom gm;
   TileGeom tg;
@@ -1142,16 +1166,20 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(RLK_WA
   const int n_act = __builtin_amdgcn_readfirstlane(*a.n_act);
   const int rtiles = (n_act + kBM - 1) / kBM;
   const int C = a.bg.G * a.tg.tps;
-  const int id = xcd_tile(rtiles * C, blockIdx.x);
-  if (id < 0) return;
+  int id, half;
+  if (!tile_of_block(rtiles * C, a.cus, blockIdx.x, id, half)) return;
   int rt, ct;
   grouped_tile(id, rtiles, rt, ct, C, row_group(rtiles));
+  rt = __builtin_amdgcn_readfirstlane(rt);  // (tile addresses derive from them)
+  ct = __builtin_amdgcn_readfirstlane(ct);
   const int i0 = rt * kBM;
-  const int sc = ct / a.tg.tps, j = ct - sc * a.tg.tps;
+  const int sc = __builtin_amdgcn_readfirstlane(ct / a.tg.tps), j = ct - sc * a.tg.tps;
   const int sbeg = (a.bg.c_lo + sc) * a.gm.S;
   const int valid_s = max(0, min(a.gm.S, a.gm.V - sbeg));  // columns of this split
-  const int c0 = sbeg + j * kBN;
-  const int c1 = sbeg + min(j * kBN + kBN, valid_s);
+  const int t0 = j * kBN + kChunk * max(half, 0), t1 = t0 + (half < 0 ? kBN : kChunk);  // the tile's, in the split
+  if (t0 >= a.bg.S_pad) return;
+  const int c0 = sbeg + t0;
+  const int c1 = sbeg + min(t1, valid_s);
   const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), wm = wave_m(w),
             wn = wave_n(w);
   float4 ri[kMI];  // loaded as in dz_tiles
@@ -1159,69 +1187,72 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(RLK_WA
 #pragma unroll
     for (int mi = 0; mi < kTailRows; ++mi) ri[mi] = a.rowinfo[i0 + acc_row(wm, mi, lane)];
   };
+  // a tile past the vocabulary runs on W's first row and is written as zeros
+  const RowsK A = rows_k(a.hA + (size_t)i0 * a.H, kBM - 1, a.H);
+  const RowsK B = c0 < c1 ? rows_k(a.W + (size_t)c0 * a.H, c1 - 1 - c0, a.H) : rows_k(a.W, 0, a.H);
+  char* stage = reinterpret_cast<char*>(lds);
+  int le = lane;  // an opaque copy, see fwd_tiles
   Acc acc;
   acc_zero(acc);
-  {
-    // a tile past the vocabulary runs on W's first row and is written as zeros
-    const RowsK A = rows_k(a.hA + (size_t)i0 * a.H, kBM - 1, a.H);
-    const RowsK B = c0 < c1 ? rows_k(a.W + (size_t)c0 * a.H, c1 - 1 - c0, a.H) : rows_k(a.W, 0, a.H);
+  if (half >= 0 && wn == 1) {
+    gemm256<false, false, 0>(A, B, a.H / kBK, acc, lds);
+    asm volatile("" : "+v"(le));
+  } else {
     gemm256<false, false>(A, B, a.H / kBK, acc, lds, load_rows);
-  }
-  int le = lane;  // an opaque copy, see fwd_tiles
-  asm volatile("" : "+v"(le));
+    asm volatile("" : "+v"(le));
 #pragma unroll
-  for (int mi = kTailRows; mi < kMI; ++mi) ri[mi] = a.rowinfo[i0 + acc_row(wm, mi, le)];
-  uint16_t* dzs = a.dZ + (size_t)sc * a.bg.S_pad;
-  // staging in LDS as in dz_tiles: 256 rows x 512 bytes, 16-byte unit u of row r at r * 512 + 16 (u ^ (r & 31))
-  char* stage = reinterpret_cast<char*>(lds);
-  auto put = [&](int r, int c, const float (&d)[4]) {
-    const uint32_t off = 512u * r + 16u * ((c >> 3) ^ (r & 31)) + 8u * ((c >> 2) & 1);
-    *reinterpret_cast<uint2*>(stage + off) = make_uint2(pack_bf16x2(d[0], d[1]), pack_bf16x2(d[2], d[3]));
-  };
-  const auto share = [&](float z, const float4& r) { return minus_share<kTop>(kTop ? z : z * a.scale, r); };
-  const int wc0 = j * kBN + 128 * wn;  // first column of the wave within the split
-  const bool full = i0 + kWaveRows * wm + kWaveRows <= n_act && wc0 + 128 <= valid_s;
+    for (int mi = kTailRows; mi < kMI; ++mi) ri[mi] = a.rowinfo[i0 + acc_row(wm, mi, le)];
+    // staging in LDS as in dz_tiles: 256 rows x 512 bytes, 16-byte unit u of row r at r * 512 + 16 (u ^ (r & 31))
+    auto put = [&](int r, int c, const float (&d)[4]) {
+      const uint32_t off = 512u * r + 16u * ((c >> 3) ^ (r & 31)) + 8u * ((c >> 2) & 1);
+      *reinterpret_cast<uint2*>(stage + off) = make_uint2(pack_bf16x2(d[0], d[1]), pack_bf16x2(d[2], d[3]));
+    };
+    const auto share = [&](float z, const float4& r) { return minus_share<kTop>(kTop ? z : z * a.scale, r); };
+    const int wc0 = t0 + 128 * wn;  // first column of the wave within the split
+    const bool full = i0 + kWaveRows * wm + kWaveRows <= n_act && wc0 + 128 <= valid_s;
 #pragma unroll
-  for (int mi = 0; mi < kMI; ++mi) {
-    const int r = acc_row(wm, mi, le);
-    const bool rvalid = i0 + r < n_act;
-    const int yl = kTop ? __float_as_int(ri[mi].w) - sbeg : -1;  // target column within the split
-    const int tl = yl - wc0;
-    const bool hit = kTop && tl >= 0 && tl < 128 && ((tl >> 2) & (kLPR - 1)) == row_lane(le);
-    if (full && !__builtin_amdgcn_ballot_w64(hit)) {
+    for (int mi = 0; mi < kMI; ++mi) {
+      const int r = acc_row(wm, mi, le);
+      const bool rvalid = i0 + r < n_act;
+      const int yl = kTop ? __float_as_int(ri[mi].w) - sbeg : -1;  // target column within the split
+      const int tl = yl - wc0;
+      const bool hit = kTop && tl >= 0 && tl < 128 && ((tl >> 2) & (kLPR - 1)) == row_lane(le);
+      if (full && !__builtin_amdgcn_ballot_w64(hit)) {
 #pragma unroll
-      for (int ni = 0; ni < kNI; ++ni)
+        for (int ni = 0; ni < kNI; ++ni)
 #pragma unroll
-        for (int q = 0; q < kQL; ++q) {
-          float d[4];
+          for (int q = 0; q < kQL; ++q) {
+            float d[4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) d[e] = share(acc.c[mi][ni][4 * q + e], ri[mi]);
-          put(r, acc_col4(wn, ni, q, le), d);
-        }
-    } else {
-      const float g = kTop ? a.rowg[i0 + r] : 0.f;
-#pragma unroll
-      for (int ni = 0; ni < kNI; ++ni)
-#pragma unroll
-        for (int q = 0; q < kQL; ++q) {
-          if (j * kBN + 128 * wn + kBlk * ni + 4 * kLPR * q >= a.bg.S_pad) continue;  // never stored
-          const int c = acc_col4(wn, ni, q, le);
-          float d[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int vl = j * kBN + c + e;
-            const float x = share(acc.c[mi][ni][4 * q + e], ri[mi]);
-            d[e] = rvalid && vl < valid_s ? (kTop && vl == yl ? g + x : x) : 0.f;
+            for (int e = 0; e < 4; ++e) d[e] = share(acc.c[mi][ni][4 * q + e], ri[mi]);
+            put(r, acc_col4(wn, ni, q, le), d);
           }
-          put(r, c, d);
-        }
+      } else {
+        const float g = kTop ? a.rowg[i0 + r] : 0.f;
+#pragma unroll
+        for (int ni = 0; ni < kNI; ++ni)
+#pragma unroll
+          for (int q = 0; q < kQL; ++q) {
+            if (t0 + 128 * wn + kBlk * ni + 4 * kLPR * q >= a.bg.S_pad) continue;  // never stored
+            const int c = acc_col4(wn, ni, q, le);
+            float d[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int vl = t0 + c + e;
+              const float x = share(acc.c[mi][ni][4 * q + e], ri[mi]);
+              d[e] = rvalid && vl < valid_s ? (kTop && vl == yl ? g + x : x) : 0.f;
+            }
+            put(r, c, d);
+          }
+      }
     }
   }
   __syncthreads();
+  uint16_t* dzs = a.dZ + (size_t)sc * a.bg.S_pad;
   constexpr int kRowsW = kBM / kWaves;
   const int u = le & 31;
-  const int col = j * kBN + 8 * u;  // column within the split
-  if (col < a.bg.S_pad) {
+  const int col = t0 + 8 * u;  // column within the split
+  if (col < min(t1, a.bg.S_pad)) {
 #pragma unroll
     for (int it = 0; it < kRowsW / 2; ++it) {
       const int r = kRowsW * w + 2 * it + (le >> 5);
@@ -1283,18 +1314,18 @@ __global__ __launch_bounds__(kMaxK) void distill_scatter(ScatterArgs a) {
 // ---------------------------------------------------------------------------
 // Gradients of a group of splits.
 //
-// grad_h: the sum over the vocabulary is cut into kParts parts of
-// kPartSplits splits each, whatever the batch; a part's sum is one fp32 MFMA
+// grad_h: the sum over the vocabulary is cut into parts of `per` splits each
+// (part_splits: by H and V, whatever the batch); a part's sum is one fp32 MFMA
 // chain per element, vocabulary ascending (it continues across groups through
 // its place in `part`), and grad_h_sum adds the parts in order.  One chain
 // over the whole vocabulary leaves most compute units without a grad_h tile
 // where rows are few: at 257 rows, H = 4096, V = 151936 its tiles take 1.97
 // ms.  (linear_logp_bwd keeps the one chain: its bits are its contract.)
-// Four parts: both gradients of that batch in 0.98 ms, of 4096 rows (3482
-// active) in 6.63 ms with grad_h_sum; two parts 1.68 and 6.49, eight 0.99 and
-// 6.73 (the parts' sums pass through HBM).
+// Four parts there: both gradients of that batch in 0.98 ms, of 4096 rows
+// (3482 active) in 6.63 ms with grad_h_sum; two parts 1.68 and 6.49, eight
+// 0.99 and 6.73 (the parts' sums pass through HBM).
 // ---------------------------------------------------------------------------
-constexpr int kPartSplits = 8, kParts = kNSplit / kPartSplits;
+constexpr int kMaxParts = kNSplit;
 
 struct PartGradHArgs {
   const uint16_t* dZ;
@@ -1303,8 +1334,9 @@ struct PartGradHArgs {
   SplitGeom gm;
   BwdGeom bg;
   int n_tiles;         // 256-column tiles of H
+  int per;             // splits of a part
   int part0, parts;    // parts of the group: part0 .. part0 + parts - 1
-  float* part;         // [kParts][T][H], rows in active order; NULL: not wanted
+  float* part;         // [part][T][H], rows in active order; NULL: not wanted
   size_t part_stride;  // T * H
 };
 
@@ -1344,7 +1376,7 @@ __device__ __forceinline__ void gradh_part_tile(const PartGradHArgs& a, int id, 
   for (int mi = 0; mi < kMI; ++mi)
 #pragma unroll
     for (int ni = 0; ni < kNI; ++ni) asm volatile("" : "+a"(acc.c[mi][ni]));
-  const int s0 = q * kPartSplits, splits = min(kPartSplits, a.bg.G - s0);  // of the group
+  const int s0 = q * a.per, splits = min(a.per, a.bg.G - s0);  // of the group
   const RowsK A = rows_k(a.dZ + (size_t)i0 * a.bg.ldz + (size_t)s0 * a.bg.S_pad, kBM - 1, a.bg.ldz);
   WRowsMN B;
   B.base = reinterpret_cast<const char*>(a.W + n0);
@@ -1500,7 +1532,7 @@ struct FewGradHArgs {
   int H;
   SplitGeom gm;
   BwdGeom bg;
-  int part0, parts;
+  int per, part0, parts;
   float* part;         // as in PartGradHArgs
   size_t part_stride;
 };
@@ -1521,7 +1553,7 @@ __global__ __launch_bounds__(256) void few_grad_h(FewGradHArgs a) {
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r16 = lane & 15, rl = lane >> 4;
   const int wc = kC == 1 ? 16 * w : 32 * (w & 1), wr = kC == 1 ? 0 : 16 * kR * (w >> 1);  // first column, row
-  const int s0 = q * kPartSplits, splits = min(kPartSplits, a.bg.G - s0), kbps = a.bg.S_pad / kBK;
+  const int s0 = q * a.per, splits = min(a.per, a.bg.G - s0), kbps = a.bg.S_pad / kBK;
   const int nk = splits * kbps;
   // direct loads of this lane: W rows 16 w + 8 i + lane / 8, dz rows 8 (w + 4 i) + lane / 8
   uint32_t w_row[2], w_col[2], dz_off[kRows / 32];
@@ -1774,14 +1806,17 @@ __global__ __launch_bounds__(256) void grad_h_sum(const float* __restrict__ part
     uint16_t* out = grad_h + (size_t)(idx ? idx[i] : i) * H;
     for (int c = 4 * threadIdx.x; c < H; c += 1024) {
       const float* src = part + (size_t)i * H + c;
-      float4 v[kParts];
+      float4 s = *reinterpret_cast<const float4*>(src);
+      constexpr int kAhead = 4;
+      for (int q0 = 1; q0 < parts; q0 += kAhead) {
+        float4 v[kAhead];
 #pragma unroll
-      for (int q = 0; q < kParts; ++q)
-        if (q < parts) v[q] = *reinterpret_cast<const float4*>(src + q * part_stride);
-      float4 s = v[0];
+        for (int q = 0; q < kAhead; ++q)
+          if (q0 + q < parts) v[q] = *reinterpret_cast<const float4*>(src + (q0 + q) * part_stride);
 #pragma unroll
-      for (int q = 1; q < kParts; ++q)
-        if (q < parts) s = make_float4(s.x + v[q].x, s.y + v[q].y, s.z + v[q].z, s.w + v[q].w);
+        for (int q = 0; q < kAhead; ++q)
+          if (q0 + q < parts) s = make_float4(s.x + v[q].x, s.y + v[q].y, s.z + v[q].z, s.w + v[q].w);
+      }
       *reinterpret_cast<uint2*>(out + c) = make_uint2(pack_bf16x2(s.x, s.y), pack_bf16x2(s.z, s.w));
     }
   }

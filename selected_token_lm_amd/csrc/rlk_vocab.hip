@@ -108,6 +108,16 @@ inline DistillFwdWs distill_fwd_layout(int64_t T, int64_t H, int64_t V, int64_t 
   return w;
 }
 
+// Splits of one of grad_h's parts: 32 / parts.  Parts are work items, so
+// narrow heads want more of them (256 blocks of 64 columns: 4 parts at H =
+// 4096, 32 at 512); their sums cost P / V of the products' traffic, so small
+// vocabularies get no more than one per 4748 columns, four at least.
+int part_splits(int64_t H, int64_t V) {
+  int parts = 4;
+  while (parts < kMaxParts && 2 * parts * H <= 256 * 64 && 2 * parts * 4748 <= V) parts *= 2;
+  return rlk::kNSplit / parts;
+}
+
 // Both backwards: G splits of dz at a time, grad_h's parts, and (distill,
 // K > 0) the teacher's rows.
 struct SoftBwdWs {
@@ -128,7 +138,7 @@ inline SoftBwdWs soft_bwd_layout(int64_t T, int64_t H, int64_t V, int64_t K) {
   w.rowg = p.take(sizeof(float) * w.T_pad);
   w.hA = p.take(2 * (size_t)w.T_pad * H);
   w.dZ = p.take(2 * (size_t)w.T_pad * w.G * w.S_pad);
-  w.part = p.take(sizeof(float) * (size_t)kParts * T * H);
+  w.part = p.take(sizeof(float) * (size_t)(rlk::kNSplit / part_splits(H, V)) * T * H);
   w.act = p.take(K > 0 ? sizeof(int32_t) * T : 0);
   w.q = p.take(sizeof(float) * (size_t)T * K);
   w.total = p.total;
@@ -171,6 +181,11 @@ inline rlk::SplitGeom split_geom(int64_t V) {
 
 // The last split that holds columns.
 inline int last_split(const rlk::SplitGeom& gm) { return (gm.V - 1) / gm.S; }
+
+// Blocks for up to n tiles dealt by tile_of_block.
+inline int64_t tile_blocks(int64_t n, int cus) { return 8 * ceil_div(n + cus / 2, 8); }
+// (tile_of_block deals whole rounds to the dies: their units, a multiple of 8)
+inline int tile_units() { return device_cus() % 8 == 0 ? device_cus() : 8; }
 
 #define RLK_LAUNCH_V(kern, grid, block, st, ...) RLK_LAUNCH(vocab::kern, grid, block, st, __VA_ARGS__)
 
@@ -225,7 +240,8 @@ rlk_status run_top_fwd(const void* h, const void* W, const int32_t* y, int64_t T
   LogitArgs la{};
   la.gm = split_geom(V);
   la.tg.tps = (int)ceil_div(la.gm.S, rlk::kBN);
-  const int64_t blocks = 8 * ceil_div(ceil_div(T, rlk::kBM) * L.G * la.tg.tps, 8);
+  la.cus = tile_units();
+  const int64_t blocks = tile_blocks(ceil_div(T, rlk::kBM) * L.G * la.tg.tps, la.cus);
   RLK_TRY(check_grid(blocks));
   TopMergeArgs ma{};
   ma.rec = at<float2>(ws, L.rec);
@@ -308,7 +324,8 @@ rlk_status run_distill_fwd(const void* h, const void* W, const int32_t* ids, con
   la.gm = split_geom(V);
   la.tg.tps = (int)ceil_div(la.gm.S, rlk::kBN);
   const int64_t row_tiles = ceil_div(T, rlk::kBM);
-  const int64_t blocks = 8 * ceil_div(row_tiles * rlk::kNSplit * la.tg.tps, 8);
+  la.cus = tile_units();
+  const int64_t blocks = tile_blocks(row_tiles * rlk::kNSplit * la.tg.tps, la.cus);
   RLK_TRY(check_grid(blocks));
   DistillMergeArgs ma{};
   ma.rec = at<float2>(ws, L.rec);
@@ -420,8 +437,8 @@ rlk_status run_soft_bwd(const SoftBwd& b, const SoftBwdWs& L, void* ws, hipStrea
   const rlk::SplitGeom gm = split_geom(b.V);
   const int tps = (int)ceil_div(gm.S, rlk::kBN), n_tiles = (int)ceil_div(b.H, rlk::kBN), G = (int)L.G;
   const int64_t row_tiles = ceil_div(b.T, rlk::kBM);
-  const int64_t dz_blocks = 8 * ceil_div(row_tiles * G * tps, 8);
-  const int group_parts = (int)ceil_div(G, kPartSplits);
+  const int64_t dz_blocks = tile_blocks(row_tiles * G * tps, tile_units());
+  const int per = part_splits(b.H, b.V), group_parts = (int)ceil_div(G, per);
   const int64_t gh_blocks = b.grad_h ? 8 * ceil_div(row_tiles * n_tiles * group_parts, 8) : 0;
   const int64_t gw_blocks = b.grad_W ? 8 * ceil_div((int64_t)n_tiles * G * tps, 8) : 0;
   RLK_TRY(check_grid(dz_blocks));
@@ -482,6 +499,7 @@ rlk_status run_soft_bwd(const SoftBwd& b, const SoftBwdWs& L, void* ws, hipStrea
     da.rowg = ga.rowg;
     da.n_act = n_act;
     da.H = (int)b.H;
+    da.cus = tile_units();
     da.scale = b.scale;
     da.gm = gm;
     da.tg.tps = tps;
@@ -542,11 +560,12 @@ rlk_status run_soft_bwd(const SoftBwd& b, const SoftBwdWs& L, void* ws, hipStrea
     ha.gm = gm;
     ha.bg = bg;
     ha.n_tiles = n_tiles;
-    ha.part0 = c / kPartSplits;
-    ha.parts = std::min(group_parts, last / kPartSplits + 1 - ha.part0);
+    ha.per = per;
+    ha.part0 = c / per;
+    ha.parts = std::min(group_parts, last / per + 1 - ha.part0);
     ha.part = b.grad_h ? part : nullptr;
     ha.part_stride = (size_t)b.T * b.H;
-    const bool cont = c % kPartSplits != 0;
+    const bool cont = c % per != 0;
 #if RLK_MFMA == 16
     if (b.grad_h && b.T <= kFewGrad) {
       FewGradHArgs fh{};
@@ -556,6 +575,7 @@ rlk_status run_soft_bwd(const SoftBwd& b, const SoftBwdWs& L, void* ws, hipStrea
       fh.H = (int)b.H;
       fh.gm = gm;
       fh.bg = bg;
+      fh.per = per;
       fh.part0 = ha.part0;
       fh.parts = ha.parts;
       fh.part = part;
@@ -587,7 +607,7 @@ rlk_status run_soft_bwd(const SoftBwd& b, const SoftBwdWs& L, void* ws, hipStrea
     }
   }
   if (b.grad_h)
-    RLK_LAUNCH_V(grad_h_sum, row_grid(b.T), dim3(256), st, part, (size_t)b.T * b.H, last / kPartSplits + 1, idx, n_act,
+    RLK_LAUNCH_V(grad_h_sum, row_grid(b.T), dim3(256), st, part, (size_t)b.T * b.H, last / per + 1, idx, n_act,
                  b.act, b.ignore, (int)b.T, (int)b.H, static_cast<uint16_t*>(b.grad_h));
   return RLK_OK;
 }
