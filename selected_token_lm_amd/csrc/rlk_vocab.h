@@ -737,7 +737,7 @@ __global__ __launch_bounds__(kBucketThreads) void bucket_entries(const int32_t* 
 }
 
 // ---------------------------------------------------------------------------
-// Row kernels after the logits: one wave (a block) per row.  With one row
+// Row kernels after the logits: a block per row, of one wave or two.  With one row
 // they are latency alone, and most of that is instruction fetch: unrolled
 // forms of these loops, which run through their code once, took 54 us where
 // the rolled ones below take 17 (20 alternatives, V = 151936).  So loops stay
@@ -858,7 +858,7 @@ constexpr int kSelList = 512;              // keys of a row in LDS
 constexpr int kSelAhead = 16;              // chunks whose logits are loaded together
 static_assert(kSelList >= kMaxK + 64, "room for a step after a cut");
 static_assert(64 * kSelGroups >= kMaxK, "K groups");
-static_assert(kSelAhead * kChunk <= kSelRuns && kFoldFloats <= kSelRuns, "one LDS array serves all three");
+static_assert(kSelAhead * kChunk <= kSelRuns, "one LDS array serves both");
 
 __device__ __forceinline__ uint32_t ordered_bits(float x) {
   const uint32_t b = __float_as_uint(x + 0.f);
@@ -920,14 +920,20 @@ struct TopMergeArgs {
   int32_t* top_ids;
 };
 
-__global__ __launch_bounds__(64) void top_merge(TopMergeArgs a) {
-  __shared__ uint32_t pool[kSelRuns];  // run maxima; then logits; then the fold's records
+// Two waves a row: one picks the alternatives, the other folds the statistics
+// (after the last group); the first then needs m and log s of the second.
+__global__ __launch_bounds__(128) void top_merge(TopMergeArgs a) {
+  __shared__ uint32_t pool[kSelRuns];  // run maxima, then logits
   __shared__ uint64_t list[kSelList];
   __shared__ uint16_t picks[kSelRuns];
-  const int lane = threadIdx.x, i = xcd_tile(a.idx ? *a.n_act : a.T, blockIdx.x);
+  __shared__ float records[kFoldFloats];
+  __shared__ float m_s, log_s;
+  const int lane = threadIdx.x & 63, i = xcd_tile(a.idx ? *a.n_act : a.T, blockIdx.x);
+  const bool folds = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) == 1;
   if (i < 0) return;
   const int t = a.idx ? a.idx[i] : i, yt = a.y[t];
   if (!a.idx && yt == a.ignore_index) {
+    if (folds) return;
     if (lane == 0) {
       a.logp[t] = a.entropy[t] = 0.f;
       if (a.lse) a.lse[t] = 0.f;
@@ -936,6 +942,25 @@ __global__ __launch_bounds__(64) void top_merge(TopMergeArgs a) {
       a.top_ids[(size_t)t * a.K + k] = -1;
       a.top_logp[(size_t)t * a.K + k] = -INFINITY;
     }
+    return;
+  }
+  if (folds) {
+    if (!a.last) return;
+    const MSU tot = fold_row<true>(a.rec, a.rec_u, a.rec_stride, i, a.gm, records);
+    if (lane == 0) {
+      const float m = tot.m, L = rlk_log(tot.s);
+      float lp = __builtin_nanf("");
+      if (yt >= 0 && yt < a.gm.V) {
+        const float zt = a.zt ? a.zt[i] : a.z[(size_t)i * a.ldz + logit_at(a.gm, yt)];
+        lp = (zt - m) - L;
+      }
+      a.logp[t] = lp;
+      if (a.lse) a.lse[t] = m + L;
+      a.entropy[t] = L - tot.u / tot.s;
+      m_s = m;
+      log_s = L;
+    }
+    __syncthreads();
     return;
   }
   int n = 0;
@@ -1051,18 +1076,8 @@ __global__ __launch_bounds__(64) void top_merge(TopMergeArgs a) {
       for (int k = lane; k < a.K; k += 64) a.best[(size_t)i * a.K + k] = k < n ? list[k] : 0;
   }
   if (!a.last) return;
-  const MSU tot = fold_row<true>(a.rec, a.rec_u, a.rec_stride, i, a.gm, reinterpret_cast<float*>(pool));
-  const float m = __shfl(tot.m, 0), L = rlk_log(__shfl(tot.s, 0));
-  if (lane == 0) {
-    float lp = __builtin_nanf("");
-    if (yt >= 0 && yt < a.gm.V) {
-      const float zt = a.zt ? a.zt[i] : a.z[(size_t)i * a.ldz + logit_at(a.gm, yt)];
-      lp = (zt - m) - L;
-    }
-    a.logp[t] = lp;
-    if (a.lse) a.lse[t] = m + L;
-    a.entropy[t] = L - tot.u / tot.s;
-  }
+  __syncthreads();
+  const float m = m_s, L = log_s;
   for (int k = lane; k < a.K; k += 64) {
     const bool some = k < n;
     const uint64_t key = some ? list[k] : 0;

@@ -267,7 +267,7 @@ rlk_status run_top_fwd(const void* h, const void* W, const int32_t* y, int64_t T
 #if RLK_MFMA == 16
   if (few_rows(T, V)) {
     RLK_TRY(few_logits<true>(h, W, T, H, V, 1.f, at<float2>(ws, L.rec), at<float>(ws, L.rec_u), at<float>(ws, L.z), st));
-    RLK_LAUNCH_V(top_merge, merge_grid, dim3(64), st, ma);
+    RLK_LAUNCH_V(top_merge, merge_grid, dim3(128), st, ma);
     return RLK_OK;
   }
 #endif
@@ -308,7 +308,7 @@ rlk_status run_top_fwd(const void* h, const void* W, const int32_t* y, int64_t T
     ma.gm = la.gm;
     ma.first = c == 0;
     ma.last = c + L.G > last;
-    RLK_LAUNCH_V(top_merge, merge_grid, dim3(64), st, ma);
+    RLK_LAUNCH_V(top_merge, merge_grid, dim3(128), st, ma);
   }
   return RLK_OK;
 }
