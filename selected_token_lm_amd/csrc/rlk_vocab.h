@@ -290,25 +290,40 @@ __device__ __forceinline__ float minus_share(float z, const float4& r) {
 }
 
 #if RLK_MFMA == 16
+// Waves wait for their own direct loads, all but the n issued last, and then
+// for one another.
+template <int n>
+__device__ __forceinline__ void loads_then_barrier() {
+  asm volatile("s_waitcnt vmcnt(%0)" : : "n"(n) : "memory");
+  wait_lds();
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_sched_barrier(0);
+}
+
 // ---------------------------------------------------------------------------
 // Few rows (T <= kFewRows): the same logits, statistics and dz with W streamed
-// straight from HBM into registers.
+// through a ring of LDS stages.
 //
-// A tile of 256 rows reads W through LDS at one tile per compute unit; with
-// few rows its 608 tiles come in 2.4 rounds, and the last one half empty
-// costs a third of the time.  Here a wave, a block of its own, owns a chunk
-// of 128 columns and all rows: 1216 blocks, all of them resident at once.  W's fragments go from memory to the MFMA's registers,
-// a stage of 32 or 64 k ahead of the one in use; h's come from L2.  Every
-// logit is the engine's MFMA chain (k ascending in steps of 32) in the
-// engine's layout, so the statistics are the same bits.  Rows are those of
-// the batch, in place: no compaction.
+// With few rows the time is W's way from HBM, and that takes bytes in flight:
+// about 2.9 us of them at full rate.  The engine has one tile per compute unit
+// at a time, 1.5 k-blocks ahead, and gaps between tiles (256 rows of V =
+// 151936: 4.3 TB/s).  Here a block stays on its unit and walks over chunks of
+// 128 columns; two waves do nothing but issue the direct loads of stages
+// (64 k of the chunk's W rows and of h, kSlots of them, kSlots - 1 in flight:
+// 64 KB of W and more per unit) across the chunks' borders, and kC waves
+// consume them, 32 rows each, while the next stages arrive.  A barrier per
+// stage hands it over and its predecessor's slot back.  Every logit is the
+// engine's MFMA chain (k ascending in steps of 32) in the engine's layout, so
+// the statistics are the same bits.  Rows are those of the batch, in place: no
+// compaction.
 // ---------------------------------------------------------------------------
-constexpr int kFewRows = 64;
+constexpr int kFewRows = 128;
 
 struct FewArgs {
   const uint16_t* h;  // [T, H]
   const uint16_t* W;
   int T, H;
+  int chunks;  // of the launch: chunk c is chunk c % cps of split gm.s0 + c / cps
   SplitGeom gm;
   float scale;  // 1 / temperature; not applied by the kTop instances
   // logits
@@ -321,132 +336,179 @@ struct FewArgs {
   const float4* rowinfo;  // [kFewRows] as for soft_dz_tiles; target kNoRow: zeros
   const float* rowg;
   BwdGeom bg;
-  uint16_t* dZ;  // rows 0 .. kFewRows - 1 are written
+  uint16_t* dZ;  // rows up to T's multiple of 64 are written
 };
 
-struct FewShape {
-  int rb, steps;  // 16-row blocks, k steps of 32 of a stage
-};
-// up to 16, 32 and 64 rows.  A stage of 64 k asks for whole cache lines and
-// keeps 16 KB in flight per wave; at 64 rows only one of 32 k fits the
-// registers beside the accumulators.  us at H = 4096, V = 151936: 230 (1
-// row), 242 (32), 335 (64); with 64 columns a wave, three waves per SIMD, 237,
-// 270 and 392; with the 64 rows as two waves of 32, 465 to 500; non-temporal
-// loads of W 260, 310, 415; the 256-row tiles 300 for any.
-constexpr FewShape kFewShapes[3] = {{1, 2}, {2, 2}, {4, 1}};
-constexpr int few_shape(int64_t T) { return T <= 16 ? 0 : T <= 32 ? 1 : 2; }
+// Waves by consumers: 1, 2 or 4 for up to 32, 64 or 128 rows.
+constexpr int few_consumers(int64_t T) { return T <= 32 ? 1 : T <= 64 ? 2 : 4; }
+constexpr int few_threads(int consumers) { return 64 * (2 + consumers); }
 
-template <bool kTop, bool kDz, int kShape>
-__global__ __launch_bounds__(64) __attribute__((amdgpu_waves_per_eu(2))) void few_tiles(FewArgs a) {
-  constexpr int kRB = kFewShapes[kShape].rb, kSteps = kFewShapes[kShape].steps, kDepth = 2;
-  constexpr int kCB = kChunk / 16;
-  // block -> chunk j of split s (of the group, for dz)
-  const int s = blockIdx.x / a.gm.cps, j = blockIdx.x - s * a.gm.cps;
-  const int sbeg = (a.gm.s0 + s) * a.gm.S, valid_s = max(0, min(a.gm.S, a.gm.V - sbeg));
-  const int width = min(kChunk, valid_s - j * kChunk);  // columns of the chunk
-  if (!kDz && width <= 0) return;
-  const int lane = threadIdx.x, r16 = lane & 15, rl = lane >> 4;
-  float acc_v[kRB][kCB][4];
-  {
-    // lane l: row l % 16 of a block, k = 8 (l / 16) .. + 7 of a step
-    const int c0 = sbeg + j * kChunk, last = max(width, 1) - 1;
-    const char* wb = reinterpret_cast<const char*>(a.W + (size_t)(width > 0 ? c0 : 0) * a.H);
-    const char* hb = reinterpret_cast<const char*>(a.h);
-    uint32_t wo[kCB], ho[kRB];
+template <bool kTop, bool kDz, int kC>
+__global__ __launch_bounds__(few_threads(kC)) void few_tiles(FewArgs a) {
+  constexpr uint32_t kWBytes = kChunk * 2 * kBK, kStage = kWBytes + 32 * kC * 2 * kBK;
+  constexpr int kSlots = (160 << 10) / kStage, kLoads = 8 + 2 * kC;  // loads of a stage per loading wave
+  static_assert((kSlots - 2) * kLoads < 64, "vmcnt");
+  constexpr int kRB = 2, kCB = kChunk / 16;  // 16-row blocks of a wave, 16-column blocks
+  __shared__ u32x4 lds[kSlots * kStage / 16];
+  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int nk = a.H / kBK;
+  const int mine = (a.chunks - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x;  // chunks b, b + grid, ...
+  if (mine <= 0) return;
+  // columns of chunk c: first one and how many (0 past the vocabulary)
+  const auto chunk_at = [&](int c, int& s, int& j, int& c0) {
+    s = c / a.gm.cps;
+    j = c - s * a.gm.cps;
+    const int sbeg = (a.gm.s0 + s) * a.gm.S;
+    c0 = sbeg + j * kChunk;
+    return max(0, min(kChunk, min(a.gm.S, a.gm.V - sbeg) - j * kChunk));
+  };
+  if (w >= kC) {
+    // ---- loads: W rows 64 p + 8 i + lane / 8 of the chunk, h rows 16 kC p + 8 i + lane / 8
+    const int p = w - kC, r8 = lane >> 3;
+    uint32_t w_off[8], h_off[2 * kC];
 #pragma unroll
-    for (int n = 0; n < kCB; ++n) wo[n] = 2u * ((uint32_t)min(16 * n + r16, last) * a.H + 8 * rl);
+    for (int i = 0; i < 2 * kC; ++i) {
+      const int row = 16 * kC * p + 8 * i + r8;
+      h_off[i] = 2u * ((uint32_t)min(row, a.T - 1) * a.H) + 16u * ((lane & 7) ^ ((row >> 1) & 7));
+    }
+    const char* wb = nullptr;
+    int l_c = (int)blockIdx.x, l_kb = 0, l_left = mine;  // chunk and k-block of the stage loaded next
+    const auto begin = [&]() {
+      int s, j, c0;
+      const int width = chunk_at(l_c, s, j, c0), last = max(width, 1) - 1;
+      wb = reinterpret_cast<const char*>(a.W) + (size_t)__builtin_amdgcn_readfirstlane(width > 0 ? c0 : 0) * (2 * a.H);
 #pragma unroll
-    for (int m = 0; m < kRB; ++m) ho[m] = 2u * ((uint32_t)min(16 * m + r16, a.T - 1) * a.H + 8 * rl);
-    struct Stage {
-      bf16x8 w[kSteps][kCB], h[kSteps][kRB];
-    } st[kDepth];
-    const int ns = a.H / (32 * kSteps);
-    const auto load = [&](Stage& x, int i) {  // (past the end: the last stage again)
-      const size_t k2 = (size_t)min(i, ns - 1) * (64 * kSteps);
-#pragma unroll
-      for (int q = 0; q < kSteps; ++q) {
-#pragma unroll
-        for (int n = 0; n < kCB; ++n) x.w[q][n] = *reinterpret_cast<const bf16x8*>(wb + k2 + 64 * q + wo[n]);
-#pragma unroll
-        for (int m = 0; m < kRB; ++m) x.h[q][m] = *reinterpret_cast<const bf16x8*>(hb + k2 + 64 * q + ho[m]);
+      for (int i = 0; i < 8; ++i) {
+        const int row = 64 * p + 8 * i + r8;
+        w_off[i] = 2u * ((uint32_t)min(row, last) * a.H) + 16u * ((lane & 7) ^ ((row >> 1) & 7));
       }
     };
+    begin();
+    // Rows 4 KB apart, or a multiple of it, lie on few memory channels, and
+    // blocks in step all ask for the same ones: they start up to 15 k-blocks
+    // (0.8 us each) apart.  One row of H = 4096 256 -> 232 us, of 2048 139 ->
+    // 124; at other widths waiting only costs (H = 4032: 213 -> 221).
+    if (a.H % 2048 == 0)
+      for (int i = (int)(blockIdx.x >> 3) & 15; i > 0; --i) __builtin_amdgcn_s_sleep(26);
+    const uint32_t lds0 = lds_addr(lds);
+    const auto load = [&](int slot) {
+      const uint32_t m0 = lds0 + kStage * slot;
+      const size_t k2 = (size_t)l_kb * (2 * kBK);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) dma16(wb + k2, w_off[i], m0 + 1024u * (8 * p + i));
+#pragma unroll
+      for (int i = 0; i < 2 * kC; ++i)
+        dma16(reinterpret_cast<const char*>(a.h) + k2, h_off[i], m0 + kWBytes + 1024u * (2 * kC * p + i));
+      if (l_kb + 1 < nk) {
+        ++l_kb;
+      } else if (l_left > 1) {  // (past the end: the last stage again, into a free slot)
+        --l_left;
+        l_kb = 0;
+        l_c += (int)gridDim.x;
+        begin();
+      }
+    };
+#pragma unroll 1
+    for (int i = 0; i + 1 < kSlots; ++i) load(i);
+    int slot = 0;
+#pragma unroll 1
+    for (int i = 0; i < mine * nk; ++i) {
+      loads_then_barrier<(kSlots - 2) * kLoads>();
+      load(slot == 0 ? kSlots - 1 : slot - 1);  // the slot read last time
+      slot = slot + 1 == kSlots ? 0 : slot + 1;
+    }
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // nothing is loaded into LDS past the block's end
+    return;
+  }
+  // ---- rows 32 w .. + 31
+  const int r16 = lane & 15, rl = lane >> 4;
+  int slot = 0;
+#pragma unroll 1
+  for (int n = 0; n < mine; ++n) {
     AccBlk acc[kRB][kCB];
 #pragma unroll
     for (int m = 0; m < kRB; ++m)
 #pragma unroll
-      for (int n = 0; n < kCB; ++n) acc[m][n] = AccBlk{};
-#pragma unroll
-    for (int d = 0; d + 1 < kDepth; ++d) load(st[d], d);
+      for (int b = 0; b < kCB; ++b) acc[m][b] = AccBlk{};
 #pragma unroll 1
-    for (int i = 0; i < ns; i += kDepth) {
+    for (int kt = 0; kt < nk; ++kt) {
+      wait_lds();
+      __builtin_amdgcn_s_barrier();
+      __builtin_amdgcn_sched_barrier(0);
+      const char* st = reinterpret_cast<const char*>(lds) + kStage * slot;
 #pragma unroll
-      for (int d = 0; d < kDepth; ++d) {
-        if (i + d >= ns) break;
-        load(st[(d + kDepth - 1) % kDepth], i + d + kDepth - 1);
-        __builtin_amdgcn_sched_barrier(0);
+      for (int kk = 0; kk < 2; ++kk) {
+        bf16x8 x[kRB];
 #pragma unroll
-        for (int q = 0; q < kSteps; ++q)
+        for (int m = 0; m < kRB; ++m)
+          x[m] = __builtin_bit_cast(bf16x8, *reinterpret_cast<const u32x4*>(
+                                                st + kWBytes + 16u * slot_k(32 * w + 16 * m + r16, 4 * kk + rl)));
 #pragma unroll
-          for (int m = 0; m < kRB; ++m)
+        for (int b = 0; b < kCB; ++b) {
+          const bf16x8 y =
+              __builtin_bit_cast(bf16x8, *reinterpret_cast<const u32x4*>(st + 16u * slot_k(16 * b + r16, 4 * kk + rl)));
 #pragma unroll
-            for (int n = 0; n < kCB; ++n)
-              acc[m][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(st[d].w[q][n], st[d].h[q][m], acc[m][n], 0, 0, 0);
-        __builtin_amdgcn_sched_barrier(0);
+          for (int m = 0; m < kRB; ++m) acc[m][b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(y, x[m], acc[m][b], 0, 0, 0);
+        }
       }
+      slot = slot + 1 == kSlots ? 0 : slot + 1;
     }
+    // lane l holds row 32 w + 16 m + l % 16, columns 16 b + 4 (l / 16) + e
+    int s, j, c0;
+    const int width = chunk_at((int)blockIdx.x + n * (int)gridDim.x, s, j, c0);
+    if constexpr (kDz) {
+      // (the last wave: zeros down to the rows' multiple of 64)
+      const int rows = w + 1 < kC ? 32 : (a.T + 63) / 64 * 64 - 32 * w;
 #pragma unroll
-    for (int m = 0; m < kRB; ++m)
+      for (int m = 0; m < 4; ++m) {
+        if (16 * m >= rows) continue;
+        const int t = 32 * w + 16 * m + r16;
+        const float4 ri = a.rowinfo[t];
+        const int target = __float_as_int(ri.w), yl = target - c0;
+        const bool on = m < kRB && target != kNoRow;
+        const float g = kTop && on ? a.rowg[t] : 0.f;
 #pragma unroll
-      for (int n = 0; n < kCB; ++n)
+        for (int b = 0; b < kCB; ++b) {
+          const int c = 16 * b + 4 * rl;
+          if (j * kChunk + c >= a.bg.S_pad) continue;  // the next split's columns
+          float d[4] = {0.f, 0.f, 0.f, 0.f};
+          if (m < kRB && on) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) acc_v[m][n][e] = kTop ? acc[m][n][e] : acc[m][n][e] * a.scale;
-  }
-  // lane l holds row 16 m + l % 16, columns 16 n + 4 (l / 16) + e
-  if constexpr (kDz) {
+            for (int e = 0; e < 4; ++e)
+              if (c + e < width) {
+                const float z = acc[m < kRB ? m : 0][b][e];
+                const float x = minus_share<kTop>(kTop ? z : z * a.scale, ri);
+                d[e] = kTop && c + e == yl ? g + x : x;
+              }
+          }
+          *reinterpret_cast<uint2*>(a.dZ + (size_t)t * a.bg.ldz + (size_t)s * a.bg.S_pad + j * kChunk + c) =
+              make_uint2(pack_bf16x2(d[0], d[1]), pack_bf16x2(d[2], d[3]));
+        }
+      }
+    } else {
+      if (width <= 0) continue;
+      const int g = (a.gm.s0 + s) * a.gm.cps + j;
 #pragma unroll
-    for (int m = 0; m < kFewRows / 16; ++m) {  // (zeros below the rows at hand)
-      const int t = 16 * m + r16;
-      const float4 ri = a.rowinfo[t];
-      const int target = __float_as_int(ri.w), yl = target - sbeg - j * kChunk;
-      const bool on = m < kRB && target != kNoRow;
-      const float g = kTop && on ? a.rowg[t] : 0.f;
+      for (int m = 0; m < kRB; ++m) {
+        const int t = 32 * w + 16 * m + r16;
+        float v[4 * kCB];
 #pragma unroll
-      for (int n = 0; n < kCB; ++n) {
-        const int c = 16 * n + 4 * rl;
-        if (j * kChunk + c >= a.bg.S_pad) continue;  // the next split's columns
-        float d[4] = {0.f, 0.f, 0.f, 0.f};
-        if (m < kRB && on) {
+        for (int b = 0; b < kCB; ++b) {
+          const int c = 16 * b + 4 * rl;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[4 * b + e] = kTop ? acc[m][b][e] : acc[m][b][e] * a.scale;
+          if (t < a.T)  // whole chunks: what lies past the split's end is not read
+            *reinterpret_cast<float4*>(a.z + (size_t)t * a.ldz + (size_t)g * kChunk + c) =
+                make_float4(v[4 * b], v[4 * b + 1], v[4 * b + 2], v[4 * b + 3]);
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            if (c + e < width) {
-              const float x = minus_share<kTop>(acc_v[m < kRB ? m : 0][n][e], ri);
-              d[e] = kTop && c + e == yl ? g + x : x;
-            }
+            if (c + e >= width) v[4 * b + e] = -INFINITY;
         }
-        *reinterpret_cast<uint2*>(a.dZ + (size_t)t * a.bg.ldz + (size_t)s * a.bg.S_pad + j * kChunk + c) =
-            make_uint2(pack_bf16x2(d[0], d[1]), pack_bf16x2(d[2], d[3]));
-      }
-    }
-  } else {
-    const int g = (a.gm.s0 + s) * a.gm.cps + j;
-#pragma unroll
-    for (int m = 0; m < kRB; ++m) {
-      const int t = 16 * m + r16;
-      float v[4 * kCB];
-#pragma unroll
-      for (int n = 0; n < kCB; ++n) {
-        const int c = 16 * n + 4 * rl;
-        if (t < a.T)  // whole chunks: what lies past the split's end is not read
-          *reinterpret_cast<float4*>(a.z + (size_t)t * a.ldz + (size_t)g * kChunk + c) =
-              make_float4(acc_v[m][n][0], acc_v[m][n][1], acc_v[m][n][2], acc_v[m][n][3]);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) v[4 * n + e] = c + e < width ? acc_v[m][n][e] : -INFINITY;
-      }
-      const MSU st = chunk_stats_moment(v);
-      if (rl == 0 && t < a.T) {
-        a.rec[(size_t)g * a.rec_stride + t] = make_float2(st.m, st.s);
-        if (kTop) a.rec_u[(size_t)g * a.rec_stride + t] = st.u;
+        const MSU st = chunk_stats_moment(v);
+        if (rl == 0 && t < a.T) {
+          a.rec[(size_t)g * a.rec_stride + t] = make_float2(st.m, st.s);
+          if (kTop) a.rec_u[(size_t)g * a.rec_stride + t] = st.u;
+        }
       }
     }
   }
@@ -1510,16 +1572,6 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(RLK_WA
 // tile at a time per compute unit, loads, MFMAs and stores in turn.  Together
 // they took 0.92 ms at 64 rows (V = 151936).
 // ---------------------------------------------------------------------------
-// Waves wait for their own direct loads, all but the n issued last, and then
-// for one another.
-template <int n>
-__device__ __forceinline__ void loads_then_barrier() {
-  asm volatile("s_waitcnt vmcnt(%0)" : : "n"(n) : "memory");
-  wait_lds();
-  __builtin_amdgcn_s_barrier();
-  __builtin_amdgcn_sched_barrier(0);
-}
-
 // Eight k of one column for each lane, from two transposing reads: `base` is
 // where the lane's 4 columns of k-row 8 (l / 16) + (l % 16) / 4 lie, kr the
 // bytes of 4 k-rows (which keep the swizzle; see frag_at).

@@ -202,11 +202,12 @@ inline dim3 row_grid(int64_t rows) { return dim3((unsigned)std::min(rows, kRowBl
 
 #if RLK_MFMA == 16
 template <bool kTop, bool kDz>
-rlk_status launch_few(const FewArgs& a, int64_t blocks, hipStream_t st) {
+rlk_status launch_few(const FewArgs& a, hipStream_t st) {
   typedef void (*Fn)(FewArgs);
-  static constexpr Fn fns[3] = {few_tiles<kTop, kDz, 0>, few_tiles<kTop, kDz, 1>, few_tiles<kTop, kDz, 2>};
-  const int f = few_shape(a.T);
-  RLK_LAUNCH_FN(kDz ? "few_tiles (dz)" : "few_tiles", fns[f], dim3((unsigned)blocks), dim3(64), st, a);
+  const int c = few_consumers(a.T);
+  const Fn fn = c == 1 ? few_tiles<kTop, kDz, 1> : c == 2 ? few_tiles<kTop, kDz, 2> : few_tiles<kTop, kDz, 4>;
+  RLK_LAUNCH_FN(kDz ? "few_tiles (dz)" : "few_tiles", fn, dim3((unsigned)std::min(a.chunks, device_cus())),
+                dim3((unsigned)few_threads(c)), st, a);
   return RLK_OK;
 }
 
@@ -226,7 +227,8 @@ rlk_status few_logits(const void* h, const void* W, int64_t T, int64_t H, int64_
   a.rec_u = rec_u;
   a.z = z;
   a.ldz = few_ldz(V);
-  return launch_few<kTop, false>(a, (int64_t)(last_split(a.gm) + 1) * a.gm.cps, st);
+  a.chunks = (last_split(a.gm) + 1) * a.gm.cps;
+  return launch_few<kTop, false>(a, st);
 }
 #endif
 
@@ -389,10 +391,9 @@ rlk_status run_distill_fwd(const void* h, const void* W, const int32_t* ids, con
 }
 
 #if RLK_MFMA == 16
-// Both gradients in their few-row kernels up to kFewGrad rows: 0.66 ms
-// together at 128 rows (H = 4096, V = 151936) against the tiles' 0.94; of 256
-// rows 1.09 against 0.95.
-constexpr int64_t kFewGrad = 128;
+// Both gradients in their few-row kernels up to kFewRows rows: 0.66 ms
+// together at 128 rows (H = 4096, V = 151936) against the tiles' 0.94; forms
+// for 256 rows took 1.09 against 0.95.
 rlk_status launch_few_grad_h(const FewGradHArgs& a, int64_t T, bool cont, hipStream_t st) {
   typedef void (*Fn)(FewGradHArgs);
   static constexpr Fn fns[2][4] = {
@@ -520,8 +521,9 @@ rlk_status run_soft_bwd(const SoftBwd& b, const SoftBwdWs& L, void* ws, hipStrea
       fa.rowg = ga.rowg;
       fa.bg = bg;
       fa.dZ = da.dZ;
-      if (top) RLK_TRY((launch_few<true, true>(fa, (int64_t)G * gm.cps, st)));
-      else RLK_TRY((launch_few<false, true>(fa, (int64_t)G * gm.cps, st)));
+      fa.chunks = G * gm.cps;
+      if (top) RLK_TRY((launch_few<true, true>(fa, st)));
+      else RLK_TRY((launch_few<false, true>(fa, st)));
     } else
 #endif
     if (top)
@@ -567,7 +569,7 @@ rlk_status run_soft_bwd(const SoftBwd& b, const SoftBwdWs& L, void* ws, hipStrea
     ha.part_stride = (size_t)b.T * b.H;
     const bool cont = c % per != 0;
 #if RLK_MFMA == 16
-    if (b.grad_h && b.T <= kFewGrad) {
+    if (few && b.grad_h) {
       FewGradHArgs fh{};
       fh.dZ = da.dZ;
       fh.W = da.W;
@@ -583,7 +585,7 @@ rlk_status run_soft_bwd(const SoftBwd& b, const SoftBwdWs& L, void* ws, hipStrea
       RLK_TRY(launch_few_grad_h(fh, b.T, cont, st));
       ha.part = nullptr;
     }
-    if (b.grad_W && b.T <= kFewGrad) {
+    if (few && b.grad_W) {
       FewGradWArgs fw{};
       fw.dZ = da.dZ;
       fw.hA = ga.hA;
