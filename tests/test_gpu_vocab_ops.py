@@ -86,7 +86,7 @@ def close(name, got, want, tol):
     assert np.array_equal(np.isfinite(got), np.isfinite(want)), name
     f = np.isfinite(want)
     assert np.array_equal(got[~f], want[~f]), name
-    d = np.abs(got - want)[f].max(initial=0.0)
+    d = np.abs(got[f] - want[f]).max(initial=0.0)
     say(f"  {name}: max error {d:.3e} of {tol:.1e}")
     assert d <= tol, name
 
@@ -141,7 +141,10 @@ def check_distill(c, K, tau, grads=True):
         check_grads(c, dz, size, gh, gW)
 
 
+# the few-row kernels end at 128 rows (by 16, 32, 64); the others' row tiles hold
+# 256, and more than 256 of their tiles run in rounds, the last one in halves
 SHAPES = [(1, 64, 1, 0.0), (1, 64, 5, 0.0), (7, 128, 33, 0.0), (64, 256, 4096, 0.0), (37, 64, 1000, 0.3),
+          (17, 2048, 700, 0.0), (100, 192, 2500, 0.2), (128, 64, 12_345, 0.1),
           (300, 192, 5000, 0.2), (129, 320, 20011, 0.15), (600, 64, 9000, 0.5), (5, 64, 300_000, 0.0)]
 
 
@@ -170,10 +173,17 @@ def test_ties_go_to_the_lowest_id():
     close("entropy", ent, [math.log(70_000), 0, math.log(70_000)], ENT_TOL)
 
 
-@pytest.mark.parametrize("budget", ["1", "12", "40"])
-def test_groups_of_splits_change_no_bit(budget, monkeypatch):
+def test_tiles_in_rounds():
+    """576 tiles of 256 columns and rows: two rounds of 256 units, and 64 in halves."""
+    check_top(Case(300, 64, 70_000, seed=21), 30)
+    check_distill(Case(300, 64, 70_000, seed=22), 30, 1.0)
+
+
+@pytest.mark.parametrize("T", [300, 40])
+@pytest.mark.parametrize("budget", ["1", "2", "12", "40"])
+def test_groups_of_splits_change_no_bit(budget, T, monkeypatch):
     """The workspace budget sets how many splits are processed together."""
-    c = Case(300, 128, 20_011, 0.2, seed=4)
+    c = Case(T, 128, 20_011, 0.2, seed=4)
     h, W = c.dev()
     y, g, ge = i32_dev(c.y), f32_dev(c.g), f32_dev(c.ge)
     n_ids, n_lg = c.teacher(20)
@@ -187,7 +197,7 @@ def test_groups_of_splits_change_no_bit(budget, monkeypatch):
 
     want = everything()
     monkeypatch.setenv("RLK_DZ_BUDGET_MB", budget)
-    sizes = rlk.vocab_workspace_bytes(rlk.VOP_TOP_FWD, 300, 128, 20_011, 50)
+    sizes = rlk.vocab_workspace_bytes(rlk.VOP_TOP_FWD, T, 128, 20_011, 50)
     say(f"[groups] budget {budget} MiB: {sizes} bytes")
     for a, b in zip(everything(), want):
         assert torch.equal(a, b)
@@ -454,6 +464,34 @@ def test_streams_and_graphs():
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(out, new))
+
+
+def test_two_streams_at_once():
+    """Calls on two streams, each with its own buffers, do not meet."""
+    c = [Case(90, 128, 30_000, 0.1, seed=31), Case(300, 64, 30_000, 0.1, seed=32)]
+    dev = []
+    for x in c:
+        n_ids, n_lg = x.teacher(16)
+        dev.append((*x.dev(), i32_dev(x.y), f32_dev(x.g), i32_dev(n_ids), f32_dev(n_lg)))
+
+    def all_of(h, W, y, g, ids, lg):
+        out = list(rlk.linear_logp_top_fwd(h, W, y, 9))
+        out += rlk.linear_logp_top_bwd(h, W, y, out[1], out[2], g, g)
+        d = list(rlk.linear_distill_fwd(h, W, ids, lg))
+        return out + d + list(rlk.linear_distill_bwd(h, W, ids, lg, d[1], d[2], g))
+
+    want = [all_of(*x) for x in dev]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = [[], []]
+    for rep in range(3):
+        for k, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[k].append(all_of(*dev[k]))
+    torch.cuda.synchronize()
+    for k in range(2):
+        for out in got[k]:
+            assert all(torch.equal(a, b) for a, b in zip(out, want[k]))
 
 
 def test_wrong_workspaces_are_refused():
