@@ -144,7 +144,7 @@ def check_distill(c, K, tau, grads=True):
 # the few-row kernels end at 128 rows (by 16, 32, 64); the others' row tiles hold
 # 256, and more than 256 of their tiles run in rounds, the last one in halves
 SHAPES = [(1, 64, 1, 0.0), (1, 64, 5, 0.0), (7, 128, 33, 0.0), (64, 256, 4096, 0.0), (37, 64, 1000, 0.3),
-          (17, 2048, 700, 0.0), (100, 192, 2500, 0.2), (128, 64, 12_345, 0.1),
+          (17, 2048, 700, 0.0), (100, 192, 2500, 0.2), (321, 448, 2500, 0.0), (448, 64, 1000, 0.0), (128, 64, 12_345, 0.1),
           (300, 192, 5000, 0.2), (129, 320, 20011, 0.15), (600, 64, 9000, 0.5), (5, 64, 300_000, 0.0)]
 
 
