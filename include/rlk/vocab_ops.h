@@ -20,7 +20,7 @@
  * synchronised; outputs are overwritten; H % 64 == 0; status codes), except:
  *   - h, W, ws, grad_h and grad_W are 16-byte aligned; arrays of rows or of
  *     rows and slots need the alignment of their elements (4 bytes);
- *   - T == 0 launches nothing but the zeroing of a wanted grad_W.
+ *   - T <= 2^23; T == 0 launches nothing but the zeroing of a wanted grad_W.
  * The current device must be the one the arrays live on.
  */
 #ifndef RLK_VOCAB_OPS_H_

@@ -388,7 +388,7 @@ __global__ __launch_bounds__(few_threads(kC)) void few_tiles(FewArgs a) {
     // blocks in step all ask for the same ones: they start up to 15 k-blocks
     // (0.8 us each) apart.  One row of H = 4096 256 -> 232 us, of 2048 139 ->
     // 124; at other widths waiting only costs (H = 4032: 213 -> 221).
-    if (a.H % 2048 == 0)
+    if (a.H % 2048 == 0 && a.chunks > (int)gridDim.x)
       for (int i = (int)(blockIdx.x >> 3) & 15; i > 0; --i) __builtin_amdgcn_s_sleep(26);
     const uint32_t lds0 = lds_addr(lds);
     const auto load = [&](int slot) {
@@ -590,10 +590,11 @@ __device__ __forceinline__ float4 grad_row(const GatherGradArgs& a, int t, float
   if constexpr (kTop) {
     const int yt = a.y[t];
     gt = a.g ? a.g[t] : 0.f;
-    if (yt < 0 || yt >= a.V) gt = __builtin_nanf("");
+    const bool ok = yt >= 0 && yt < a.V;
+    if (!ok) gt = __builtin_nanf("");
     ri.z = a.g_entropy ? a.g_entropy[t] : 0.f;
     ri.y = gt + ri.z * a.entropy[t];
-    ri.w = __int_as_float(yt);
+    ri.w = __int_as_float(ok ? yt : -1);
   } else {
     ri.y = a.act[t] == 1 ? __builtin_nanf("") : -(a.g[t] * a.scale);
   }

@@ -150,8 +150,11 @@ T* at(void* ws, size_t off) {
   return reinterpret_cast<T*>(static_cast<char*>(ws) + off);
 }
 
+// Rows: the row kernels take up to 128 threads each, 2^31 - 1 to a launch.
+constexpr int64_t kMaxRows = int64_t(1) << 23;
+
 inline rlk_status check_sizes(int64_t T, int64_t H, int64_t V, int64_t K, int64_t least_k) {
-  if (T < 0 || T > kMaxT) return fail(RLK_ERR_BAD_SHAPE, "T=%lld out of [0, 2^24]", (long long)T);
+  if (T < 0 || T > kMaxRows) return fail(RLK_ERR_BAD_SHAPE, "T=%lld out of [0, 2^23]", (long long)T);
   if (H <= 0 || H > kMaxH || H % 64 != 0)
     return fail(RLK_ERR_BAD_SHAPE, "H=%lld must be a positive multiple of 64 up to 65536", (long long)H);
   if (V <= 0 || V > kMaxV) return fail(RLK_ERR_BAD_SHAPE, "V=%lld out of [1, 8000000]", (long long)V);
@@ -637,7 +640,7 @@ rlk_status check_grads(int64_t T, int64_t H, int64_t V, const void* grad_h, void
 extern "C" {
 
 size_t rlk_vocab_workspace_bytes(int32_t op, int64_t T, int64_t H, int64_t V, int64_t K) {
-  if (T < 0 || T > kMaxT || H <= 0 || H > kMaxH || H % 64 != 0 || V <= 0 || V > kMaxV || K < 0 || K > kMaxK) return 0;
+  if (T < 0 || T > kMaxRows || H <= 0 || H > kMaxH || H % 64 != 0 || V <= 0 || V > kMaxV || K < 0 || K > kMaxK) return 0;
   switch (op) {
     case RLK_VOP_TOP_FWD: return top_fwd_layout(T, H, V, K).total;
     case RLK_VOP_TOP_BWD: return soft_bwd_layout(T, H, V, 0).total;

@@ -18,6 +18,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import operator
 
 import torch
 from torch.autograd.function import once_differentiable
@@ -61,6 +62,26 @@ def _ws(ws, op, T, H, V, K, device):
     if n == 0:
         raise ValueError(f"invalid shape T={T} H={H} V={V} K={K}")
     return torch.empty(n, dtype=torch.uint8, device=device), n
+
+
+def _top_k(k):
+    try:
+        n = -1 if isinstance(k, bool) else operator.index(k)
+    except TypeError:
+        n = -1
+    if not 0 <= n <= MAX_K:
+        raise ValueError(f"top_k must be an integer in [0, {MAX_K}], got {k!r}")
+    return n
+
+
+def _targets(h, W, y, ignore_index):
+    """_prep, with 64-bit targets and ignore_index kept inside 32 bits: a
+    target past int32 stays outside every vocabulary."""
+    if not -2 ** 31 <= ignore_index < 2 ** 31:
+        raise ValueError(f"ignore_index must fit an int32, got {ignore_index}")
+    if y.dtype == torch.int64:
+        y = y.clamp(-2 ** 31, 2 ** 31 - 1)
+    return _prep(h, W, y)
 
 
 def _slots(T, device, ids, logits):
@@ -122,9 +143,8 @@ def linear_logp_top_fwd(h, W, y, top_k: int, ignore_index: int = IGNORE_INDEX, w
     vocabulary hold id -1 and -inf, and so do inactive rows (y ==
     ignore_index), whose logp, lse and entropy are 0.
     """
-    if isinstance(top_k, bool) or not isinstance(top_k, int) or not 0 <= top_k <= MAX_K:
-        raise ValueError(f"top_k must be an integer in [0, {MAX_K}], got {top_k!r}")
-    h, W, y = _prep(h, W, y)
+    top_k = _top_k(top_k)
+    h, W, y = _targets(h, W, y, ignore_index)
     T, H = h.shape
     V = W.shape[0]
     with _on(h.device):
@@ -143,7 +163,7 @@ def linear_logp_top_bwd(h, W, y, lse, entropy, g, g_entropy=None, ignore_index: 
                         need_grad_h: bool = True, need_grad_W: bool = True, grad_W_dtype=torch.float32, ws=None):
     """(grad_h bf16 [T,H] or None, grad_W [V,H] of grad_W_dtype or None) of
     sum_t g_t logp_t + g_entropy_t entropy_t; g or g_entropy may be None (zero)."""
-    h, W, y = _prep(h, W, y)
+    h, W, y = _targets(h, W, y, ignore_index)
     T, H = h.shape
     V = W.shape[0]
     named = dict(lse=lse, entropy=entropy, g=g, g_entropy=g_entropy)

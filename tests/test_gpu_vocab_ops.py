@@ -261,14 +261,16 @@ def test_inactive_rows_and_masked_values():
     assert gh.eq(0).all() and gW.eq(0).all()
 
 
-def test_undefined_rows_are_nan_and_only_they():
-    c = Case(20, 64, 500, seed=3)
+@pytest.mark.parametrize("T", [20, 150])  # few rows and row tiles
+@pytest.mark.parametrize("outside", [(500, -7), (2 ** 31 - 1, -2 ** 31), (2 ** 32 + 5, -2 ** 40)])
+def test_undefined_rows_are_nan_and_only_they(T, outside):
+    c = Case(T, 64, 500, seed=3)
     h, W = c.dev()
-    y, g = i32_dev(c.y), f32_dev(c.g)
-    y[3], y[4] = 500, -7
+    y, g = i32_dev(c.y).long(), f32_dev(c.g)
+    y[3], y[4] = outside
     logp, lse, ent, top, ids = rlk.linear_logp_top_fwd(h, W, y, 6)
-    want = O.top_forward(c.h, c.W, np.where(np.isin(np.arange(20), (3, 4)), 0, c.y), 6)
-    bad = torch.zeros(20, dtype=torch.bool, device=DEV)
+    want = O.top_forward(c.h, c.W, np.where(np.isin(np.arange(T), (3, 4)), 0, c.y), 6)
+    bad = torch.zeros(T, dtype=torch.bool, device=DEV)
     bad[3:5] = True
     assert logp[bad].isnan().all() and logp[~bad].isfinite().all()
     close("entropy", ent, want[2], ENT_TOL)
@@ -277,8 +279,8 @@ def test_undefined_rows_are_nan_and_only_they():
     assert gh[bad].isnan().all() and gh[~bad].isfinite().all() and gW.isnan().all()
     n_ids, n_lg = c.teacher(4, empty=0.0)
     t_ids, lg = i32_dev(n_ids), f32_dev(n_lg)
-    t_ids[3, 1] = 500
-    lg[4, 2] = float("nan")
+    t_ids[3, 1] = min(outside[0], 2 ** 31 - 1)
+    lg[4, 2] = float("nan") if T == 20 else float("inf")
     loss, lse, lp = rlk.linear_distill_fwd(h, W, t_ids, lg)
     assert loss[bad].isnan().all() and loss[~bad].isfinite().all()
     gh, _ = rlk.linear_distill_bwd(h, W, t_ids, lg, lse, lp, g, need_grad_W=False)

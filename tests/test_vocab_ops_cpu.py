@@ -32,7 +32,7 @@ def test_workspace_bytes(monkeypatch):
     for op in range(4):
         assert W(op, 0, 64, 10, 1) > 0
         for bad in [(-1, 64, 10, 1), (4, 63, 10, 1), (4, 64, 0, 1), (4, 64, 8_000_001, 1), (4, 64, 10, 129),
-                    (4, 64, 10, -1), ((1 << 24) + 1, 64, 10, 1)]:
+                    (4, 64, 10, -1), ((1 << 23) + 1, 64, 10, 1)]:
             assert W(op, *bad) == 0, (op, bad)
     assert W(4, 4, 64, 10, 1) == 0
     assert W(rlk.VOP_TOP_FWD, 4, 64, 10, 0) > 0 and W(rlk.VOP_DISTILL_FWD, 4, 64, 10, 0) == 0
@@ -60,16 +60,16 @@ def test_top_forward_refusals():
         assert top_fwd(**{a: OFF8}) == BAD_ALIGN, a
     for a in ("y", "logp", "lse", "ent", "tl", "ti"):
         assert top_fwd(**{a: OFF2}) == BAD_ALIGN, a
-    for bad in (dict(T=-1), dict(H=96), dict(V=0), dict(V=9_000_000), dict(K=129), dict(K=-1), dict(T=(1 << 24) + 1)):
+    for bad in (dict(T=-1), dict(H=96), dict(V=0), dict(V=9_000_000), dict(K=129), dict(K=-1), dict(T=(1 << 23) + 1)):
         assert top_fwd(**bad) == BAD_SHAPE, bad
     need = rlk.vocab_workspace_bytes(rlk.VOP_TOP_FWD, 64, 256, 4096, 8)
     assert top_fwd(n=need - 1) == WS_SMALL
     assert b"need" in rlk.lib().rlk_last_error_message()
     assert top_fwd(T=0, h=None, y=None, logp=None, ent=None, ws=None, n=0) == OK
     assert rlk.lib().rlk_last_error_message() == b""
-    # more tiles than a launch holds: 65536 row tiles x 32 x 977 column tiles
-    assert top_fwd(T=1 << 24, H=64, V=8_000_000, K=0) == WS_SMALL
-    assert top_fwd(T=1 << 24, H=64, V=8_000_000, K=0, n=1 << 60) in (BAD_SHAPE, HIP, DEVICE)
+    # more tiles than a launch holds: 32768 row tiles x 32 x 977 column tiles
+    assert top_fwd(T=1 << 23, H=64, V=8_000_000, K=0) == WS_SMALL
+    assert top_fwd(T=1 << 23, H=64, V=8_000_000, K=0, n=1 << 60) in (BAD_SHAPE, HIP, DEVICE)
 
 
 def top_bwd(h=FAKE, W=FAKE, y=FAKE, lse=FAKE, ent=FAKE, g=FAKE, ge=FAKE, T=64, H=256, V=4096, gh=FAKE, gW=FAKE, dt=0,
@@ -147,7 +147,7 @@ def host_as_device(monkeypatch):
     monkeypatch.setattr(vo, "_head", lambda h, W: (h, W))
 
 
-@pytest.mark.parametrize("bad", [-1, 129, 2.0, True, None])
+@pytest.mark.parametrize("bad", [-1, 129, 2.0, True, None, torch.ones(2, dtype=torch.int64)[0] * 1.5])
 def test_binding_refuses_top_k(bad):
     with pytest.raises(ValueError, match="top_k"):
         rlk.linear_logp_top_fwd(bf(T, H), bf(V, H), i32(T), bad)
@@ -175,6 +175,11 @@ def test_binding_refuses_shapes_and_types(host_as_device):
 
 
 def test_binding_refuses_the_rest():
+    for f in (lambda i: rlk.linear_logp_top_fwd(bf(T, H), bf(V, H), i32(T), 1, ignore_index=i),
+              lambda i: rlk.linear_logp_top_bwd(bf(T, H), bf(V, H), i32(T), f32(T), f32(T), f32(T), ignore_index=i)):
+        for bad in (2 ** 31, -2 ** 31 - 1, 2 ** 40):
+            with pytest.raises(ValueError, match="int32"):
+                f(bad)
     with pytest.raises(ValueError, match="device tensors"):
         rlk.linear_logp_top(bf(T, H), bf(V, H), i32(T), 4)
     with pytest.raises(ValueError, match="device tensors"):
