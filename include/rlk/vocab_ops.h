@@ -43,7 +43,10 @@ enum { RLK_VOP_TOP_FWD = 0, RLK_VOP_TOP_BWD = 1, RLK_VOP_DISTILL_FWD = 2, RLK_VO
  * The vocabulary is processed in groups of splits: the forward of
  * linear_logp_top keeps a group's fp32 logits (K > 0), the backwards a
  * group's bf16 dz, each within the budget of rlk_workspace_bytes
- * (RLK_DZ_BUDGET_MB; no result bit depends on it). */
+ * (RLK_DZ_BUDGET_MB; no result bit depends on it).  Up to 128 rows both
+ * forwards keep all logits where the budget holds them.  The backwards also
+ * hold grad_h in fp32 parts, 4 T H floats of them or more for narrow heads
+ * (8 at H = 2048, 32 at 512, V = 151936). */
 size_t rlk_vocab_workspace_bytes(int32_t op, int64_t T, int64_t H, int64_t V, int64_t K);
 
 /* Selected log-probability, entropy and top alternatives, z = h W^T:
@@ -58,7 +61,8 @@ size_t rlk_vocab_workspace_bytes(int32_t op, int64_t T, int64_t H, int64_t V, in
  *                         and -inf; may be NULL when K == 0
  * 0 <= K <= RLK_MAX_K.  A target outside [0, V) gives NaN in the row's logp;
  * its entropy and alternatives are those of the row.  A NaN logit makes
- * logp, lse, entropy and top_logp NaN and is never an alternative. */
+ * logp, lse, entropy and top_logp NaN and is never an alternative; a row of
+ * nothing but NaN has no alternatives (-1 and -inf), and its lse is -inf. */
 rlk_status rlk_linear_logp_top_fwd(const void* h, const void* W, const int32_t* y, int64_t T, int64_t H, int64_t V,
                                    int32_t ignore_index, int64_t K, float* logp, float* lse, float* entropy,
                                    float* top_logp, int32_t* top_ids, void* ws, size_t ws_bytes, void* stream);

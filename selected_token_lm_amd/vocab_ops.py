@@ -76,11 +76,14 @@ def _top_k(k):
 
 def _targets(h, W, y, ignore_index):
     """_prep, with 64-bit targets and ignore_index kept inside 32 bits: a
-    target past int32 stays outside every vocabulary."""
-    if not -2 ** 31 <= ignore_index < 2 ** 31:
+    target past int32 stays outside every vocabulary, and apart from an
+    ignore_index at int32's end."""
+    lo, hi = -2 ** 31, 2 ** 31 - 1
+    if not lo <= ignore_index <= hi:
         raise ValueError(f"ignore_index must fit an int32, got {ignore_index}")
     if y.dtype == torch.int64:
-        y = y.clamp(-2 ** 31, 2 ** 31 - 1)
+        inside = y.clamp(lo + (ignore_index == lo), hi - (ignore_index == hi))
+        y = torch.where(y == ignore_index, y, inside) if ignore_index in (lo, hi) else inside
     return _prep(h, W, y)
 
 

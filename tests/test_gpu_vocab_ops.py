@@ -292,6 +292,38 @@ def test_undefined_rows_are_nan_and_only_they(T, outside):
     assert logp.isnan().all() and lse.isnan().all() and ent.isnan().all() and not ids.eq(7).any() and ids.ge(0).all()
 
 
+@pytest.mark.parametrize("T", [20, 150])
+def test_rows_of_nan_and_targets_beyond_the_ignored_one(T):
+    c = Case(T, 64, 500, seed=8)
+    h, W = c.dev()
+    y, g = i32_dev(c.y).long(), f32_dev(c.g)
+    t_ids, lg = i32_dev(c.r.integers(0, 500, (T, 4))), f32_dev(c.r.standard_normal((T, 4)))
+    want = rlk.linear_logp_top_fwd(h, W, y, 6)
+    want_d = rlk.linear_distill_fwd(h, W, t_ids, lg)
+    bad = torch.zeros(T, dtype=torch.bool, device=DEV)
+    bad[3] = bad[T - 1] = True
+    h2 = torch.where(bad[:, None], float("nan"), h)
+    logp, lse, ent, top, ids = got = rlk.linear_logp_top_fwd(h2, W, y, 6)
+    assert logp[bad].isnan().all() and ent[bad].isnan().all() and ids[bad].eq(-1).all()
+    for a, b in zip(got, want):
+        assert torch.equal(a[~bad], b[~bad])
+    gh, gW = rlk.linear_logp_top_bwd(h2, W, y, lse, ent, g, g)
+    assert gh[bad].isnan().all() and gh[~bad].isfinite().all() and gW.isnan().all()
+    loss, lse, lp = got = rlk.linear_distill_fwd(h2, W, t_ids, lg)
+    assert loss[bad].isnan().all()
+    for a, b in zip(got, want_d):
+        assert torch.equal(a[~bad], b[~bad])
+    gh, gW = rlk.linear_distill_bwd(h2, W, t_ids, lg, lse, lp, g)
+    assert gh[bad].isnan().all() and gh[~bad].isfinite().all() and gW.isnan().all()
+    # targets at and past int32's ends, one of which is the ignored one
+    for ignore, far in ((-2 ** 31, -2 ** 31 - 1), (2 ** 31 - 1, 2 ** 31)):
+        y2 = y.clone()
+        y2[2], y2[5] = ignore, far
+        logp, _, _, _, ids = rlk.linear_logp_top_fwd(h, W, y2, 6, ignore_index=ignore)
+        assert logp[2] == 0 and ids[2].eq(-1).all()
+        assert logp[5].isnan() and torch.equal(ids[5], want[4][5])
+
+
 def test_lengths_and_strides():
     c = Case(33, 64, 900, 0.1, seed=6)
     h, W = c.dev()
