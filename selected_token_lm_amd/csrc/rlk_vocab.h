@@ -18,6 +18,14 @@
 //   distill_scatter    dz at the teacher's tokens
 //   part_grad_tiles    grad_h in parts of the vocabulary, grad_W
 //   grad_h_sum         the parts together (after the last group)
+// Up to 128 rows (few_rows: the batch's rows in place, no compaction) other
+// kernels give the same bits:
+//   few_tiles          for logit_tiles and soft_dz_tiles
+//   few_rows_grad      for gather_rows_grad
+//   few_grad_h, few_grad_w   for part_grad_tiles
+//
+// Times below are of one MI355X (which copies at 4.9 TB/s, and whose library
+// multiplies 8192^3 bf16 matrices at 1.53 PFLOP/s), V = 151936.
 #pragma once
 
 #include "rlk_kernels.h"
@@ -87,6 +95,14 @@ __device__ __forceinline__ MSU chunk_stats_moment(const float (&v)[kRowVals]) {
 //   z + i * ldz + 128 (sl cps + j).
 // !kTop: logits times `scale` (1 / temperature); the tile's entries (see
 //   bucket_entries) pick the scaled logits of the teacher's tokens.
+// Bound by the engine's MFMAs.  3482 active rows, H = 4096 (4.33 TFLOP): 2.91
+// ms (1.49 PFLOP/s) with 64 tokens of a teacher; 4096 rows (5.10 TFLOP) with
+// every logit stored 3.26 - 3.38 ms (1.51 - 1.56), 0.35 of them for the first
+// moment and the 2.5 GB of stores (the accumulators' registers leave none to
+// pick the alternatives here).  Stores that bypass the caches: 3.64.
+// At 129 to 512 rows each tile waits for its loads: 256 rows 0.31 ms, 257
+// 0.44; leaving out the MFMAs of a short row tile's padding gained 3 % there
+// and is not done.
 // ---------------------------------------------------------------------------
 struct LogitArgs {
   const uint16_t* hA;  // active rows of h, compacted, zero padded to a multiple of 256
@@ -316,6 +332,12 @@ __device__ __forceinline__ void loads_then_barrier() {
 // engine's MFMA chain (k ascending in steps of 32) in the engine's layout, so
 // the statistics are the same bits.  Rows are those of the batch, in place: no
 // compaction.
+//
+// One row, H = 4096: 223 - 230 us (5.4 - 5.6 TB/s of W; the copy's rate is 4.9
+// read and written together); 48 rows of H = 2048: 146 (4.3 TB/s; the logits
+// are 30 MB of stores besides).  W straight into registers took 225 at one row
+// of H = 4096 but 335 at 64, and 193 at 48 of H = 2048; waves of 64 columns, or
+// that split the rows, 465 and more (W's rows pass LDS once per wave).
 // ---------------------------------------------------------------------------
 constexpr int kFewRows = 128;
 
@@ -560,8 +582,9 @@ __global__ __launch_bounds__(256) void gather_rows_fill(GatherArgs a) {
 
 // hA as above, and per active row the coefficients of
 //     dz_v = g [v == target] - p_v (a + b (z_v - lse)),  p_v = e(z_v - lse):
-// rowinfo = {lse, a, b, target (bits)}, rowg = g; {0, 0, 0, -1} past n_act.  top: a = g + b entropy, b = dL/dentropy.  distill: a = -(dL/dloss
-// / temperature), b = 0, no target; the teacher's share of dz comes from
+// rowinfo = {lse, a, b, target (bits)}, rowg = g; {0, 0, 0, -1} past n_act.
+// top: a = g + b entropy, b = dL/dentropy.  distill: a = -(dL/dloss /
+// temperature), b = 0, no target; the teacher's share of dz comes from
 // distill_scatter.  A row without a defined loss (a target, or a kept
 // teacher's token, outside the vocabulary) gets NaN coefficients.
 struct GatherGradArgs {
@@ -646,7 +669,8 @@ __device__ __forceinline__ float wave_sum(float x) {
 }
 
 // A teacher's row over a wave: lane l holds slots l and l + 64.
-// q = softmax of the kept logits / temperature, lq = log q.
+// q = softmax of the kept logits / temperature, lq = log q.  (distill_rows of
+// 4096 rows: 4 us.)
 constexpr int kSlots2 = kMaxK / 64;
 struct TeacherRow {
   int id[kSlots2];
@@ -805,8 +829,11 @@ __global__ __launch_bounds__(kBucketThreads) void bucket_entries(const int32_t* 
 // forms of these loops, which run through their code once, took 54 us where
 // the rolled ones below take 17 (20 alternatives, V = 151936).  So loops stay
 // rolled, what is loaded ahead goes through LDS, and only the loads are
-// unrolled.  A chunk's records of neighbouring rows share cache lines, so a
-// die takes consecutive rows (xcd_tile).
+// unrolled.  With the fold in a wave of its own one row takes 20 - 21 us with
+// its alternatives.  A chunk's records of neighbouring rows share cache lines,
+// so a die takes consecutive rows (xcd_tile): 4096 rows, 20 alternatives, 108
+// us (60 MB of records and about 21 of a row's 1216 chunks); 3482 rows'
+// divergences 37 us.
 // ---------------------------------------------------------------------------
 // The lanes of a wave see one another's LDS writes.
 __device__ __forceinline__ void wave_lds_sync() {
@@ -1221,6 +1248,9 @@ __global__ __launch_bounds__(64) void distill_merge(DistillMergeArgs a) {
 // z scaled by 1 / temperature.  fp32, each operation rounded once, then bf16
 // once: dz is an operand of the gradients' bf16 products.
 // kTop: with target and b; !kTop: a alone.
+// Bound by the engine's MFMAs: 3482 active rows, H = 4096 (4.33 TFLOP) 2.95 -
+// 3.0 ms (1.44 - 1.47 PFLOP/s), 3 % above the logits of the forward (1.1 GB
+// of dz).
 // ---------------------------------------------------------------------------
 struct SoftDzArgs {
   const uint16_t* hA;
@@ -1343,7 +1373,8 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(RLK_WA
 // dz at the teacher's tokens of the group: a (q - p) with a = -dL/dloss /
 // temperature and p = e(log p) of the forward.  A token in several slots of
 // a row has the sum of their q, in slot order, written by the first of them.
-// Block kMaxK, one thread per slot, rows strided over the grid.
+// Block kMaxK, one thread per slot, rows strided over the grid.  Scattered
+// two-byte stores into dz, 64 a row: 4096 rows 16 us, 257 rows 11.
 struct ScatterArgs {
   const int32_t* ids;
   const float* q;         // [T][K], 0 for slots that are not kept
@@ -1401,7 +1432,9 @@ __global__ __launch_bounds__(kMaxK) void distill_scatter(ScatterArgs a) {
 // ms.  (linear_logp_bwd keeps the one chain: its bits are its contract.)
 // Four parts there: both gradients of that batch in 0.98 ms, of 4096 rows
 // (3482 active) in 6.63 ms with grad_h_sum; two parts 1.68 and 6.49, eight
-// 0.99 and 6.73 (the parts' sums pass through HBM).
+// 0.99 and 6.73 (the parts' sums pass through HBM).  3482 active rows: 6.23 -
+// 6.33 ms for 8.67 TFLOP (1.37 - 1.39 PFLOP/s), bound by MFMAs and by the
+// transposing reads of both products' operands.
 // ---------------------------------------------------------------------------
 constexpr int kMaxParts = kNSplit;
 
@@ -1571,7 +1604,7 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(RLK_WA
 // grad_W has its size), and the 256 x 256 tiles leave that far off: 64 of
 // them for grad_h at H = 4096, each as long as its part, and for grad_W one
 // tile at a time per compute unit, loads, MFMAs and stores in turn.  Together
-// they took 0.92 ms at 64 rows (V = 151936).
+// they took 0.92 ms at 64 rows of H = 4096; the kernels below take 0.52.
 // ---------------------------------------------------------------------------
 // Eight k of one column for each lane, from two transposing reads: `base` is
 // where the lane's 4 columns of k-row 8 (l / 16) + (l % 16) / 4 lie, kr the
@@ -1588,8 +1621,10 @@ __device__ __forceinline__ bf16x8 tr_frag(const char* base, uint32_t kr4) {
 // the part's W through a ring of kSlots LDS stages of 64 vocabulary rows
 // (8 KB, and the dz block they meet), kSlots - 1 in flight.  Its four waves
 // take 16 columns each, or (above 64 rows, where reading dz from LDS counts)
-// 32 columns and half of the rows.  The same chains as
-// gradh_part_tile.
+// 32 columns and half of the rows.  The same chains as gradh_part_tile.
+// Bound by W's way from HBM up to 64 rows: 257 - 274 us at H = 4096 (4.5 - 4.8
+// TB/s), 126 - 140 at 2048; above, by reading dz from LDS: 354 and 181 at 128
+// rows.  A form for 256 rows took 544.
 // A stage: W as 64 k-rows of 128 bytes, 32-byte units xor-ed with
 // (row >> 1 & 1) + 2 (row >> 3 & 1): the 8 k-rows of a transposing pass fall
 // on distinct banks; dz as rows of 128 bytes in the engine's K layout (slot_k).
@@ -1716,8 +1751,14 @@ __global__ __launch_bounds__(256) void few_grad_h(FewGradHArgs a) {
 // and all of H, 128 columns at a time; its four waves take 64 x 64 of that
 // each.  dz's fragments are read once, through LDS, and stay in registers
 // (32 kKB of them); h comes in stages of 64 rows x 128 columns, two LDS slots.
+// Block b starts with the b-th 128 columns: rows of grad_W lie 2 H or 4 H bytes
+// apart, and blocks in step would all write to the same few memory channels.
 // Several blocks per compute unit overlap one's stores with another's loads
 // and MFMAs.  The same chains as gradw_tile (rows ascending).
+// Bound by grad_W's stores: bf16, up to 128 rows, 250 us at H = 4096 (5.0 TB/s;
+// 300 with all blocks starting at column 0), 111 - 134 at 2048.  A form for
+// 256 rows took 480 beside the tiles' 950 for both gradients, of which grad_h
+// alone is 745.
 // A lane's columns of an MFMA block are free to choose, four by four.  For a
 // bf16 grad_W block n of a wave's four takes, in lanes r = l / 16, columns
 // 32 (n / 2) + 8 r + 4 (n % 2) .. + 3: two blocks make 8 consecutive columns
@@ -1789,7 +1830,8 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2))) void f
   }
   loads_then_barrier<0>();  // every wave has its fragments: the slots are free
   const int steps = (a.H + 127) / 128;
-  int l_n = 0, l_k = 0;
+  const int first = (int)blockIdx.x % steps;
+  int l_n = first, l_k = 0;
   const auto load = [&](uint32_t slot) {
     const char* base = hb + (size_t)l_k * 128 * a.H;
 #pragma unroll
@@ -1797,7 +1839,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2))) void f
       dma16(base, h_off[i] + 2u * (uint32_t)min(128 * l_n + 8 * h_piece[i], a.H - 8), slot + 1024u * (4 * w + i));
     if (++l_k >= kb) {
       l_k = 0;
-      if (l_n + 1 < steps) ++l_n;
+      l_n = l_n + 1 < steps ? l_n + 1 : 0;
     }
   };
   load(lds0);
@@ -1805,7 +1847,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2))) void f
   Out* out = reinterpret_cast<Out*>(a.grad_W) + (size_t)(sbeg + v0) * a.H;
   uint32_t slot = 0;
 #pragma unroll 1
-  for (int n = 0; n < steps; ++n) {
+  for (int i = 0, n = first; i < steps; ++i, n = n + 1 < steps ? n + 1 : 0) {
     AccBlk acc[4][4];
 #pragma unroll
     for (int m = 0; m < 4; ++m)
@@ -1859,7 +1901,8 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2))) void f
 
 // grad_h[idx[i]] = the parts' sum, left to right, rounded to bf16 once; zero
 // rows for inactive rows.  Block b takes active row b and row b of the batch
-// (idx NULL: they are the same).
+// (idx NULL: they are the same).  HBM: 3482 rows of four parts, H = 4096 (0.26
+// GB), 57 us.
 __global__ __launch_bounds__(256) void grad_h_sum(const float* __restrict__ part, size_t part_stride, int parts,
                                                   const int32_t* __restrict__ idx,
                                                   const int32_t* __restrict__ n_act_p, const int32_t* __restrict__ act,

@@ -16,7 +16,7 @@
 namespace rlk {
 namespace vocab {
 
-// Zeroes n 16-byte words and the bytes after them (T == 0: grad_W).
+// Zeroes n16 16-byte words (T == 0: grad_W).
 __global__ __launch_bounds__(256) void zero_bytes(u32x4* p, int64_t n16) {
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n16; i += (int64_t)gridDim.x * 256)
     p[i] = u32x4{0u, 0u, 0u, 0u};
@@ -394,9 +394,9 @@ rlk_status run_distill_fwd(const void* h, const void* W, const int32_t* ids, con
 }
 
 #if RLK_MFMA == 16
-// Both gradients in their few-row kernels up to kFewRows rows: 0.66 ms
+// Both gradients in their few-row kernels up to kFewRows rows: 0.60 ms
 // together at 128 rows (H = 4096, V = 151936) against the tiles' 0.94; forms
-// for 256 rows took 1.09 against 0.95.
+// for 256 rows took 1.02 against 0.95.
 rlk_status launch_few_grad_h(const FewGradHArgs& a, int64_t T, bool cont, hipStream_t st) {
   typedef void (*Fn)(FewGradHArgs);
   static constexpr Fn fns[2][4] = {
