@@ -1447,21 +1447,31 @@ struct PartGradHArgs {
   int n_tiles;         // 256-column tiles of H
   int per;             // splits of a part
   int part0, parts;    // parts of the group: part0 .. part0 + parts - 1
+  int cus;
   float* part;         // [part][T][H], rows in active order; NULL: not wanted
   size_t part_stride;  // T * H
 };
 
+// At most a tile for every fourth compute unit (up to 256 rows): they are cut
+// into their two 128-column halves.  Both gradients at 256 rows: 0.96 -> 0.85
+// ms (H = 4096), 0.48 -> 0.42 (2048).  A half's loads are a tile's, and twice
+// the tiles cut so cost: 257 rows 0.98 -> 1.17, 512 rows 1.15 -> 1.38.
+__device__ __forceinline__ bool cut_tiles(int n, int cus) { return 4 * n <= cus; }
+
 // kCont: the group starts inside its (one) part.
 template <bool kCont>
-__device__ __forceinline__ void gradh_part_tile(const PartGradHArgs& a, int id, int rtiles, int n_act, u32x4* lds) {
+__device__ __forceinline__ void gradh_part_tile(const PartGradHArgs& a, int id, int half, int rtiles, int n_act,
+                                                u32x4* lds) {
   const int per = rtiles * a.n_tiles;
   const int q = __builtin_amdgcn_readfirstlane(id / per);  // part within the group
   int rt, nt;
   grouped_tile(id - q * per, rtiles, rt, nt, a.n_tiles, row_group(rtiles));
   rt = __builtin_amdgcn_readfirstlane(rt);  // (tile addresses derive from them)
   nt = __builtin_amdgcn_readfirstlane(nt);
-  const int i0 = rt * kBM, n0 = nt * kBN;
-  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, wm = wave_m(w), wn = wave_n(w);
+  const int i0 = rt * kBM, n0 = nt * kBN + 128 * max(half, 0), n1 = min(n0 + (half < 0 ? kBN : 128), a.H);
+  if (n0 >= n1) return;
+  const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), wm = wave_m(w),
+            wn = wave_n(w);
   float* part = a.part + (size_t)(a.part0 + q) * a.part_stride;
   Acc acc;
   acc_zero(acc);
@@ -1499,8 +1509,12 @@ __device__ __forceinline__ void gradh_part_tile(const PartGradHArgs& a, int id, 
   B.V = a.gm.V;
 #pragma unroll
   for (int i = 0; i < kDma; ++i) {
-    B.col2[i] = 2 * (min(n0 + dma_mn_piece(dma_mn_krow(i)) * 8, a.H - 8) - n0);
+    B.col2[i] = 2 * (min(n0 + dma_mn_piece(dma_mn_krow(i)) * 8, n1 - 8) - n0);
     B.krow[i] = (uint32_t)dma_mn_krow(i);
+  }
+  if (half >= 0 && wn == 1) {
+    gemm256<false, true, 0>(A, B, splits * B.kbps, acc, lds);
+    return;
   }
   gemm256<false, true>(A, B, splits * B.kbps, acc, lds);
 #pragma unroll
@@ -1583,12 +1597,14 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(RLK_WA
   __shared__ u32x4 lds[kLdsU4];
   const int n_act = __builtin_amdgcn_readfirstlane(*wa.n_act);
   const int rtiles = (n_act + kBM - 1) / kBM;
-  const int nh = ha.part ? rtiles * ha.n_tiles * ha.parts : 0;
+  const int nt = ha.part ? rtiles * ha.n_tiles * ha.parts : 0;
+  const bool cut = cut_tiles(nt, ha.cus);
+  const int nh = cut ? 2 * nt : nt;
   const int nh_blocks = 8 * ((nh + 7) >> 3);
   const int bid = blockIdx.x;
   if (bid < nh_blocks) {
     const int id = xcd_tile(nh, bid);
-    if (id >= 0) gradh_part_tile<kCont>(ha, id, rtiles, n_act, lds);
+    if (id >= 0) gradh_part_tile<kCont>(ha, cut ? id >> 1 : id, cut ? id & 1 : -1, rtiles, n_act, lds);
     return;
   }
   const int nw = wa.grad_W ? wa.n_tiles * wa.bg.G * wa.tps : 0;

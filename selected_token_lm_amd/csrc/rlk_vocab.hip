@@ -443,7 +443,9 @@ rlk_status run_soft_bwd(const SoftBwd& b, const SoftBwdWs& L, void* ws, hipStrea
   const int64_t row_tiles = ceil_div(b.T, rlk::kBM);
   const int64_t dz_blocks = tile_blocks(row_tiles * G * tps, tile_units());
   const int per = part_splits(b.H, b.V), group_parts = (int)ceil_div(G, per);
-  const int64_t gh_blocks = b.grad_h ? 8 * ceil_div(row_tiles * n_tiles * group_parts, 8) : 0;
+  const int64_t gh_tiles = row_tiles * n_tiles * group_parts;  // (or up to cus / 2 halves: cut_tiles)
+  const int64_t gh_blocks =
+      b.grad_h ? 8 * ceil_div(std::max(gh_tiles, std::min<int64_t>(2 * gh_tiles, device_cus() / 2)), 8) : 0;
   const int64_t gw_blocks = b.grad_W ? 8 * ceil_div((int64_t)n_tiles * G * tps, 8) : 0;
   RLK_TRY(check_grid(dz_blocks));
   RLK_TRY(check_grid(gh_blocks + gw_blocks));
@@ -566,6 +568,7 @@ rlk_status run_soft_bwd(const SoftBwd& b, const SoftBwdWs& L, void* ws, hipStrea
     ha.bg = bg;
     ha.n_tiles = n_tiles;
     ha.per = per;
+    ha.cus = device_cus();
     ha.part0 = c / per;
     ha.parts = std::min(group_parts, last / per + 1 - ha.part0);
     ha.part = b.grad_h ? part : nullptr;

@@ -179,11 +179,11 @@ def test_tiles_in_rounds():
     check_distill(Case(300, 64, 70_000, seed=22), 30, 1.0)
 
 
-@pytest.mark.parametrize("T", [300, 40])
+@pytest.mark.parametrize("T,H", [(300, 128), (40, 128), (200, 448)])
 @pytest.mark.parametrize("budget", ["1", "2", "12", "40"])
-def test_groups_of_splits_change_no_bit(budget, T, monkeypatch):
+def test_groups_of_splits_change_no_bit(budget, T, H, monkeypatch):
     """The workspace budget sets how many splits are processed together."""
-    c = Case(T, 128, 20_011, 0.2, seed=4)
+    c = Case(T, H, 20_011, 0.2, seed=4)
     h, W = c.dev()
     y, g, ge = i32_dev(c.y), f32_dev(c.g), f32_dev(c.ge)
     n_ids, n_lg = c.teacher(20)
@@ -197,7 +197,7 @@ def test_groups_of_splits_change_no_bit(budget, T, monkeypatch):
 
     want = everything()
     monkeypatch.setenv("RLK_DZ_BUDGET_MB", budget)
-    sizes = rlk.vocab_workspace_bytes(rlk.VOP_TOP_FWD, T, 128, 20_011, 50)
+    sizes = rlk.vocab_workspace_bytes(rlk.VOP_TOP_FWD, T, H, 20_011, 50)
     say(f"[groups] budget {budget} MiB: {sizes} bytes")
     for a, b in zip(everything(), want):
         assert torch.equal(a, b)
