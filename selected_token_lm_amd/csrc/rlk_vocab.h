@@ -95,11 +95,11 @@ __device__ __forceinline__ MSU chunk_stats_moment(const float (&v)[kRowVals]) {
 //   z + i * ldz + 128 (sl cps + j).
 // !kTop: logits times `scale` (1 / temperature); the tile's entries (see
 //   bucket_entries) pick the scaled logits of the teacher's tokens.
-// Bound by the engine's MFMAs.  3482 active rows, H = 4096 (4.33 TFLOP): 2.91
-// ms (1.49 PFLOP/s) with 64 tokens of a teacher; 4096 rows (5.10 TFLOP) with
-// every logit stored 3.26 - 3.38 ms (1.51 - 1.56), 0.35 of them for the first
-// moment and the 2.5 GB of stores (the accumulators' registers leave none to
-// pick the alternatives here).  Stores that bypass the caches: 3.64.
+// Bound by the engine's MFMAs.  3482 active rows, H = 4096 (4.33 TFLOP): 2.91 -
+// 3.02 ms (1.43 - 1.49 PFLOP/s) with 64 tokens of a teacher; with the first
+// moment and every logit stored 3.38 - 3.46 ms, 0.35 of them for the 2.2 GB of
+// stores (the accumulators leave no registers to pick the alternatives here).
+// Stores that bypass the caches add 0.1 ms.
 // At 129 to 512 rows each tile waits for its loads: 256 rows 0.31 ms, 257
 // 0.44; leaving out the MFMAs of a short row tile's padding gained 3 % there
 // and is not done.
@@ -670,7 +670,7 @@ __device__ __forceinline__ float wave_sum(float x) {
 
 // A teacher's row over a wave: lane l holds slots l and l + 64.
 // q = softmax of the kept logits / temperature, lq = log q.  (distill_rows of
-// 4096 rows: 4 us.)
+// 4096 rows of 64: 4 us.)
 constexpr int kSlots2 = kMaxK / 64;
 struct TeacherRow {
   int id[kSlots2];
@@ -831,9 +831,9 @@ __global__ __launch_bounds__(kBucketThreads) void bucket_entries(const int32_t* 
 // rolled, what is loaded ahead goes through LDS, and only the loads are
 // unrolled.  With the fold in a wave of its own one row takes 20 - 21 us with
 // its alternatives.  A chunk's records of neighbouring rows share cache lines,
-// so a die takes consecutive rows (xcd_tile): 4096 rows, 20 alternatives, 108
-// us (60 MB of records and about 21 of a row's 1216 chunks); 3482 rows'
-// divergences 37 us.
+// so a die takes consecutive rows (xcd_tile): 3482 rows, 20 alternatives, 108
+// us (51 MB of records and about 21 of a row's 1216 chunks of logits each);
+// their divergences from 64 tokens 37 us.
 // ---------------------------------------------------------------------------
 // The lanes of a wave see one another's LDS writes.
 __device__ __forceinline__ void wave_lds_sync() {
@@ -1248,8 +1248,8 @@ __global__ __launch_bounds__(64) void distill_merge(DistillMergeArgs a) {
 // z scaled by 1 / temperature.  fp32, each operation rounded once, then bf16
 // once: dz is an operand of the gradients' bf16 products.
 // kTop: with target and b; !kTop: a alone.
-// Bound by the engine's MFMAs: 3482 active rows, H = 4096 (4.33 TFLOP) 2.95 -
-// 3.0 ms (1.44 - 1.47 PFLOP/s), 3 % above the logits of the forward (1.1 GB
+// Bound by the engine's MFMAs: 3482 active rows, H = 4096 (4.33 TFLOP) 3.00 -
+// 3.11 ms (1.39 - 1.44 PFLOP/s), 3 % above the logits of the forward (1.1 GB
 // of dz).
 // ---------------------------------------------------------------------------
 struct SoftDzArgs {
@@ -1374,7 +1374,7 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(RLK_WA
 // temperature and p = e(log p) of the forward.  A token in several slots of
 // a row has the sum of their q, in slot order, written by the first of them.
 // Block kMaxK, one thread per slot, rows strided over the grid.  Scattered
-// two-byte stores into dz, 64 a row: 4096 rows 16 us, 257 rows 11.
+// two-byte stores into dz, 64 a row: 3482 rows 16 us, 257 rows 11.
 struct ScatterArgs {
   const int32_t* ids;
   const float* q;         // [T][K], 0 for slots that are not kept
@@ -1432,8 +1432,8 @@ __global__ __launch_bounds__(kMaxK) void distill_scatter(ScatterArgs a) {
 // ms.  (linear_logp_bwd keeps the one chain: its bits are its contract.)
 // Four parts there: both gradients of that batch in 0.98 ms, of 4096 rows
 // (3482 active) in 6.63 ms with grad_h_sum; two parts 1.68 and 6.49, eight
-// 0.99 and 6.73 (the parts' sums pass through HBM).  3482 active rows: 6.23 -
-// 6.33 ms for 8.67 TFLOP (1.37 - 1.39 PFLOP/s), bound by MFMAs and by the
+// 0.99 and 6.73 (the parts' sums pass through HBM).  3482 active rows: 6.33 -
+// 6.55 ms for 8.67 TFLOP (1.32 - 1.37 PFLOP/s), bound by MFMAs and by the
 // transposing reads of both products' operands.
 // ---------------------------------------------------------------------------
 constexpr int kMaxParts = kNSplit;
