@@ -21,7 +21,7 @@
 // Up to 128 rows (few_rows: the batch's rows in place, no compaction) other
 // kernels give the same bits:
 //   few_tiles          for logit_tiles and soft_dz_tiles
-//   few_rows_grad      for gather_rows_grad
+//   few_rows_grad      for gather_rows_grad (and the backward's distill_rows)
 //   few_grad_h, few_grad_w   for part_grad_tiles
 //
 // Times below are of one MI355X (which copies at 4.9 TB/s, and whose library
@@ -601,13 +601,12 @@ struct GatherGradArgs {
   const int32_t* y;
   const float* entropy;
   const float* g_entropy;   // may be NULL (zero)
-  // distill
-  const int32_t* act;       // 1 where a kept token lies outside the vocabulary
+  const int32_t* act;       // top: y; distill: the rows' states (distill_row)
   float scale;
 };
 
 template <bool kTop>
-__device__ __forceinline__ float4 grad_row(const GatherGradArgs& a, int t, float* g_out) {
+__device__ __forceinline__ float4 grad_row(const GatherGradArgs& a, int t, int state, float* g_out) {
   float4 ri = make_float4(a.lse[t], 0.f, 0.f, __int_as_float(-1));
   float gt = 0.f;
   if constexpr (kTop) {
@@ -619,7 +618,7 @@ __device__ __forceinline__ float4 grad_row(const GatherGradArgs& a, int t, float
     ri.y = gt + ri.z * a.entropy[t];
     ri.w = __int_as_float(ok ? yt : -1);
   } else {
-    ri.y = a.act[t] == 1 ? __builtin_nanf("") : -(a.g[t] * a.scale);
+    ri.y = state == 1 ? __builtin_nanf("") : -(a.g[t] * a.scale);
   }
   *g_out = gt;
   return ri;
@@ -631,23 +630,7 @@ __global__ __launch_bounds__(256) void gather_rows_grad(GatherGradArgs a) {
   for (int i = blockIdx.x; i < a.rows; i += gridDim.x) {
     gather_row(a.h, a.idx, n_act, i, a.H, a.hA);
     if (threadIdx.x == 0)
-      a.rowinfo[i] = i < n_act ? grad_row<kTop>(a, a.idx[i], a.rowg + i) : make_float4(0.f, 0.f, 0.f, __int_as_float(-1));
-  }
-}
-
-// Few rows: the batch's rows in place.  hA[t] = h[t], zeros for inactive rows
-// and past T (they meet dz = 0 in grad_W, and may hold anything in h);
-// n_act = T.  Grid: `rows` blocks.
-template <bool kTop>
-__global__ __launch_bounds__(256) void few_rows_grad(GatherGradArgs a, int T, int ignore_index, int32_t* n_act) {
-  const int t = blockIdx.x;
-  const bool on = t < T && a.act[t] != ignore_index;
-  u32x4* dst = reinterpret_cast<u32x4*>(a.hA + (size_t)t * a.H);
-  const u32x4* src = reinterpret_cast<const u32x4*>(a.h + (size_t)t * a.H);
-  for (int p = threadIdx.x; p < a.H / 8; p += 256) dst[p] = on ? src[p] : u32x4{0u, 0u, 0u, 0u};
-  if (threadIdx.x == 0) {
-    a.rowinfo[t] = on ? grad_row<kTop>(a, t, a.rowg + t) : make_float4(0.f, 0.f, 0.f, __int_as_float(kNoRow));
-    if (t == 0) *n_act = T;
+      a.rowinfo[i] = i < n_act ? grad_row<kTop>(a, a.idx[i], kTop ? 0 : a.act[a.idx[i]], a.rowg + i) : make_float4(0.f, 0.f, 0.f, __int_as_float(-1));
   }
 }
 
@@ -711,24 +694,76 @@ __device__ __forceinline__ TeacherRow teacher_row(const int32_t* ids, const floa
   return r;
 }
 
-// act[t] = -100 for rows without a kept token, 1 for rows with a kept token
-// outside the vocabulary, else 0; q (optional) = the teacher's distribution.
-// One wave per row.
+// The state of row t over a wave: -100 without a kept token, 1 with a kept
+// token outside the vocabulary, else 0; q (optional): the teacher's
+// distribution.
+__device__ __forceinline__ int distill_row(const int32_t* ids, const float* logits, int t, int K, int V, float scale,
+                                           float* q) {
+  const int lane = threadIdx.x & 63;
+  const TeacherRow r = teacher_row(ids + (size_t)t * K, logits + (size_t)t * K, K, scale);
+  bool any = false, out = false;
+#pragma unroll
+  for (int s = 0; s < kSlots2; ++s) {
+    any |= r.kept[s];
+    out |= r.kept[s] && r.id[s] >= V;
+    if (q && lane + 64 * s < K) q[(size_t)t * K + lane + 64 * s] = r.q[s];
+  }
+  const bool any_w = __builtin_amdgcn_ballot_w64(any) != 0, out_w = __builtin_amdgcn_ballot_w64(out) != 0;
+  return !any_w ? -100 : out_w ? 1 : 0;
+}
+
+// act[t] = the rows' states.  One wave per row.
 __global__ __launch_bounds__(256) void distill_rows(const int32_t* __restrict__ ids, const float* __restrict__ logits,
                                                     int T, int K, int V, float scale, int32_t* __restrict__ act,
                                                     float* __restrict__ q) {
-  const int lane = threadIdx.x & 63;
   for (int t = blockIdx.x * 4 + (threadIdx.x >> 6); t < T; t += gridDim.x * 4) {
-    const TeacherRow r = teacher_row(ids + (size_t)t * K, logits + (size_t)t * K, K, scale);
-    bool any = false, out = false;
-#pragma unroll
-    for (int s = 0; s < kSlots2; ++s) {
-      any |= r.kept[s];
-      out |= r.kept[s] && r.id[s] >= V;
-      if (q && lane + 64 * s < K) q[(size_t)t * K + lane + 64 * s] = r.q[s];
+    const int state = distill_row(ids, logits, t, K, V, scale, q);
+    if ((threadIdx.x & 63) == 0) act[t] = state;
+  }
+}
+
+// Few rows: the batch's rows in place.  hA[t] = h[t], zeros for inactive rows
+// and past T (they meet dz = 0 in grad_W, and may hold anything in h);
+// n_act = T.  distill: wave 0 finds the row's state first (and act, q for the
+// kernels after this one).  Grid: `rows` blocks.
+struct FewRowsArgs {
+  GatherGradArgs ga;
+  int T, ignore_index;
+  int32_t* n_act;
+  // distill
+  const int32_t* ids;
+  const float* logits;
+  int K;
+  int32_t* act;  // = ga.act
+  float* q;
+};
+
+template <bool kTop>
+__global__ __launch_bounds__(256) void few_rows_grad(FewRowsArgs f) {
+  __shared__ int state_s;
+  const GatherGradArgs& a = f.ga;
+  const int t = blockIdx.x;
+  int state = f.ignore_index;
+  if constexpr (kTop) {
+    if (t < f.T) state = a.act[t];
+  } else {
+    if (threadIdx.x < 64) {
+      if (t < f.T) {
+        state = distill_row(f.ids, f.logits, t, f.K, a.V, a.scale, f.q);
+        if (threadIdx.x == 0) f.act[t] = state;
+      }
+      if (threadIdx.x == 0) state_s = state;
     }
-    const bool any_w = __builtin_amdgcn_ballot_w64(any) != 0, out_w = __builtin_amdgcn_ballot_w64(out) != 0;
-    if (lane == 0) act[t] = !any_w ? -100 : out_w ? 1 : 0;
+    __syncthreads();
+    state = state_s;
+  }
+  const bool on = t < f.T && state != f.ignore_index;
+  u32x4* dst = reinterpret_cast<u32x4*>(a.hA + (size_t)t * a.H);
+  const u32x4* src = reinterpret_cast<const u32x4*>(a.h + (size_t)t * a.H);
+  for (int p = threadIdx.x; p < a.H / 8; p += 256) dst[p] = on ? src[p] : u32x4{0u, 0u, 0u, 0u};
+  if (threadIdx.x == 0) {
+    a.rowinfo[t] = on ? grad_row<kTop>(a, t, state, a.rowg + t) : make_float4(0.f, 0.f, 0.f, __int_as_float(kNoRow));
+    if (t == 0) *f.n_act = f.T;
   }
 }
 

@@ -449,14 +449,14 @@ rlk_status run_soft_bwd(const SoftBwd& b, const SoftBwdWs& L, void* ws, hipStrea
   const int64_t gw_blocks = b.grad_W ? 8 * ceil_div((int64_t)n_tiles * G * tps, 8) : 0;
   RLK_TRY(check_grid(dz_blocks));
   RLK_TRY(check_grid(gh_blocks + gw_blocks));
-  if (!top)
-    RLK_LAUNCH_V(distill_rows, row_grid(ceil_div(b.T, 4)), dim3(256), st, b.ids, b.logits, (int)b.T, (int)b.K,
-                 (int)b.V, b.scale, at<int32_t>(ws, L.act), at<float>(ws, L.q));
 #if RLK_MFMA == 16
   const bool few = b.T <= kFewRows;
 #else
   const bool few = false;
 #endif
+  if (!top && !few)
+    RLK_LAUNCH_V(distill_rows, row_grid(ceil_div(b.T, 4)), dim3(256), st, b.ids, b.logits, (int)b.T, (int)b.K,
+                 (int)b.V, b.scale, at<int32_t>(ws, L.act), at<float>(ws, L.q));
   if (few) idx = nullptr;  // the batch's rows in place
   else RLK_TRY(compact(st, b.act, b.T, b.ignore, idx, nullptr, n_act, nullptr, nullptr, nullptr));
   GatherGradArgs ga{};
@@ -477,13 +477,20 @@ rlk_status run_soft_bwd(const SoftBwd& b, const SoftBwdWs& L, void* ws, hipStrea
   ga.act = b.act;
   ga.scale = b.scale;
 #if RLK_MFMA == 16
-  const dim3 few_grid(kFewRows);
+  FewRowsArgs ra{};
+  ra.ga = ga;
+  ra.T = (int)b.T;
+  ra.ignore_index = b.ignore;
+  ra.n_act = n_act;
+  ra.ids = b.ids;
+  ra.logits = b.logits;
+  ra.K = (int)b.K;
+  ra.act = at<int32_t>(ws, L.act);
+  ra.q = at<float>(ws, L.q);
   if (few && top)
-    RLK_LAUNCH_FN("few_rows_grad", (rlk::vocab::few_rows_grad<true>), few_grid, dim3(256), st, ga, (int)b.T, b.ignore,
-                  n_act);
+    RLK_LAUNCH_FN("few_rows_grad", (rlk::vocab::few_rows_grad<true>), dim3(kFewRows), dim3(256), st, ra);
   else if (few)
-    RLK_LAUNCH_FN("few_rows_grad", (rlk::vocab::few_rows_grad<false>), few_grid, dim3(256), st, ga, (int)b.T, b.ignore,
-                  n_act);
+    RLK_LAUNCH_FN("few_rows_grad", (rlk::vocab::few_rows_grad<false>), dim3(kFewRows), dim3(256), st, ra);
   else
 #endif
   if (top)
