@@ -101,8 +101,7 @@ __device__ __forceinline__ MSU chunk_stats_moment(const float (&v)[kRowVals]) {
 // stores (the accumulators leave no registers to pick the alternatives here).
 // Stores that bypass the caches add 0.1 ms.
 // At 129 to 512 rows each tile waits for its loads: 256 rows 0.31 ms, 257
-// 0.44; leaving out the MFMAs of a short row tile's padding gained 3 % there
-// and is not done.
+// 0.40 (see gemm_rows).
 // ---------------------------------------------------------------------------
 struct LogitArgs {
   const uint16_t* hA;  // active rows of h, compacted, zero padded to a multiple of 256
@@ -145,9 +144,49 @@ __device__ __forceinline__ bool tile_of_block(int n, int cus, int bid, int& id, 
   return true;
 }
 
+// Row block b (kBlk rows) of a tile of logits or dz is block b / kWM of wave
+// row b % kWM: the row blocks of a last, short row tile are spread over the
+// SIMDs, and the waves leave out the others (gemm_rows).
+__device__ __forceinline__ int spread_block(int wm, int mi) { return kWM * mi + wm; }
+__device__ __forceinline__ int spread_row(int wm, int mi, int lane) { return kBlk * spread_block(wm, mi) + lane % kBlk; }
+
+// rows_k in that order.  Rows past `last` repeat it: 257 rows of H = 4096 lose
+// their second tile's other row blocks' MFMAs and, in L2, its 255 other rows
+// (each alone gains 2 % or nothing, both 10: 0.44 -> 0.40 ms; 300 rows of H =
+// 2048 by half of V 0.158 -> 0.143).
+__device__ __forceinline__ RowsK rows_k_spread(const uint16_t* base, int last, int ld) {
+  RowsK R;
+  R.base = reinterpret_cast<const char*>(base);
+#pragma unroll
+  for (int i = 0; i < kDma; ++i) {
+    const int row = dma_k_row(i), b = row / kBlk;
+    const int at = min(kBlk * spread_block(b / kMI, b % kMI) + row % kBlk, last);
+    R.off[i] = (uint32_t)(2 * ((size_t)at * ld + dma_k_seg(row) * 8));
+  }
+  return R;
+}
+
+// The tile product of a wave of which `rows` rows of the tile are wanted: the
+// wave's blocks of them, up to a power of two.  Every element computed is the
+// same MFMA chain.
+template <class LA, class LB, class Tail>
+__device__ __forceinline__ void gemm_rows(const LA& A, const LB& B, int nk, Acc& acc, u32x4* lds, int wm, int rows,
+                                          const Tail& tail) {
+  const int blocks = (rows + kBlk - 1) / kBlk, mine = max(0, (blocks - wm + kWM - 1) / kWM);
+  if (mine == 0) {
+    gemm256<false, false, 0>(A, B, nk, acc, lds, tail);
+  } else if (mine == 1) {
+    gemm256<false, false, 1>(A, B, nk, acc, lds, tail);
+  } else if (mine == 2 && kMI > 2) {
+    gemm256<false, false, kMI / 2>(A, B, nk, acc, lds, tail);
+  } else {
+    gemm256<false, false>(A, B, nk, acc, lds, tail);
+  }
+}
+
 // Teacher's tokens are sorted in groups of kBucketRows rows (bucket_entries).
 constexpr int kBucketRows = 32;
-static_assert(kWaveRows % kBucketRows == 0 && kBucketRows % kBlk == 0, "a row group is whole row blocks of one wave");
+static_assert(kBM % kBucketRows == 0 && kBucketRows % kBlk == 0, "a row group is whole row blocks");
 
 // An entry: column and row within the tile, slot of the row.
 __device__ __forceinline__ uint32_t entry_of(int col, int row, int k) { return (uint32_t)(col | row << 8 | k << 16); }
@@ -177,13 +216,13 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(RLK_WA
   // this lane's rows' targets, loaded as in fwd_tiles
   int tgt[kMI];
   const auto load_row = [&](int mi, int ln) {
-    if constexpr (kTop) tgt[mi] = a.yA[min(i0 + acc_row(wm, mi, ln), n_act - 1)];
+    if constexpr (kTop) tgt[mi] = a.yA[min(i0 + spread_row(wm, mi, ln), n_act - 1)];
   };
   const auto load_rows = [&]() {
 #pragma unroll
     for (int mi = 0; mi < kTailRows; ++mi) load_row(mi, lane);
   };
-  const RowsK A = rows_k(a.hA + (size_t)i0 * a.H, kBM - 1, a.H);
+  const RowsK A = rows_k_spread(a.hA + (size_t)i0 * a.H, min(n_act - i0, kBM) - 1, a.H);
   const RowsK B = rows_k(a.W + (size_t)c0 * a.H, c1 - 1 - c0, a.H);
   Acc acc;
   acc_zero(acc);
@@ -191,7 +230,7 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(RLK_WA
     gemm256<false, false, 0>(A, B, a.H / kBK, acc, lds);
     return;
   }
-  gemm256<false, false>(A, B, a.H / kBK, acc, lds, load_rows);
+  gemm_rows(A, B, a.H / kBK, acc, lds, wm, min(n_act - i0, kBM), load_rows);
 
   const int cc0 = c0 + kChunk * wn;  // this wave's chunk
   const int width = min(cc0 + kChunk, c1) - cc0;
@@ -215,7 +254,9 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(RLK_WA
   };
 #pragma unroll
   for (int mi = 0; mi < kMI; ++mi) {
-    const int i = i0 + acc_row(wm, mi, le);
+    const int b = spread_block(wm, mi), i_mi = i0 + kBlk * b;  // the row block and its first row
+    if (i_mi >= n_act) continue;
+    const int i = i_mi + le % kBlk;
     __builtin_amdgcn_sched_barrier(0);
     float v[kRowVals];
 #pragma unroll
@@ -251,13 +292,11 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(RLK_WA
       }
     } else {
       bool staged = false;
-      const int i_mi = i0 + kWaveRows * wm + kBlk * mi;  // first row of the block
-      if (i_mi >= n_act) continue;
-      if (mi * kBlk % kBucketRows == 0) entries(i_mi / kBucketRows);
+      entries(i_mi / kBucketRows);
       for (int eb = e0; eb < e1; eb += 64) {
         const uint32_t x = eb + le < e1 ? ent[eb + le] : 0u;
         const int row = (x >> 8) & 255, col = x & 255;
-        const bool mine = eb + le < e1 && row / kBlk == kMI * wm + mi && (col >> 7) == ch;
+        const bool mine = eb + le < e1 && row / kBlk == b && (col >> 7) == ch;
         if (!__builtin_amdgcn_ballot_w64(mine)) continue;
         if (!staged) {
           stage();
@@ -1328,11 +1367,13 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(RLK_WA
   float4 ri[kMI];  // loaded as in dz_tiles
   const auto load_rows = [&]() {
 #pragma unroll
-    for (int mi = 0; mi < kTailRows; ++mi) ri[mi] = a.rowinfo[i0 + acc_row(wm, mi, lane)];
+    for (int mi = 0; mi < kTailRows; ++mi) ri[mi] = a.rowinfo[i0 + spread_row(wm, mi, lane)];
   };
   // a tile past the vocabulary runs on W's first row and is written as zeros
-  const RowsK A = rows_k(a.hA + (size_t)i0 * a.H, kBM - 1, a.H);
+  const RowsK A = rows_k_spread(a.hA + (size_t)i0 * a.H, min(n_act - i0, kBM) - 1, a.H);
   const RowsK B = c0 < c1 ? rows_k(a.W + (size_t)c0 * a.H, c1 - 1 - c0, a.H) : rows_k(a.W, 0, a.H);
+  // rows whose dz is written: zeros up to a k-block of grad_W's product
+  const int rows = min(n_act - i0, kBM), rows_out = (rows + kBK - 1) / kBK * kBK;
   char* stage = reinterpret_cast<char*>(lds);
   int le = lane;  // an opaque copy, see fwd_tiles
   Acc acc;
@@ -1341,10 +1382,10 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(RLK_WA
     gemm256<false, false, 0>(A, B, a.H / kBK, acc, lds);
     asm volatile("" : "+v"(le));
   } else {
-    gemm256<false, false>(A, B, a.H / kBK, acc, lds, load_rows);
+    gemm_rows(A, B, a.H / kBK, acc, lds, wm, rows, load_rows);
     asm volatile("" : "+v"(le));
 #pragma unroll
-    for (int mi = kTailRows; mi < kMI; ++mi) ri[mi] = a.rowinfo[i0 + acc_row(wm, mi, le)];
+    for (int mi = kTailRows; mi < kMI; ++mi) ri[mi] = a.rowinfo[i0 + spread_row(wm, mi, le)];
     // staging in LDS as in dz_tiles: 256 rows x 512 bytes, 16-byte unit u of row r at r * 512 + 16 (u ^ (r & 31))
     auto put = [&](int r, int c, const float (&d)[4]) {
       const uint32_t off = 512u * r + 16u * ((c >> 3) ^ (r & 31)) + 8u * ((c >> 2) & 1);
@@ -1352,15 +1393,16 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(RLK_WA
     };
     const auto share = [&](float z, const float4& r) { return minus_share<kTop>(kTop ? z : z * a.scale, r); };
     const int wc0 = t0 + 128 * wn;  // first column of the wave within the split
-    const bool full = i0 + kWaveRows * wm + kWaveRows <= n_act && wc0 + 128 <= valid_s;
+    const bool full_c = wc0 + 128 <= valid_s;
 #pragma unroll
     for (int mi = 0; mi < kMI; ++mi) {
-      const int r = acc_row(wm, mi, le);
+      const int r0 = kBlk * spread_block(wm, mi), r = r0 + le % kBlk;  // the row block's first row, this lane's
+      if (r0 >= rows_out) continue;
       const bool rvalid = i0 + r < n_act;
       const int yl = kTop ? __float_as_int(ri[mi].w) - sbeg : -1;  // target column within the split
       const int tl = yl - wc0;
       const bool hit = kTop && tl >= 0 && tl < 128 && ((tl >> 2) & (kLPR - 1)) == row_lane(le);
-      if (full && !__builtin_amdgcn_ballot_w64(hit)) {
+      if (full_c && r0 + kBlk <= rows && !__builtin_amdgcn_ballot_w64(hit)) {
 #pragma unroll
         for (int ni = 0; ni < kNI; ++ni)
 #pragma unroll
@@ -1399,6 +1441,7 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(RLK_WA
 #pragma unroll
     for (int it = 0; it < kRowsW / 2; ++it) {
       const int r = kRowsW * w + 2 * it + (le >> 5);
+      if (r >= rows_out) continue;
       const u32x4 v = *reinterpret_cast<const u32x4*>(stage + 512u * r + 16u * (u ^ (r & 31)));
       __builtin_nontemporal_store(v, reinterpret_cast<u32x4*>(dzs + (size_t)(i0 + r) * a.bg.ldz + col));
     }
