@@ -153,7 +153,7 @@ __device__ __forceinline__ int spread_row(int wm, int mi, int lane) { return kBl
 // rows_k in that order.  Rows past `last` repeat it: 257 rows of H = 4096 lose
 // their second tile's other row blocks' MFMAs and, in L2, its 255 other rows
 // (each alone gains 2 % or nothing, both 10: 0.44 -> 0.40 ms; 300 rows of H =
-// 2048 by half of V 0.158 -> 0.143).
+// 2048 by half of V 0.158 -> 0.136).  grad_h's tiles have no registers for it.
 __device__ __forceinline__ RowsK rows_k_spread(const uint16_t* base, int last, int ld) {
   RowsK R;
   R.base = reinterpret_cast<const char*>(base);
@@ -1576,7 +1576,10 @@ __device__ __forceinline__ void gradh_part_tile(const PartGradHArgs& a, int id, 
 #pragma unroll
     for (int ni = 0; ni < kNI; ++ni) asm volatile("" : "+a"(acc.c[mi][ni]));
   const int s0 = q * a.per, splits = min(a.per, a.bg.G - s0);  // of the group
-  const RowsK A = rows_k(a.dZ + (size_t)i0 * a.bg.ldz + (size_t)s0 * a.bg.S_pad, kBM - 1, a.bg.ldz);
+  // (a lone row tile does not fetch its padding: both gradients of 130 rows of
+  // H = 4096 0.83 -> 0.72 ms; a second tile's gains nothing: 257 rows 0.97 -> 0.98)
+  const RowsK A = rows_k(a.dZ + (size_t)i0 * a.bg.ldz + (size_t)s0 * a.bg.S_pad, rtiles > 1 ? kBM - 1 : n_act - 1,
+                         a.bg.ldz);
   WRowsMN B;
   B.base = reinterpret_cast<const char*>(a.W + n0);
   B.H = a.H;
