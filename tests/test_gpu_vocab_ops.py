@@ -203,10 +203,11 @@ def test_groups_of_splits_change_no_bit(budget, T, H, monkeypatch):
         assert torch.equal(a, b)
 
 
-def test_a_row_does_not_depend_on_its_batch():
+@pytest.mark.parametrize("H", [128, 448])
+def test_a_row_does_not_depend_on_its_batch(H):
     """Alone, in a small batch, in a large one, in another order: the same
     bits, grad_h among them; and twice the same."""
-    c = Case(700, 128, 6001, 0.1, seed=9)
+    c = Case(700, H, 6001, 0.1, seed=9)
     h, W = c.dev()
     y, g, ge = i32_dev(c.y), f32_dev(c.g), f32_dev(c.ge)
     n_ids, n_lg = c.teacher(30)
@@ -224,7 +225,7 @@ def test_a_row_does_not_depend_on_its_batch():
     want = rows(every)
     assert all(torch.equal(a, b) for a, b in zip(rows(every), want))
     r = np.random.Generator(np.random.PCG64(1))
-    for n in (1, 2, 17, 48, 65, 97, 256, 300):
+    for n in (1, 2, 17, 48, 65, 97, 145, 190, 256, 285, 290, 300, 340, 400, 500):
         at = torch.from_numpy(r.permutation(700)[:n].copy()).to(DEV)
         say(f"[batch] {n} rows")
         for a, b in zip(rows(at), want):
