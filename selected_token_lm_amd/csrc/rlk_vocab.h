@@ -624,8 +624,8 @@ __global__ __launch_bounds__(256) void gather_rows_fill(GatherArgs a) {
 // rowinfo = {lse, a, b, target (bits)}, rowg = g; {0, 0, 0, -1} past n_act.
 // top: a = g + b entropy, b = dL/dentropy.  distill: a = -(dL/dloss /
 // temperature), b = 0, no target; the teacher's share of dz comes from
-// distill_scatter.  A row without a defined loss (a target, or a kept
-// teacher's token, outside the vocabulary) gets NaN coefficients.
+// distill_scatter.  A row without a defined loss (a target outside the
+// vocabulary; see distill_row) gets NaN coefficients.
 struct GatherGradArgs {
   const uint16_t* h;
   const int32_t* idx;
@@ -733,9 +733,9 @@ __device__ __forceinline__ TeacherRow teacher_row(const int32_t* ids, const floa
   return r;
 }
 
-// The state of row t over a wave: -100 without a kept token, 1 with a kept
-// token outside the vocabulary, else 0; q (optional): the teacher's
-// distribution.
+// The state of row t over a wave: -100 without a kept token, 1 where the loss
+// is undefined (a kept token outside the vocabulary, or a logit that makes q
+// NaN), else 0; q (optional): the teacher's distribution.
 __device__ __forceinline__ int distill_row(const int32_t* ids, const float* logits, int t, int K, int V, float scale,
                                            float* q) {
   const int lane = threadIdx.x & 63;
@@ -744,7 +744,7 @@ __device__ __forceinline__ int distill_row(const int32_t* ids, const float* logi
 #pragma unroll
   for (int s = 0; s < kSlots2; ++s) {
     any |= r.kept[s];
-    out |= r.kept[s] && r.id[s] >= V;
+    out |= r.kept[s] && (r.id[s] >= V || r.q[s] != r.q[s]);
     if (q && lane + 64 * s < K) q[(size_t)t * K + lane + 64 * s] = r.q[s];
   }
   const bool any_w = __builtin_amdgcn_ballot_w64(any) != 0, out_w = __builtin_amdgcn_ballot_w64(out) != 0;
