@@ -27,7 +27,8 @@
  *     exp(z - m) over the columns in four interleaved parts (column c in
  *     part (c / 4) mod 4), each a balanced pairwise tree in ascending
  *     column order, combined as (s0 + s1) + (s2 + s3) (version 1: two
- *     parts, (c / 4) mod 2, s0 + s1); chunks of a split are folded left to
+ *     parts, (c / 4) mod 2, s0 + s1), and s = 0 where every logit of the
+ *     chunk is -inf; chunks of a split are folded left to
  *     right with the operator  (ma,sa) + (mb,sb) = (m, sa*e(ma-m) + sb*e(mb-m)),
  *     m = max(ma,mb); splits are merged with a balanced binary tree;
  *   - exp(x) = exp2(x * log2(e)) and log(x) = log2(x) * ln(2) on the

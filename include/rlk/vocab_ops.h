@@ -60,7 +60,8 @@ size_t rlk_vocab_workspace_bytes(int32_t op, int64_t T, int64_t H, int64_t V, in
  *   top_logp  fp32 [T,K] out, top_ids int32 [T,K] out; slots past V hold -1
  *                         and -inf; may be NULL when K == 0
  * 0 <= K <= RLK_MAX_K.  A target outside [0, V) gives NaN in the row's logp;
- * its entropy and alternatives are those of the row.  A NaN logit makes
+ * its entropy and alternatives are those of the row.  A logit of -inf has
+ * probability 0 and is an alternative only after all others.  A NaN logit makes
  * logp, lse, entropy and top_logp NaN and is never an alternative; a row of
  * nothing but NaN has no alternatives (-1 and -inf), and its lse is -inf. */
 rlk_status rlk_linear_logp_top_fwd(const void* h, const void* W, const int32_t* y, int64_t T, int64_t H, int64_t V,

@@ -217,6 +217,11 @@ __device__ __forceinline__ float exp_tree(const float (&v)[kRowVals], int k0, fl
   }
 }
 
+// What chunk statistics subtract from the logits: the max, but 0 where every
+// logit is -inf (a masked vocabulary), so that their e is exp(-inf) = 0 too
+// and not the NaN of (-inf) - (-inf).
+__device__ __forceinline__ float stats_shift(float mx) { return mx == -INFINITY ? 0.f : mx; }
+
 // (m, s) of one row of a chunk from this lane's values v and those of the
 // other lanes of the row; columns outside the chunk enter as -inf (they do
 // not move the max, and their e is exp(-inf) = 0).
@@ -225,7 +230,7 @@ __device__ __forceinline__ float2 chunk_stats(const float (&v)[kRowVals]) {
 #pragma unroll
   for (int k = 0; k < kRowVals; ++k) mx = fmaxf(mx, v[k]);
   mx = row_max(mx);
-  return make_float2(mx, row_sum(exp_tree<kRowVals>(v, 0, mx)));
+  return make_float2(mx, row_sum(exp_tree<kRowVals>(v, 0, stats_shift(mx))));
 }
 
 // Engine call for a K-mode x K-mode tile.  kSkinny = 1..3 (four-wave

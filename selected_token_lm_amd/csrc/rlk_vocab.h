@@ -83,7 +83,7 @@ __device__ __forceinline__ MSU chunk_stats_moment(const float (&v)[kRowVals]) {
 #pragma unroll
   for (int k = 0; k < kRowVals; ++k) mx = fmaxf(mx, v[k]);
   mx = row_max(mx);
-  const float2 t = moment_tree<kRowVals>(v, 0, mx);
+  const float2 t = moment_tree<kRowVals>(v, 0, stats_shift(mx));
   return {mx, row_sum(t.x), row_sum(t.y)};
 }
 

@@ -1,15 +1,20 @@
-"""linear_logp_top and linear_distill on values at the edges: a teacher's
-undefined logits.
+"""linear_logp_top, linear_distill and linear_logp on values at the edges: a
+teacher's undefined logits, -inf among the student's.  Against the fp64 oracle
+(oracle/vocab_ops.py) where a result is defined, with the inputs and the
+tolerances of test_gpu_vocab_ops.py.
 """
 import numpy as np
 import pytest
 import torch
 
 import selected_token_lm_amd as rlk
-from tests.gpu_util import DEV, f32_dev, i32_dev
-from tests.test_gpu_vocab_ops import Case
+from oracle import vocab_ops as O
+from tests.gpu_util import DEV, f32_dev, i32_dev, say
+from tests.test_gpu_vocab_ops import LOGP_TOL, LOSS_TOL, Case, check_grads, check_top, close
 
 pytestmark = pytest.mark.gpu
+
+BF16_LOWEST = float(torch.finfo(torch.bfloat16).min)
 
 
 def distinct_teacher(c, K, of=None):
@@ -41,3 +46,74 @@ def test_a_teachers_undefined_logit_makes_every_gradient_nan(T, value):
     loss, lse, lp = rlk.linear_distill_fwd(h, W, ids, lg)
     gh, gW = rlk.linear_distill_bwd(h, W, ids, lg, lse, lp, g)
     assert all(x.isfinite().all() for x in (loss, gh, gW))
+
+
+def column_sets(V):
+    """Sets of tokens (not 0) that are whole chunks, whole splits, or neither."""
+    S = -(-V // 32)
+    sets = {"one": [1], "spread": list(range(1, V, 3)), "last": [V - 1]}
+    if S > 128:
+        sets["first chunk"] = list(range(7 * S, 7 * S + 128))
+        sets["second chunk"] = list(range(7 * S + 128, min(7 * S + 256, 8 * S)))
+    if V > 2 * S:
+        sets["split"] = list(range(S, 2 * S))
+        sets["splits"] = [v for v in range(V) if v // S % 2]
+    return sets
+
+
+@pytest.mark.parametrize("T", [20, 150])
+@pytest.mark.parametrize("V", [5, 20, 621, 20011])  # splits of 1, 1, 20 and 626 columns; the third's last is 1 wide
+def test_logits_of_minus_infinity_count_nothing(T, V):
+    """A masked vocabulary: a constant 1 in h, -inf in W for the tokens masked."""
+    for name, off in column_sets(V).items():
+        say(f"[-inf] T={T} V={V}: {name}")
+        c = Case(T, 64, V, seed=5)
+        opened = np.setdiff1d(np.arange(V), off)
+        c.h[:, 0], c.W[:, 0] = 1.0, 0.0
+        c.W[off, 0] = -np.inf
+        c.y = opened[c.r.integers(0, len(opened), T)].astype(np.int32)
+        check_top(c, min(8, len(opened)), grads=False)  # (and linear_logp_fwd's bits)
+        n_ids, n_lg = distinct_teacher(c, 3, opened)
+        h, W = c.dev()
+        got = rlk.linear_distill_fwd(h, W, i32_dev(n_ids), f32_dev(n_lg), 2.0)
+        want = O.distill_forward(c.h, c.W, n_ids, n_lg, 2.0)
+        for what, a, b, tol in zip(("loss", "lse", "logp_ids"), got, want, (LOSS_TOL, LOGP_TOL, LOGP_TOL)):
+            close(what, a, b, tol)
+        y = i32_dev(c.y)
+        parts = torch.stack([rlk.lse_partial(h, W, y, 0, V)])
+        for a, b in zip(rlk.lse_merge(parts, y), rlk.linear_logp_fwd_save(h, W, y)):
+            assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("T", [20, 150])
+def test_a_vocabulary_masked_with_the_lowest_value_and_a_temperature(T):
+    """z / temperature passes fp32's range in the masked tokens: they count
+    nothing, and the gradients stay defined."""
+    V, tau = 20011, 0.5
+    c = Case(T, 64, V, seed=6)
+    off = np.concatenate([column_sets(V)[n] for n in ("split", "second chunk")])
+    opened = np.setdiff1d(np.arange(V), off)
+    c.h[:, 0], c.W[:, 0] = 1.0, 0.0
+    c.W[off, 0] = BF16_LOWEST
+    n_ids, n_lg = distinct_teacher(c, 6, opened)
+    h, W = c.dev()
+    ids, lg, g = i32_dev(n_ids), f32_dev(n_lg), f32_dev(c.g)
+    loss, lse, lp = rlk.linear_distill_fwd(h, W, ids, lg, tau)
+    want = O.distill_forward(c.h, c.W, n_ids, n_lg, tau)
+    close("loss", loss, want[0], LOSS_TOL)
+    close("lse", lse, want[1], LOGP_TOL)
+    close("logp_ids", lp, want[2], LOGP_TOL / tau)
+    dz, size = O.distill_dz(c.h, c.W, n_ids, n_lg, c.g, tau)
+    check_grads(c, dz, size, *rlk.linear_distill_bwd(h, W, ids, lg, lse, lp, g, tau))
+
+
+@pytest.mark.parametrize("T", [20, 150])
+def test_rows_of_minus_infinity_alone(T):
+    """No distribution: an lse of -inf, the rest NaN; the alternatives are the first tokens."""
+    c = Case(T, 64, 500, seed=8)
+    c.h[:, 0] = 1.0
+    h, W = c.dev()
+    W[:, 0] = -np.inf
+    logp, lse, ent, top, ids = rlk.linear_logp_top_fwd(h, W, i32_dev(c.y), 6)
+    assert logp.isnan().all() and lse.eq(-np.inf).all() and ent.isnan().all()
+    assert torch.equal(ids, torch.arange(6, device=DEV, dtype=torch.int32).expand(T, 6))
