@@ -30,11 +30,13 @@
  *     parts, (c / 4) mod 2, s0 + s1), and s = 0 where every logit of the
  *     chunk is -inf; chunks of a split are folded left to
  *     right with the operator  (ma,sa) + (mb,sb) = (m, sa*e(ma-m) + sb*e(mb-m)),
- *     m = max(ma,mb); splits are merged with a balanced binary tree;
+ *     m = max(ma,mb), or (m, sa + sb) where m is -inf; splits are merged with
+ *     a balanced binary tree;
  *   - exp(x) = exp2(x * log2(e)) and log(x) = log2(x) * ln(2) on the
  *     hardware exp2/log2, every operation rounded separately (no FMA
  *     contraction);
- *   - logp = (z_t - m) - log(s), lse = m + log(s), both fp32.
+ *   - logp = (z_t - m) - log(s), lse = m + log(s), both fp32; a NaN logit
+ *     makes both NaN (the max leaves NaN out, the sums do not).
  * Consequences: a row's results depend only on that row (batch- and
  * order-invariant), repeated runs are bit-identical, and merging the partials
  * of equal, aligned power-of-two blocks of splits reproduces the unsharded

@@ -63,7 +63,7 @@ size_t rlk_vocab_workspace_bytes(int32_t op, int64_t T, int64_t H, int64_t V, in
  * its entropy and alternatives are those of the row.  A logit of -inf has
  * probability 0 and is an alternative only after all others.  A NaN logit makes
  * logp, lse, entropy and top_logp NaN and is never an alternative; a row of
- * nothing but NaN has no alternatives (-1 and -inf), and its lse is -inf. */
+ * nothing but NaN has no alternatives (-1 and -inf). */
 rlk_status rlk_linear_logp_top_fwd(const void* h, const void* W, const int32_t* y, int64_t T, int64_t H, int64_t V,
                                    int32_t ignore_index, int64_t K, float* logp, float* lse, float* entropy,
                                    float* top_logp, int32_t* top_ids, void* ws, size_t ws_bytes, void* stream);

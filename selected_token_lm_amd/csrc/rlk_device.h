@@ -43,11 +43,13 @@ __device__ __forceinline__ MS ms_identity() { return {-INFINITY, 0.f}; }
 // a = lower vocabulary indices, b = higher ones:
 //   m = max(ma, mb),  s = (sa * e(ma - m)) + (sb * e(mb - m)),
 // two rounded products and one rounded add.  One exponent argument is
-// exactly 0 (factor exactly 1).  Combining two empty sets gives the empty
-// set without ever evaluating (-inf) - (-inf).
+// exactly 0 (factor exactly 1).  Two sets without a max above -inf never
+// evaluate (-inf) - (-inf): their sums are 0 (empty, or logits of -inf), or
+// NaN where a logit is (which fmaxf leaves out of the max), and just add up,
+// so that no NaN is lost.
 __device__ __forceinline__ MS ms_combine(MS a, MS b) {
   const float m = fmaxf(a.m, b.m);
-  if (m == -INFINITY) return ms_identity();
+  if (m == -INFINITY) return {m, a.s + b.s};
   const float pa = a.s * rlk_exp(a.m - m);
   const float pb = b.s * rlk_exp(b.m - m);
   return {m, pa + pb};

@@ -54,10 +54,11 @@ struct MSU {
 __device__ __forceinline__ MSU msu_identity() { return {-INFINITY, 0.f, 0.f}; }
 
 // a = lower vocabulary indices.  Moving a set from its max ma to m multiplies
-// s by e(ma - m) and gives u' = e(ma - m) u + s' (ma - m).
+// s by e(ma - m) and gives u' = e(ma - m) u + s' (ma - m).  Sums of sets without
+// a max above -inf are 0 or NaN, as in ms_combine.
 __device__ __forceinline__ MSU msu_combine(MSU a, MSU b) {
   const float m = fmaxf(a.m, b.m);
-  if (m == -INFINITY) return msu_identity();
+  if (m == -INFINITY) return {m, a.s + b.s, a.u + b.u};
   const float ea = rlk_exp(a.m - m), eb = rlk_exp(b.m - m);
   const float pa = a.s * ea, pb = b.s * eb;
   const float ua = a.u * ea + pa * fmaxf(a.m - m, kDeepest);

@@ -1,7 +1,7 @@
 """linear_logp_top, linear_distill and linear_logp on values at the edges: a
-teacher's undefined logits, -inf among the student's.  Against the fp64 oracle
-(oracle/vocab_ops.py) where a result is defined, with the inputs and the
-tolerances of test_gpu_vocab_ops.py.
+teacher's undefined logits, -inf and NaN among the student's.  Against the
+fp64 oracle (oracle/vocab_ops.py) where a result is defined, with the inputs
+and the tolerances of test_gpu_vocab_ops.py.
 """
 import numpy as np
 import pytest
@@ -117,3 +117,44 @@ def test_rows_of_minus_infinity_alone(T):
     logp, lse, ent, top, ids = rlk.linear_logp_top_fwd(h, W, i32_dev(c.y), 6)
     assert logp.isnan().all() and lse.eq(-np.inf).all() and ent.isnan().all()
     assert torch.equal(ids, torch.arange(6, device=DEV, dtype=torch.int32).expand(T, 6))
+
+
+@pytest.mark.parametrize("T", [20, 150])
+@pytest.mark.parametrize("V", [5, 20, 621, 20011])
+def test_a_nan_logit_is_never_lost(T, V):
+    """Wherever it lies in the order of the statistics: first or alone in its
+    chunk or split.  Results without it would look sound."""
+    for name, off in column_sets(V).items():
+        say(f"[NaN] T={T} V={V}: {name}")
+        c = Case(T, 64, V, seed=7)
+        opened = np.setdiff1d(np.arange(V), off)
+        c.y = opened[c.r.integers(0, len(opened), T)].astype(np.int32)
+        n_ids, n_lg = distinct_teacher(c, 3, opened)
+        h, W = c.dev()
+        W[torch.tensor(off, device=DEV)] = float("nan")
+        y, ids, lg, g = i32_dev(c.y), i32_dev(n_ids), f32_dev(n_lg), f32_dev(c.g)
+        K = min(8, len(opened))
+        logp, lse, ent, top, best = rlk.linear_logp_top_fwd(h, W, y, K)
+        for x in (logp, lse, ent, top):
+            assert x.isnan().all()
+        assert best.ge(0).all() and not torch.isin(best, torch.tensor(off, device=DEV, dtype=torch.int32)).any()
+        for x in rlk.linear_distill_fwd(h, W, ids, lg):
+            assert x.isnan().all()
+        for x in (*rlk.linear_logp_fwd(h, W, y), *rlk.linear_logp_fwd_save(h, W, y)[:2]):
+            assert x.isnan().all()
+        P = 2
+        S = -(-V // 32)
+        parts = [rlk.lse_partial(h, W[16 * S * p: min(V, 16 * S * (p + 1))], y, 16 * S * p, V)
+                 for p in range(P) if 16 * S * p < V]
+        for x in rlk.lse_merge(torch.stack(parts), y):
+            assert x.isnan().all()
+        gh, gW = rlk.linear_logp_top_bwd(h, W, y, lse, ent, g, g)
+        assert gh.isnan().all() and gW.isnan().all()
+
+
+@pytest.mark.parametrize("T", [20, 150])
+def test_rows_of_nan_alone(T):
+    c = Case(T, 64, 500, seed=8)
+    h, W = c.dev()
+    logp, lse, ent, top, ids = rlk.linear_logp_top_fwd(torch.full_like(h, float("nan")), W, i32_dev(c.y), 6)
+    assert logp.isnan().all() and lse.isnan().all() and ent.isnan().all() and ids.eq(-1).all() and top.eq(-np.inf).all()
