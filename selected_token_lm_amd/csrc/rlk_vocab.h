@@ -692,8 +692,11 @@ __device__ __forceinline__ float wave_sum(float x) {
 }
 
 // A teacher's row over a wave: lane l holds slots l and l + 64.
-// q = softmax of the kept logits / temperature, lq = log q.  (distill_rows of
-// 4096 rows of 64: 4 us.)
+// q = softmax of the kept logits / temperature, lq = log q.  The max is taken
+// off before the quotient: any finite logits are defined then (rows masked
+// with the type's lowest value, under a temperature below 1), and a quotient's
+// error is that of the distance to the max.  (distill_rows of 4096 rows of 64:
+// 4 us.)
 constexpr int kSlots2 = kMaxK / 64;
 struct TeacherRow {
   int id[kSlots2];
@@ -712,7 +715,7 @@ __device__ __forceinline__ TeacherRow teacher_row(const int32_t* ids, const floa
     r.id[s] = k < K ? ids[k] : -1;
     const float l = k < K ? logits[k] : -INFINITY;
     r.kept[s] = slot_kept(r.id[s], l);
-    x[s] = r.kept[s] ? l * scale : -INFINITY;
+    x[s] = r.kept[s] ? l : -INFINITY;
     m = fmaxf(m, x[s]);
     bad |= x[s] != x[s];
   }
@@ -721,14 +724,15 @@ __device__ __forceinline__ TeacherRow teacher_row(const int32_t* ids, const floa
   float sum = 0.f;
 #pragma unroll
   for (int s = 0; s < kSlots2; ++s) {
-    r.q[s] = r.kept[s] ? rlk_exp(x[s] - m) : 0.f;
+    x[s] = (x[s] - m) * scale;
+    r.q[s] = r.kept[s] ? rlk_exp(x[s]) : 0.f;
     sum = sum + r.q[s];
   }
   sum = wave_sum(sum);
   const float L = rlk_log(sum);
 #pragma unroll
   for (int s = 0; s < kSlots2; ++s) {
-    r.lq[s] = r.kept[s] ? (x[s] - m) - L : 0.f;
+    r.lq[s] = r.kept[s] ? x[s] - L : 0.f;
     r.q[s] = r.kept[s] ? r.q[s] / sum : 0.f;
   }
   return r;

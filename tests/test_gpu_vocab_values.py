@@ -1,7 +1,7 @@
 """linear_logp_top, linear_distill and linear_logp on values at the edges: a
-teacher's undefined logits, -inf and NaN among the student's.  Against the
-fp64 oracle (oracle/vocab_ops.py) where a result is defined, with the inputs
-and the tolerances of test_gpu_vocab_ops.py.
+teacher's undefined logits and those near the type's ends, -inf and NaN among
+the student's.  Against the fp64 oracle (oracle/vocab_ops.py) where a result
+is defined, with the inputs and the tolerances of test_gpu_vocab_ops.py.
 """
 import numpy as np
 import pytest
@@ -15,6 +15,7 @@ from tests.test_gpu_vocab_ops import LOGP_TOL, LOSS_TOL, Case, check_grads, chec
 pytestmark = pytest.mark.gpu
 
 BF16_LOWEST = float(torch.finfo(torch.bfloat16).min)
+F32_LOWEST = float(torch.finfo(torch.float32).min)
 
 
 def distinct_teacher(c, K, of=None):
@@ -158,3 +159,33 @@ def test_rows_of_nan_alone(T):
     h, W = c.dev()
     logp, lse, ent, top, ids = rlk.linear_logp_top_fwd(torch.full_like(h, float("nan")), W, i32_dev(c.y), 6)
     assert logp.isnan().all() and lse.isnan().all() and ent.isnan().all() and ids.eq(-1).all() and top.eq(-np.inf).all()
+
+
+@pytest.mark.parametrize("T", [20, 150])
+@pytest.mark.parametrize("tau", [0.5, 1.0, 0.001, 8.0])
+def test_a_teachers_logits_near_the_types_ends(T, tau):
+    """Rows masked with the lowest value as a whole (uniform over their
+    slots), in part, and logits whose quotient by the temperature passes
+    fp32: all are finite logits, and their q is defined."""
+    K = 5
+    c = Case(T, 64, 700, seed=9)
+    n_ids, n_lg = distinct_teacher(c, K)
+    n_lg[1] = F32_LOWEST
+    n_lg[2] = BF16_LOWEST
+    n_lg[3, 1:] = F32_LOWEST
+    n_lg[4] = [3e38, -3e38, 2e38, 0.0, 3e38]
+    n_lg[5] = [F32_LOWEST, F32_LOWEST, -np.inf, F32_LOWEST, -np.inf]
+    n_lg[6] = -F32_LOWEST
+    h, W = c.dev()
+    ids, lg, g = i32_dev(n_ids), f32_dev(n_lg), f32_dev(c.g)
+    loss, lse, lp = rlk.linear_distill_fwd(h, W, ids, lg, tau)
+    with np.errstate(over="ignore"):
+        want = O.distill_forward(c.h, c.W, n_ids, n_lg, tau)
+        dz, size = O.distill_dz(c.h, c.W, n_ids, n_lg, c.g, tau)
+    # z / tau: logits of up to 64 / tau, and the teacher's slots as far apart
+    scale = max(1.0, 1.0 / tau)
+    close("loss", loss, want[0], LOSS_TOL * scale)
+    close("lse", lse, want[1], LOGP_TOL * scale)
+    close("logp_ids", lp, want[2], LOGP_TOL * scale)
+    if tau >= 0.5:  # (the bounds of check_grads are of exponents up to 64)
+        check_grads(c, dz, size, *rlk.linear_distill_bwd(h, W, ids, lg, lse, lp, g, tau))
