@@ -94,10 +94,13 @@ rlk_status rlk_linear_logp_top_bwd(const void* h, const void* W, const int32_t* 
  *   lse       fp32 [T] out    log-sum-exp of z / temperature
  *   logp_ids  fp32 [T,K] out  log p[ids_k]; -inf in empty slots
  * A row whose slots are all empty is inactive: loss = lse = 0, zero
- * gradient.  The same id in several slots counts with the sum of their q.  A
- * kept slot with an id >= V, or a NaN or +inf logit, makes the row's loss
- * and gradients NaN.  1 <= K <= RLK_MAX_K; temperature > 0 and finite (as is
- * its reciprocal). */
+ * gradient.  The same id in several slots counts as the formulas say: each
+ * slot keeps its own log q_k in the loss, which is then below the divergence
+ * from the ids' summed q, Q, by sum_k q_k log(Q[ids_k] / q_k), a constant of
+ * the teacher (it may be negative); dz has their sum.  A kept slot with an
+ * id >= V, or a NaN or +inf logit, makes the row's loss, its grad_h row and
+ * grad_W NaN; any finite logits are defined.  1 <= K <= RLK_MAX_K;
+ * temperature > 0 and finite (as is its reciprocal). */
 rlk_status rlk_linear_distill_fwd(const void* h, const void* W, const int32_t* ids, const float* logits, int64_t T,
                                   int64_t H, int64_t V, int64_t K, float temperature, float* loss, float* lse,
                                   float* logp_ids, void* ws, size_t ws_bytes, void* stream);

@@ -9,7 +9,8 @@ Plain definitions in float64 on the exact values of the inputs, z = h W^T:
             (ties to the lowest id) and their log p;
             dz_v = g [v = y] - p_v (g + g_entropy (entropy + log p_v)).
   distill:  q = softmax over the kept slots of logits / temperature, p =
-            softmax of z / temperature, loss = sum q (log q - log p[ids]);
+            softmax of z / temperature, loss = sum q (log q - log p[ids])
+            over slots (an id in two of them keeps two terms);
             dz_v = (g / temperature) (p_v - sum over slots k of v of q_k).
   grad_h = dz W, grad_W = dz^T h.
 

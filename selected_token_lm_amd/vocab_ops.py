@@ -188,7 +188,9 @@ def linear_distill_fwd(h, W, ids, logits, temperature: float = 1.0, ws=None):
     p = softmax of h W^T / temperature over the vocabulary; lse and logp_ids
     (the student's log p at the ids) are the state the backward needs.  An id
     below 0 or a logit of -inf marks an empty slot; rows without a kept slot
-    have loss 0 and no gradient."""
+    have loss 0 and no gradient.  The ids of a row are meant to be distinct:
+    where one is repeated its slots keep their own log q, so the loss is below
+    KL(q || p) by a constant of the teacher (the gradient has their sum)."""
     h, W = _head(h, W)
     T, H = h.shape
     V = W.shape[0]

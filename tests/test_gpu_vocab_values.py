@@ -189,3 +189,23 @@ def test_a_teachers_logits_near_the_types_ends(T, tau):
     close("logp_ids", lp, want[2], LOGP_TOL * scale)
     if tau >= 0.5:  # (the bounds of check_grads are of exponents up to 64)
         check_grads(c, dz, size, *rlk.linear_distill_bwd(h, W, ids, lg, lse, lp, g, tau))
+
+
+def test_the_same_id_in_several_slots():
+    """Each slot keeps its own log q in the loss, which is then below the
+    divergence of the ids' summed q by a constant of the teacher: two slots
+    of weight 1/2 on one token against a uniform student of V tokens give
+    log V - log 2.  The gradient is that of the sum."""
+    V = 900
+    for T in (3, 140):
+        h, W = torch.zeros((T, 64), dtype=torch.bfloat16, device=DEV), torch.ones((V, 64), dtype=torch.bfloat16, device=DEV)
+        twice, once = (torch.full((T, k), 7, dtype=torch.int32, device=DEV) for k in (2, 1))
+        zero = torch.zeros((T, 2), device=DEV)
+        a = rlk.linear_distill_fwd(h, W, twice, zero)
+        b = rlk.linear_distill_fwd(h, W, once, zero[:, :1])
+        close("loss of two slots", a[0], np.full(T, np.log(V) - np.log(2)), LOSS_TOL)
+        close("loss of one", b[0], np.full(T, np.log(V)), LOSS_TOL)
+        one = torch.ones(T, device=DEV)
+        ga = rlk.linear_distill_bwd(h, W, twice, zero, a[1], a[2], one)
+        gb = rlk.linear_distill_bwd(h, W, once, zero[:, :1], b[1], b[2], one)
+        assert torch.equal(ga[0], gb[0]) and torch.equal(ga[1], gb[1])
