@@ -108,13 +108,20 @@ inline DistillFwdWs distill_fwd_layout(int64_t T, int64_t H, int64_t V, int64_t 
   return w;
 }
 
-// Splits of one of grad_h's parts: 32 / parts.  Parts are work items, so
-// narrow heads want more of them (256 blocks of 64 columns: 4 parts at H =
-// 4096, 32 at 512); their sums cost P / V of the products' traffic, so small
-// vocabularies get no more than one per 4748 columns, four at least.
+// Splits of one of grad_h's parts: 32 / parts.  grad_h's bits depend on them,
+// so they go by H and V alone.  Parts are work items, so narrow heads want more
+// of them: 256 blocks of 64 columns, one for each of the part's units, are 4
+// parts at H = 4096 and 32 at 512.  Their sums pass through HBM (P T H floats
+// beside a product of 2 T H V), so a part has 4096 columns at least, four
+// parts aside.  Both sides of that border, a backward with both gradients in
+// us at T = 32, 300, 2000: V = 132000 in 16 and 32 parts at H = 512 129, 260,
+// 884 and 125, 228, 891, at H = 256 105, 213, 583 and 92, 156, 615; V = 66000
+// in 8 and 16 at H = 512 95, 174, 453 and 82, 135, 481; V = 33000 in 4 and 8
+// 80, 152, 257 and 66, 103, 252 (in 16 60, 86, 272; in 32 59, 86, 309).
+constexpr int64_t kPartColumns = 4096;
 int part_splits(int64_t H, int64_t V) {
   int parts = 4;
-  while (parts < kMaxParts && 2 * parts * H <= 256 * 64 && 2 * parts * 4748 <= V) parts *= 2;
+  while (parts < kMaxParts && 2 * parts * H <= 256 * 64 && 2 * parts * kPartColumns <= V) parts *= 2;
   return rlk::kNSplit / parts;
 }
 

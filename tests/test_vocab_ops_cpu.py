@@ -192,3 +192,21 @@ def test_binding_refuses_the_rest():
         vo._grads(bf(T, H), bf(V, H), True, True, torch.float16)
     with pytest.raises(ValueError, match="must be float32"):
         vo._slot_values(T, K, torch.device("cpu"), logp_ids=f32(T, K + 1))
+
+
+@pytest.mark.parametrize("H,V,parts", [(512, 32768, (4, 8)), (512, 65536, (8, 16)), (64, 131072, (16, 32)),
+                                       (512, 131072, (16, 32)), (1024, 65536, (8, 16)), (1024, 131072, (16, 16)),
+                                       (2048, 32768, (4, 8)), (2048, 65536, (8, 8)), (4096, 131072, (4, 4)),
+                                       (512, 151936, (32, 32))])
+def test_parts_of_grad_h_by_width_and_vocabulary(H, V, parts):
+    """The backward's workspace holds grad_h's fp32 parts: their number (it
+    fixes grad_h's bits) on both sides of a vocabulary, all else being equal."""
+    T = 256
+    below, at = (rlk.vocab_workspace_bytes(rlk.VOP_TOP_BWD, T, H, v, 0) for v in (V - 1, V))
+    assert -(-(V - 1) // 32) == -(-V // 32)  # one split width
+    assert at - below == 4 * T * H * (parts[1] - parts[0])
+    wide = rlk.vocab_workspace_bytes(rlk.VOP_TOP_BWD, 2 * T, H, V, 0)
+    # twice the rows: twice the parts, beside the rows' indices (4 bytes) and
+    # coefficients (20), h and the dz of 32 splits
+    S_pad = (V // 32 + 63) // 64 * 64
+    assert wide - at == T * (4 + 20) + 2 * T * H + 2 * T * 32 * S_pad + 4 * T * H * parts[1]
