@@ -76,9 +76,10 @@ rlk_status rlk_linear_logp_top_fwd(const void* h, const void* W, const int32_t* 
  *   grad_h  bf16 [T,H] out, may be NULL; zero rows for inactive rows
  *   grad_W  [V,H] out of grad_W_dtype (RLK_DT_F32, or RLK_DT_BF16: each fp32
  *           sum rounded once), may be NULL
- * dz is rounded to bf16 once, as in rlk_linear_logp_bwd; sums are fp32.  An
- * active row whose target lies outside [0, V) makes its grad_h row and
- * grad_W NaN. */
+ * dz is rounded to bf16 once, as in rlk_linear_logp_bwd (up to 2^-8 of each
+ * dz; where one dz dominates, with one or two active rows, that scales whole
+ * rows of the gradients); sums are fp32.  An active row whose target lies
+ * outside [0, V) makes its grad_h row and grad_W NaN. */
 rlk_status rlk_linear_logp_top_bwd(const void* h, const void* W, const int32_t* y, const float* lse,
                                    const float* entropy, const float* g, const float* g_entropy, int64_t T, int64_t H,
                                    int64_t V, int32_t ignore_index, void* grad_h, void* grad_W, int32_t grad_W_dtype,

@@ -1325,7 +1325,9 @@ __global__ __launch_bounds__(64) void distill_merge(DistillMergeArgs a) {
 // stores as in dz_tiles;
 //     dz_v = g [v == target] - p_v (a + b (z_v - lse)),  p_v = e(z_v - lse),
 // z scaled by 1 / temperature.  fp32, each operation rounded once, then bf16
-// once: dz is an operand of the gradients' bf16 products.
+// once: dz is an operand of the gradients' bf16 products, and two bf16 terms of
+// it would double them (gradients 0.0023 - 0.0025 off 64 bits, where their own
+// rounding to bf16 is 0.0017).
 // kTop: with target and b; !kTop: a alone.
 // Bound by the engine's MFMAs: 3482 active rows, H = 4096 (4.33 TFLOP) 3.00 -
 // 3.11 ms (1.39 - 1.44 PFLOP/s), 3 % above the logits of the forward (1.1 GB
