@@ -35,8 +35,8 @@
  *   - exp(x) = exp2(x * log2(e)) and log(x) = log2(x) * ln(2) on the
  *     hardware exp2/log2, every operation rounded separately (no FMA
  *     contraction);
- *   - logp = (z_t - m) - log(s), lse = m + log(s), both fp32; a NaN logit
- *     makes both NaN (the max leaves NaN out, the sums do not).
+ *   - logp = (z_t - m) - log(s), lse = m + log(s), both fp32; a NaN or
+ *     +inf logit makes both NaN (the max leaves NaN out, the sums do not).
  * Consequences: a row's results depend only on that row (batch- and
  * order-invariant), repeated runs are bit-identical, and merging the partials
  * of equal, aligned power-of-two blocks of splits reproduces the unsharded

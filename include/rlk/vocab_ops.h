@@ -61,9 +61,10 @@ size_t rlk_vocab_workspace_bytes(int32_t op, int64_t T, int64_t H, int64_t V, in
  *                         and -inf; may be NULL when K == 0
  * 0 <= K <= RLK_MAX_K.  A target outside [0, V) gives NaN in the row's logp;
  * its entropy and alternatives are those of the row.  A logit of -inf has
- * probability 0 and is an alternative only after all others.  A NaN logit makes
- * logp, lse, entropy and top_logp NaN and is never an alternative; a row of
- * nothing but NaN has no alternatives (-1 and -inf). */
+ * probability 0 and is an alternative only after all others (grad_h has the
+ * NaN of 0 times an infinite weight; a finite mask keeps it defined).  A NaN
+ * or +inf logit makes logp, lse, entropy and top_logp NaN; NaN is never an
+ * alternative, and a row of nothing but NaN has none (-1 and -inf). */
 rlk_status rlk_linear_logp_top_fwd(const void* h, const void* W, const int32_t* y, int64_t T, int64_t H, int64_t V,
                                    int32_t ignore_index, int64_t K, float* logp, float* lse, float* entropy,
                                    float* top_logp, int32_t* top_ids, void* ws, size_t ws_bytes, void* stream);

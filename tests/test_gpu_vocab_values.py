@@ -154,6 +154,24 @@ def test_a_nan_logit_is_never_lost(T, V):
 
 
 @pytest.mark.parametrize("T", [20, 150])
+@pytest.mark.parametrize("V", [5, 621, 20011])
+def test_a_logit_of_plus_infinity(T, V):
+    """No distribution, as with torch's log_softmax; the token is the first alternative."""
+    for at in (0, V // 2, V - 1):
+        c = Case(T, 64, V, seed=10)
+        c.h[:, 0], c.W[:, 0] = 1.0, 0.0
+        c.W[at, 0] = np.inf
+        c.y[:] = (at + 1) % V
+        n_ids, n_lg = distinct_teacher(c, 3)
+        h, W = c.dev()
+        y, ids, lg = i32_dev(c.y), i32_dev(n_ids), f32_dev(n_lg)
+        logp, lse, ent, top, best = rlk.linear_logp_top_fwd(h, W, y, 3)
+        for x in (logp, lse, ent, top, *rlk.linear_distill_fwd(h, W, ids, lg), *rlk.linear_logp_fwd(h, W, y)):
+            assert x.isnan().all()
+        assert best[:, 0].eq(at).all()
+
+
+@pytest.mark.parametrize("T", [20, 150])
 def test_rows_of_nan_alone(T):
     c = Case(T, 64, 500, seed=8)
     h, W = c.dev()
