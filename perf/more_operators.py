@@ -133,13 +133,13 @@ def _own(s):
             return {"y": rlk.rms_norm(s["x"], s["weight"], s["eps"], out_dtype=_TYPES[s["y_type"]])}
         y, rstd = rlk.rms_norm_fwd(s["x"], s["weight"], s["eps"], out_dtype=_TYPES[s["y_type"]])
         gx, gw = rlk.rms_norm_bwd(s["x"], s["weight"], rstd, s["g"], grad_weight_dtype=_TYPES[s["w_type"]])
-        return {"y_type": y, "grad_x": gx, "grad_weight": gw}
+        return {"y": y, "grad_x": gx, "grad_weight": gw}
     if s["op"] == "layer":
         if not s["train"]:
             return {"y": rlk.layer_norm(s["x"], s["weight"], s["bias"], s["eps"], out_dtype=_TYPES[s["y_type"]])}
         y, mean, rstd = rlk.layer_norm_fwd(s["x"], s["weight"], s["bias"], s["eps"], out_dtype=_TYPES[s["y_type"]])
         gx, gw, gb = rlk.layer_norm_bwd(s["x"], s["weight"], mean, rstd, s["g"], grad_weight_dtype=_TYPES[s["w_type"]])
-        return {"y_type": y, "grad_x": gx, "grad_weight": gw, "grad_bias": gb}
+        return {"y": y, "grad_x": gx, "grad_weight": gw, "grad_bias": gb}
     if s["op"] == "embed":
         out = {"out": rlk.embed_fwd(s["ids"], s["E"], s["scale"])}
         if s["train"]:
