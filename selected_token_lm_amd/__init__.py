@@ -17,6 +17,9 @@ library is missing or the device is not gfx950, calls raise.
     grad_h, grad_W = linear_logp_bwd_saved(h, W, y, lse, g, z)
     logp, entropy, top_logp, top_ids = linear_logp_top(h, W, y, top_k)   # vocab_ops.py, autograd-aware
     loss = linear_distill(h, W, ids, logits, temperature)                # vocab_ops.py, autograd-aware
+    h = rms_norm(x, weight)                              # step_ops.py, autograd-aware; layer_norm too
+    x = embed(ids, E, scale)                             # step_ops.py, autograd-aware
+    norm, grads = clip_grads(grads, max_norm)            # step_ops.py
 """
 from __future__ import annotations
 
@@ -33,6 +36,8 @@ __all__ = [
     "linear_logp_fwd_noalloc", "NOALLOC_SCRATCH_BYTES", "linear_logp_fwd_rl",
     "linear_logp_top", "linear_logp_top_fwd", "linear_logp_top_bwd", "linear_distill", "linear_distill_fwd",
     "linear_distill_bwd", "vocab_workspace_bytes", "MAX_K",
+    "layer_norm", "layer_norm_fwd", "layer_norm_bwd", "rms_norm", "rms_norm_fwd", "rms_norm_bwd", "embed", "embed_fwd",
+    "embed_bwd", "grad_norm", "clip_grads", "step_workspace_bytes",
 ]
 
 IGNORE_INDEX = -100
@@ -108,7 +113,7 @@ def lib():
         if not os.path.exists(library_path):
             raise RuntimeError(f"{library_path} is not built; run `python -m selected_token_lm_amd.build`")
         L = ctypes.CDLL(library_path)
-        for name, (res, args) in {**_SIGNATURES, **vocab_ops.SIGNATURES}.items():
+        for name, (res, args) in {**_SIGNATURES, **vocab_ops.SIGNATURES, **step_ops.SIGNATURES}.items():
             fn = getattr(L, name)
             fn.restype = res
             fn.argtypes = args
@@ -491,4 +496,9 @@ from . import vocab_ops  # noqa: E402  (uses the helpers above)
 from .vocab_ops import (  # noqa: E402
     MAX_K, VOP_DISTILL_BWD, VOP_DISTILL_FWD, VOP_TOP_BWD, VOP_TOP_FWD, linear_distill, linear_distill_bwd,
     linear_distill_fwd, linear_logp_top, linear_logp_top_bwd, linear_logp_top_fwd, vocab_workspace_bytes,
+)
+from . import step_ops  # noqa: E402
+from .step_ops import (  # noqa: E402
+    SOP_EMBED_BWD, SOP_GRADS, SOP_NORM_BWD, clip_grads, embed, embed_bwd, embed_fwd, grad_norm, layer_norm,
+    layer_norm_bwd, layer_norm_fwd, rms_norm, rms_norm_bwd, rms_norm_fwd, step_workspace_bytes,
 )

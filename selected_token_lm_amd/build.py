@@ -18,8 +18,9 @@ HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 # rlk_api.hip: the C ABI and every kernel with the RLK_WAVES-wave engine;
 # rlk_tiles_w8.hip: the forward, dz and gradient tile kernels with eight waves;
-# rlk_vocab.hip: the operators on the whole distribution (include/rlk/vocab_ops.h).
-SOURCES = ["rlk_api.hip", "rlk_tiles_w8.hip", "rlk_vocab.hip"]
+# rlk_vocab.hip: the operators on the whole distribution (include/rlk/vocab_ops.h);
+# rlk_step.hip: norms, embeddings, gradient clipping (include/rlk/step_ops.h).
+SOURCES = ["rlk_api.hip", "rlk_tiles_w8.hip", "rlk_vocab.hip", "rlk_step.hip"]
 
 FLAGS = [
     "--offload-arch=gfx950",
