@@ -99,7 +99,7 @@ rlk_status rlk_embed_bwd(const void* ids, int32_t id_bytes, const void* g, int32
 /* norm = sqrt of the sum of squares over all elements of n tensors, taken in
  * fp64 and rounded once.
  *   grads, sizes, dtypes  HOST arrays of n: device pointers, element counts
- *          (>= 0) and types; read before the call returns
+ *          (0 .. 2^36) and types; read before the call returns
  *   norm   fp32 [1] out
  * 0 <= n <= 2^20. */
 rlk_status rlk_grad_norm(const void* const* grads, const int64_t* sizes, const int32_t* dtypes, int32_t n, float* norm,

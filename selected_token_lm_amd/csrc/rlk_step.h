@@ -2,10 +2,11 @@
 // and clipping.  All of them are bound by HBM (a few operations an element)
 // or, for a few rows, by latency; there is no product for the matrix units.
 //
-// Elements move in vectors of eight (16 bytes of bf16, 32 of fp32).  Rows may
-// start at any element (odd widths, strides): the hardware loads and stores
-// 16 bytes at any address, so one path serves every alignment and a row's
-// sums keep their order; only a row's last, short vector goes by elements.
+// Elements move in vectors of eight (16 bytes of bf16, 32 of fp32), or of four
+// where all are fp32.  Rows may start at
+// any element (odd widths, strides): the hardware loads and stores 16 bytes
+// at any address, so one path serves every alignment and a row's sums keep
+// their order; only a row's last, short vector goes by elements.
 #pragma once
 
 #include "rlk_device.h"
@@ -15,83 +16,89 @@ namespace step {
 
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
-struct F8 {
-  float v[8];
+// Elements of a vector that moves between arrays of these types.
+template <class A, class B = A>
+constexpr int width_of() {
+  return sizeof(A) == 4 && sizeof(B) == 4 ? 4 : 8;
+}
+
+template <int V>
+struct FV {
+  float v[V];
 };
 
-// Eight elements as they lie in memory.
-template <class T>
+// V elements as they lie in memory.
+template <class T, int V>
 struct Raw {
-  u32x4 q[sizeof(T) / 2];
+  uint32_t q[sizeof(T) * V / 4];
 };
 
-__device__ __forceinline__ float bf16_to_f32(uint32_t b) { return __uint_as_float(b << 16); }
-
-__device__ __forceinline__ F8 widen(const Raw<uint16_t>& r) {
-  F8 f;
+template <int V>
+__device__ __forceinline__ FV<V> widen(const Raw<uint16_t, V>& r) {
+  FV<V> f;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    f.v[2 * i] = __uint_as_float(r.q[0][i] << 16);
-    f.v[2 * i + 1] = __uint_as_float(r.q[0][i] & 0xffff0000u);
+  for (int i = 0; i < V / 2; ++i) {
+    f.v[2 * i] = __uint_as_float(r.q[i] << 16);
+    f.v[2 * i + 1] = __uint_as_float(r.q[i] & 0xffff0000u);
   }
   return f;
 }
-__device__ __forceinline__ F8 widen(const Raw<float>& r) {
-  F8 f;
+template <int V>
+__device__ __forceinline__ FV<V> widen(const Raw<float, V>& r) {
+  FV<V> f;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) f.v[i] = __uint_as_float(r.q[i >> 2][i & 3]);
+  for (int i = 0; i < V; ++i) f.v[i] = __uint_as_float(r.q[i]);
   return f;
 }
 
-// Elements p[0 .. n), n <= 8 (the rest zero; nothing is read where n <= 0).
-template <class T>
-__device__ __forceinline__ Raw<T> load(const T* p, int n) {
-  Raw<T> r;
-  if (n >= 8) {
+// Elements p[0 .. n), n <= V (the rest zero; nothing is read where n <= 0).
+template <int V, class T>
+__device__ __forceinline__ Raw<T, V> load(const T* p, int n) {
+  Raw<T, V> r;
+  if (n >= V) {
     __builtin_memcpy(&r, p, sizeof(r));
     return r;
   }
-  r = Raw<T>{};
+  r = Raw<T, V>{};
 #pragma unroll
-  for (int i = 0; i < 7; ++i) {
+  for (int i = 0; i < V - 1; ++i) {
     if (i < n) {
-      if constexpr (sizeof(T) == 4) r.q[i >> 2][i & 3] = __float_as_uint(p[i]);
-      else r.q[0][i >> 1] |= (uint32_t)p[i] << (16 * (i & 1));
+      if constexpr (sizeof(T) == 4) r.q[i] = __float_as_uint(p[i]);
+      else r.q[i >> 1] |= (uint32_t)p[i] << (16 * (i & 1));
     }
   }
   return r;
 }
 
-__device__ __forceinline__ void store(uint16_t* p, const F8& f, int n) {
-  u32x4 q;
+template <int V>
+__device__ __forceinline__ void store(uint16_t* p, const FV<V>& f, int n) {
+  Raw<uint16_t, V> r;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) q[i] = pack_bf16x2(f.v[2 * i], f.v[2 * i + 1]);
-  if (n >= 8) {
-    __builtin_memcpy(p, &q, 16);
+  for (int i = 0; i < V / 2; ++i) r.q[i] = pack_bf16x2(f.v[2 * i], f.v[2 * i + 1]);
+  if (n >= V) {
+    __builtin_memcpy(p, &r, sizeof(r));
     return;
   }
 #pragma unroll
-  for (int i = 0; i < 7; ++i)
-    if (i < n) p[i] = (uint16_t)(q[i >> 1] >> (16 * (i & 1)));
+  for (int i = 0; i < V - 1; ++i)
+    if (i < n) p[i] = (uint16_t)(r.q[i >> 1] >> (16 * (i & 1)));
 }
-__device__ __forceinline__ void store(float* p, const F8& f, int n) {
-  if (n >= 8) {
-    __builtin_memcpy(p, &f, 32);
+template <int V>
+__device__ __forceinline__ void store(float* p, const FV<V>& f, int n) {
+  if (n >= V) {
+    __builtin_memcpy(p, &f, sizeof(f));
     return;
   }
 #pragma unroll
-  for (int i = 0; i < 7; ++i)
+  for (int i = 0; i < V - 1; ++i)
     if (i < n) p[i] = f.v[i];
 }
 
-// Eight elements of an array whose type is known at run time (uniform).
-__device__ __forceinline__ F8 load_any(const void* p, bool f32, int64_t at, int n) {
-  if (f32) return widen(load(static_cast<const float*>(p) + at, n));
-  return widen(load(static_cast<const uint16_t*>(p) + at, n));
-}
-__device__ __forceinline__ void store_any(void* p, bool f32, int64_t at, const F8& f, int n) {
-  if (f32) store(static_cast<float*>(p) + at, f, n);
-  else store(static_cast<uint16_t*>(p) + at, f, n);
+// Elements of an array whose type is known at run time (uniform).
+template <int V>
+__device__ __forceinline__ FV<V> load_any(const void* p, bool f32, int64_t at, int n) {
+  if (f32) return widen(load<V>(static_cast<const float*>(p) + at, n));
+  return widen(load<V>(static_cast<const uint16_t*>(p) + at, n));
 }
 
 // Sum over a wave, in every lane: pairs 1, 2, then mirrored quads and octets
@@ -113,8 +120,8 @@ __device__ __forceinline__ float wave_sum(float v) {
 }
 
 // --- norms -------------------------------------------------------------------
-// R threads hold a row in registers, N vectors each: vector i * R + lane.  The
-// split goes by H alone, so a row's sums have one order.
+// R threads hold a row in registers, N vectors of V each: vector i * R + lane.
+// The split goes by H and the types alone, so a row's sums have one order.
 template <int R>
 struct RowSum {
   static constexpr int kWaves = R / 64;
@@ -160,8 +167,9 @@ struct NormFwdArgs {
 
 // y = (x - mean) rstd w + b (kCenter), or x rstd w.  The row is read once; the
 // variance is taken about the mean (a second sum over registers).
-template <class X, class Y, bool kCenter, int R, int N>
+template <class X, class Y, bool kCenter, int R, int E>
 __global__ __launch_bounds__(norm_block(R)) void norm_fwd(NormFwdArgs a) {
+  constexpr int V = width_of<X, Y>(), N = E / V;
   constexpr int kRows = norm_rows(R);
   constexpr int kWaves = R / 64;
   __shared__ float red[2 * kWaves];
@@ -169,16 +177,16 @@ __global__ __launch_bounds__(norm_block(R)) void norm_fwd(NormFwdArgs a) {
   const float fH = (float)a.H;
   for (int64_t row = (int64_t)blockIdx.x * kRows + threadIdx.x / R; row < a.T; row += (int64_t)gridDim.x * kRows) {
     const X* x = static_cast<const X*>(a.x) + row * a.ldx;
-    Raw<X> raw[N];
+    Raw<X, V> raw[N];
 #pragma unroll
-    for (int i = 0; i < N; ++i) raw[i] = load(x + 8 * (i * R + lane), a.H - 8 * (i * R + lane));
-    F8 v[N];
+    for (int i = 0; i < N; ++i) raw[i] = load<V>(x + V * (i * R + lane), a.H - V * (i * R + lane));
+    FV<V> v[N];
     float s[1] = {0.f};
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       v[i] = widen(raw[i]);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) s[0] += kCenter ? v[i].v[j] : v[i].v[j] * v[i].v[j];
+      for (int j = 0; j < V; ++j) s[0] += kCenter ? v[i].v[j] : v[i].v[j] * v[i].v[j];
     }
     RowSum<R>::run(s, red);
     float mean = 0.f;
@@ -187,9 +195,9 @@ __global__ __launch_bounds__(norm_block(R)) void norm_fwd(NormFwdArgs a) {
       s[0] = 0.f;
 #pragma unroll
       for (int i = 0; i < N; ++i) {
-        const int n = a.H - 8 * (i * R + lane);
+        const int n = a.H - V * (i * R + lane);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
+        for (int j = 0; j < V; ++j) {
           v[i].v[j] = j < n ? v[i].v[j] - mean : 0.f;
           s[0] += v[i].v[j] * v[i].v[j];
         }
@@ -204,20 +212,20 @@ __global__ __launch_bounds__(norm_block(R)) void norm_fwd(NormFwdArgs a) {
     Y* y = static_cast<Y*>(a.y) + row * a.H;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const int c = 8 * (i * R + lane), n = a.H - c;
+      const int c = V * (i * R + lane), n = a.H - c;
       if (n <= 0) continue;
-      F8 o;
+      FV<V> o;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) o.v[j] = v[i].v[j] * rstd;
+      for (int j = 0; j < V; ++j) o.v[j] = v[i].v[j] * rstd;
       if (a.w) {
-        const F8 w = load_any(a.w, a.w_f32, c, n);
+        const FV<V> w = load_any<V>(a.w, a.w_f32, c, n);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) o.v[j] *= w.v[j];
+        for (int j = 0; j < V; ++j) o.v[j] *= w.v[j];
       }
       if (kCenter && a.b) {
-        const F8 b = load_any(a.b, a.w_f32, c, n);
+        const FV<V> b = load_any<V>(a.b, a.w_f32, c, n);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) o.v[j] += b.v[j];
+        for (int j = 0; j < V; ++j) o.v[j] += b.v[j];
       }
       store(y + c, o, n);
     }
@@ -241,24 +249,28 @@ struct NormBwdArgs {
 // A block takes rows b, b + P, ...: grad_x of each, and the block's sums for
 // the weight's and bias's gradients in registers.  The next row's loads are
 // issued before the current row's sums are exchanged.
-template <class X, class G, bool kCenter, bool kSums, int R, int N>
+template <class X, class G, bool kCenter, bool kSums, int R, int E>
 __global__ __launch_bounds__(norm_block(R)) void norm_bwd(NormBwdArgs a) {
+  constexpr int V = width_of<X, G>(), N = E / V;
   constexpr int kRows = norm_rows(R);
   constexpr int kVals = kCenter ? 2 : 1;
   constexpr int kWaves = R / 64;
   __shared__ float red[2][kVals * kWaves];
   const int lane = threadIdx.x % R;
   const float fH = (float)a.H;
-  F8 w[N], dw[N], db[N];
+  FV<V> w[N], dw[N], db[N];
+  FV<V> ones;
+#pragma unroll
+  for (int j = 0; j < V; ++j) ones.v[j] = 1.f;
 #pragma unroll
   for (int i = 0; i < N; ++i) {
-    const int c = 8 * (i * R + lane), n = a.H - c;
-    if (a.w) w[i] = load_any(a.w, a.w_f32, c, n);
-    else w[i] = F8{{1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f}};
-    dw[i] = db[i] = F8{};
+    const int c = V * (i * R + lane), n = a.H - c;
+    if (a.w) w[i] = load_any<V>(a.w, a.w_f32, c, n);
+    else w[i] = ones;
+    dw[i] = db[i] = FV<V>{};
   }
-  Raw<X> xr[N];
-  Raw<G> gr[N];
+  Raw<X, V> xr[N];
+  Raw<G, V> gr[N];
   float mean = 0.f, rstd = 0.f;
   int64_t row = (int64_t)blockIdx.x * kRows + threadIdx.x / R;
   const int64_t stride = (int64_t)gridDim.x * kRows;
@@ -267,9 +279,9 @@ __global__ __launch_bounds__(norm_block(R)) void norm_bwd(NormBwdArgs a) {
     const G* g = static_cast<const G*>(a.g) + t * a.ldg;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const int c = 8 * (i * R + lane);
-      xr[i] = load(x + c, a.H - c);
-      gr[i] = load(g + c, a.H - c);
+      const int c = V * (i * R + lane);
+      xr[i] = load<V>(x + c, a.H - c);
+      gr[i] = load<V>(g + c, a.H - c);
     }
     if (kCenter) mean = a.mean[t];
     rstd = a.rstd[t];
@@ -277,14 +289,14 @@ __global__ __launch_bounds__(norm_block(R)) void norm_bwd(NormBwdArgs a) {
   if (row < a.T) fetch(row);
   int turn = 0;
   for (; row < a.T; row += stride, turn ^= 1) {
-    F8 nv[N], gw[N];
+    FV<V> nv[N], gw[N];
     float s[kVals] = {};
     const float r = rstd, mu = mean;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const F8 xv = widen(xr[i]), gv = widen(gr[i]);
+      const FV<V> xv = widen(xr[i]), gv = widen(gr[i]);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
+      for (int j = 0; j < V; ++j) {
         const float n = kCenter ? (xv.v[j] - mu) * r : xv.v[j] * r;
         const float g = gv.v[j];
         nv[i].v[j] = n;
@@ -306,11 +318,11 @@ __global__ __launch_bounds__(norm_block(R)) void norm_bwd(NormBwdArgs a) {
     X* gx = static_cast<X*>(a.grad_x) + row * a.H;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const int c = 8 * (i * R + lane);
+      const int c = V * (i * R + lane);
       if (c >= a.H) continue;
-      F8 o;
+      FV<V> o;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
+      for (int j = 0; j < V; ++j) {
         const float t = kCenter ? gw[i].v[j] - c2 : gw[i].v[j];
         o.v[j] = r * (t - nv[i].v[j] * c1);
       }
@@ -322,19 +334,16 @@ __global__ __launch_bounds__(norm_block(R)) void norm_bwd(NormBwdArgs a) {
     const int64_t second = (int64_t)gridDim.x * a.Hp;
     if constexpr (kRows > 1) {
       // the row groups' sums in order, through LDS
-      __shared__ float4 lds[kRows][R * N * 2];
+      __shared__ float4 lds[kRows][R * E / 4];
 #pragma unroll
       for (int k = 0; k < kVals; ++k) {
         if (k) __syncthreads();
-        const F8* d = k ? db : dw;
-        const int q = threadIdx.x / R;
+        const FV<V>* d = k ? db : dw;
+        float* mine = reinterpret_cast<float*>(lds[threadIdx.x / R]);
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-          lds[q][2 * (i * R + lane)] = make_float4(d[i].v[0], d[i].v[1], d[i].v[2], d[i].v[3]);
-          lds[q][2 * (i * R + lane) + 1] = make_float4(d[i].v[4], d[i].v[5], d[i].v[6], d[i].v[7]);
-        }
+        for (int i = 0; i < N; ++i) *reinterpret_cast<FV<V>*>(mine + V * (i * R + lane)) = d[i];
         __syncthreads();
-        for (int e = threadIdx.x; e < 2 * R * N; e += norm_block(R)) {
+        for (int e = threadIdx.x; e < R * E / 4; e += norm_block(R)) {
           if (4 * e >= a.Hp) continue;
           float4 t = lds[0][e];
 #pragma unroll
@@ -350,10 +359,10 @@ __global__ __launch_bounds__(norm_block(R)) void norm_bwd(NormBwdArgs a) {
     } else {
 #pragma unroll
       for (int i = 0; i < N; ++i) {
-        const int c = 8 * (i * R + lane);
+        const int c = V * (i * R + lane);
         if (c >= a.H) continue;
-        store(part + c, dw[i], 8);
-        if (kCenter) store(part + second + c, db[i], 8);
+        store(part + c, dw[i], V);
+        if (kCenter) store(part + second + c, db[i], V);
       }
     }
   }
@@ -363,26 +372,26 @@ __global__ __launch_bounds__(norm_block(R)) void norm_bwd(NormBwdArgs a) {
 // row comes from L2 then) and one for the result.
 template <class X, class Y, bool kCenter>
 __global__ __launch_bounds__(1024) void norm_fwd_wide(NormFwdArgs a) {
-  constexpr int R = 1024;
+  constexpr int R = 1024, V = width_of<X, Y>();
   __shared__ float red[2][R / 64];
   const float fH = (float)a.H;
   for (int64_t row = blockIdx.x; row < a.T; row += gridDim.x) {
     const X* x = static_cast<const X*>(a.x) + row * a.ldx;
     float mean = 0.f, s[1] = {0.f};
     if constexpr (kCenter) {
-      for (int c = 8 * threadIdx.x; c < a.H; c += 8 * R) {
-        const F8 f = widen(load(x + c, a.H - c));
+      for (int c = V * threadIdx.x; c < a.H; c += V * R) {
+        const FV<V> f = widen(load<V>(x + c, a.H - c));
 #pragma unroll
-        for (int j = 0; j < 8; ++j) s[0] += f.v[j];
+        for (int j = 0; j < V; ++j) s[0] += f.v[j];
       }
       RowSum<R>::run(s, red[0]);
       mean = s[0] / fH;
       s[0] = 0.f;
     }
-    for (int c = 8 * threadIdx.x; c < a.H; c += 8 * R) {
-      const F8 f = widen(load(x + c, a.H - c));
+    for (int c = V * threadIdx.x; c < a.H; c += V * R) {
+      const FV<V> f = widen(load<V>(x + c, a.H - c));
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
+      for (int j = 0; j < V; ++j) {
         const float d = c + j < a.H ? f.v[j] - mean : 0.f;
         s[0] += d * d;
       }
@@ -394,19 +403,19 @@ __global__ __launch_bounds__(1024) void norm_fwd_wide(NormFwdArgs a) {
       if (a.rstd) a.rstd[row] = rstd;
     }
     Y* y = static_cast<Y*>(a.y) + row * a.H;
-    for (int c = 8 * threadIdx.x; c < a.H; c += 8 * R) {
-      F8 o = widen(load(x + c, a.H - c));
+    for (int c = V * threadIdx.x; c < a.H; c += V * R) {
+      FV<V> o = widen(load<V>(x + c, a.H - c));
 #pragma unroll
-      for (int j = 0; j < 8; ++j) o.v[j] = (kCenter ? o.v[j] - mean : o.v[j]) * rstd;
+      for (int j = 0; j < V; ++j) o.v[j] = (kCenter ? o.v[j] - mean : o.v[j]) * rstd;
       if (a.w) {
-        const F8 w = load_any(a.w, a.w_f32, c, a.H - c);
+        const FV<V> w = load_any<V>(a.w, a.w_f32, c, a.H - c);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) o.v[j] *= w.v[j];
+        for (int j = 0; j < V; ++j) o.v[j] *= w.v[j];
       }
       if (kCenter && a.b) {
-        const F8 b = load_any(a.b, a.w_f32, c, a.H - c);
+        const FV<V> b = load_any<V>(a.b, a.w_f32, c, a.H - c);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) o.v[j] += b.v[j];
+        for (int j = 0; j < V; ++j) o.v[j] += b.v[j];
       }
       store(y + c, o, a.H - c);
     }
@@ -417,7 +426,7 @@ __global__ __launch_bounds__(1024) void norm_fwd_wide(NormFwdArgs a) {
 // The backward of such rows: one pass for its sums, one for grad_x.
 template <class X, class G, bool kCenter>
 __global__ __launch_bounds__(1024) void norm_bwd_wide(NormBwdArgs a) {
-  constexpr int R = 1024, kVals = kCenter ? 2 : 1;
+  constexpr int R = 1024, V = width_of<X, G>(), kVals = kCenter ? 2 : 1;
   __shared__ float red[2][kVals * (R / 64)];
   const float fH = (float)a.H;
   int turn = 0;
@@ -425,23 +434,23 @@ __global__ __launch_bounds__(1024) void norm_bwd_wide(NormBwdArgs a) {
     const X* x = static_cast<const X*>(a.x) + row * a.ldx;
     const G* g = static_cast<const G*>(a.g) + row * a.ldg;
     const float mu = kCenter ? a.mean[row] : 0.f, r = a.rstd[row];
-    auto values = [&](int c, F8& nv, F8& gw) {
-      nv = widen(load(x + c, a.H - c));
-      gw = widen(load(g + c, a.H - c));
+    auto values = [&](int c, FV<V>& nv, FV<V>& gw) {
+      nv = widen(load<V>(x + c, a.H - c));
+      gw = widen(load<V>(g + c, a.H - c));
       if (a.w) {
-        const F8 w = load_any(a.w, a.w_f32, c, a.H - c);
+        const FV<V> w = load_any<V>(a.w, a.w_f32, c, a.H - c);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) gw.v[j] *= w.v[j];
+        for (int j = 0; j < V; ++j) gw.v[j] *= w.v[j];
       }
 #pragma unroll
-      for (int j = 0; j < 8; ++j) nv.v[j] = kCenter ? (nv.v[j] - mu) * r : nv.v[j] * r;
+      for (int j = 0; j < V; ++j) nv.v[j] = kCenter ? (nv.v[j] - mu) * r : nv.v[j] * r;
     };
     float s[kVals] = {};
-    for (int c = 8 * threadIdx.x; c < a.H; c += 8 * R) {
-      F8 nv, gw;
+    for (int c = V * threadIdx.x; c < a.H; c += V * R) {
+      FV<V> nv, gw;
       values(c, nv, gw);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
+      for (int j = 0; j < V; ++j) {
         s[0] = __builtin_fmaf(gw.v[j], nv.v[j], s[0]);
         if constexpr (kCenter) s[1] += gw.v[j];
       }
@@ -451,36 +460,37 @@ __global__ __launch_bounds__(1024) void norm_bwd_wide(NormBwdArgs a) {
     float c2 = 0.f;
     if constexpr (kCenter) c2 = s[1] / fH;
     X* gx = static_cast<X*>(a.grad_x) + row * a.H;
-    for (int c = 8 * threadIdx.x; c < a.H; c += 8 * R) {
-      F8 nv, gw;
+    for (int c = V * threadIdx.x; c < a.H; c += V * R) {
+      FV<V> nv, gw;
       values(c, nv, gw);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) gw.v[j] = r * ((kCenter ? gw.v[j] - c2 : gw.v[j]) - nv.v[j] * c1);
+      for (int j = 0; j < V; ++j) gw.v[j] = r * ((kCenter ? gw.v[j] - c2 : gw.v[j]) - nv.v[j] * c1);
       store(gx + c, gw, a.H - c);
     }
   }
 }
 
-// The sums of such rows: 2048 columns a block, rows p, p + P, ...
+// The sums of such rows: 256 vectors a block, rows p, p + P, ...
 template <class X, class G, bool kCenter>
 __global__ __launch_bounds__(256) void norm_sums_wide(NormBwdArgs a) {
-  const int c = 8 * (blockIdx.x * 256 + threadIdx.x);
+  constexpr int V = width_of<X, G>();
+  const int c = V * (blockIdx.x * 256 + threadIdx.x);
   if (c >= a.H) return;
-  F8 dw{}, db{};
+  FV<V> dw{}, db{};
   for (int64_t row = blockIdx.y; row < a.T; row += gridDim.y) {
-    const F8 x = widen(load(static_cast<const X*>(a.x) + row * a.ldx + c, a.H - c));
-    const F8 g = widen(load(static_cast<const G*>(a.g) + row * a.ldg + c, a.H - c));
+    const FV<V> x = widen(load<V>(static_cast<const X*>(a.x) + row * a.ldx + c, a.H - c));
+    const FV<V> g = widen(load<V>(static_cast<const G*>(a.g) + row * a.ldg + c, a.H - c));
     const float mu = kCenter ? a.mean[row] : 0.f, r = a.rstd[row];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
+    for (int j = 0; j < V; ++j) {
       const float n = kCenter ? (x.v[j] - mu) * r : x.v[j] * r;
       dw.v[j] = __builtin_fmaf(g.v[j], n, dw.v[j]);
       db.v[j] += g.v[j];
     }
   }
   float* part = a.part + (int64_t)blockIdx.y * a.Hp + c;
-  store(part, dw, 8);
-  if (kCenter) store(part + (int64_t)gridDim.y * a.Hp, db, 8);
+  store(part, dw, V);
+  if (kCenter) store(part + (int64_t)gridDim.y * a.Hp, db, V);
 }
 
 struct NormSumArgs {
@@ -543,22 +553,25 @@ struct EmbedArgs {
 // out[t] = scale E[id]: L lanes a row, each vectors lane, lane + L, ...
 template <class E, class O, int L>
 __global__ __launch_bounds__(256) void embed_rows(EmbedArgs a) {
+  constexpr int V = width_of<E, O>();
   const int lane = threadIdx.x % L;
   for (int64_t t = (int64_t)blockIdx.x * (256 / L) + threadIdx.x / L; t < a.T; t += (int64_t)gridDim.x * (256 / L)) {
     const int64_t id = id_at(a.ids, t);
     O* out = static_cast<O*>(a.out) + t * a.H;
     const bool ignored = id == a.ids.ignore;
     if (ignored || id < 0 || id >= a.V) {
-      const float f = ignored ? 0.f : __builtin_nanf("");
-      for (int c = 8 * lane; c < a.H; c += 8 * L) store(out + c, F8{{f, f, f, f, f, f, f, f}}, a.H - c);
+      FV<V> f;
+#pragma unroll
+      for (int j = 0; j < V; ++j) f.v[j] = ignored ? 0.f : __builtin_nanf("");
+      for (int c = V * lane; c < a.H; c += V * L) store(out + c, f, a.H - c);
       continue;
     }
     const E* row = static_cast<const E*>(a.E) + id * a.H;
 #pragma unroll 4
-    for (int c = 8 * lane; c < a.H; c += 8 * L) {
-      F8 f = widen(load(row + c, a.H - c));
+    for (int c = V * lane; c < a.H; c += V * L) {
+      FV<V> f = widen(load<V>(row + c, a.H - c));
 #pragma unroll
-      for (int j = 0; j < 8; ++j) f.v[j] *= a.scale;
+      for (int j = 0; j < V; ++j) f.v[j] *= a.scale;
       store(out + c, f, a.H - c);
     }
   }
@@ -571,50 +584,113 @@ __device__ __forceinline__ int key_of(const IdsArg& a, int64_t t, int V) {
   return id == a.ignore || id < 0 || id >= V ? V : (int)id;
 }
 
-// Up to kRankRows tokens: a token's position is the number of tokens before it
-// in that order, counted against all others.  64 tokens a block, one a lane;
-// the 16 waves count a sixteenth of the others each.
-constexpr int kRankRows = 16384;
-
-__global__ __launch_bounds__(1024) void embed_rank(IdsArg ids, int T, int V, int32_t* keys, int32_t* perm) {
-  __shared__ int32_t all[kRankRows];
-  __shared__ int32_t count[16][64];
-  // padded to whole groups of four per wave with keys that precede nothing
-  const int per = (T + 63) / 64 * 4;
-  for (int t = threadIdx.x; t < 16 * per; t += 1024) all[t] = t < T ? key_of(ids, t, V) : INT32_MAX;
-  __syncthreads();
-  const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
-  const int t0 = 64 * blockIdx.x, t = t0 + lane;
-  const int key = t < T ? all[t] : INT32_MIN;
-  const int lo = wave * per, hi = lo + per;
-  int n = 0;
-  // tokens before this block's, its own, and those behind (bounds are
-  // multiples of four)
-  const int a = min(max(t0, lo), hi), b = min(max(t0 + 64, lo), hi);
-#pragma unroll 4
-  for (int i = lo; i < a; i += 4) {
-    const int4 k = *reinterpret_cast<const int4*>(all + i);
-    n += (k.x <= key) + (k.y <= key) + (k.z <= key) + (k.w <= key);
+// Zeroes of the dense gradient, by the blocks of a sort's launch that do not
+// sort: the sort is bound by latency and leaves the memory idle.  Rows of
+// tokens that occur are written again afterwards.
+struct ZeroArgs {
+  char* p;        // NULL: nothing to zero
+  int64_t bytes;  // even
+};
+__device__ __forceinline__ void zero_share(const ZeroArgs& z, int64_t block, int64_t blocks, int threads) {
+  const int64_t n16 = z.bytes / 16;
+  for (int64_t i = block * threads + threadIdx.x; i < n16; i += blocks * threads) {
+    const u32x4 zero = {0u, 0u, 0u, 0u};
+    __builtin_memcpy(z.p + 16 * i, &zero, 16);
   }
-  for (int i = a; i < b; ++i) n += all[i] < key || (all[i] == key && i < t);
-#pragma unroll 4
-  for (int i = b; i < hi; i += 4) {
-    const int4 k = *reinterpret_cast<const int4*>(all + i);
-    n += (k.x < key) + (k.y < key) + (k.z < key) + (k.w < key);
-  }
-  count[wave][lane] = n;
-  __syncthreads();
-  if (wave || t >= T) return;
-  int at = 0;
-#pragma unroll
-  for (int w = 0; w < 16; ++w) at += count[w][lane];
-  keys[at] = key;
-  perm[at] = t;
+  if (block == 0 && threadIdx.x < (z.bytes - 16 * n16) / 2)
+    reinterpret_cast<uint16_t*>(z.p + 16 * n16)[threadIdx.x] = 0;
 }
 
-// More tokens: a radix sort by digits of up to nine bits, the lowest first;
-// tiles of 4096 tokens, a wave's 1024 in order.
+// Up to kRankRows tokens: a token's place is the number of tokens before it in
+// that order, counted against all others, which wait in LDS.  kTok tokens a
+// block; a thread counts a sixteenth of the others for one of them.  Up to
+// 4096 tokens small blocks with little LDS leave the units to the blocks that
+// zero; beyond, fewer blocks read all ids.
+constexpr int kRankRows = 16384;
+
+struct RankArgs {
+  IdsArg ids;
+  int32_t* keys;
+  int32_t* perm;
+  int T, V;
+  int blocks;  // that rank
+  ZeroArgs zero;
+};
+
+template <int kTok, int kMost>
+__global__ __launch_bounds__(16 * kTok) void embed_rank(RankArgs a) {
+  constexpr int kThreads = 16 * kTok, kSets = 16;  // others: groups of four, set, set + 16, ...
+  __shared__ int32_t all[kMost];
+  __shared__ int32_t count[kThreads / 64][64];
+  if ((int)blockIdx.x >= a.blocks) {
+    zero_share(a.zero, blockIdx.x - a.blocks, gridDim.x - a.blocks, kThreads);
+    return;
+  }
+  const int tok = threadIdx.x % kTok, set = threadIdx.x / kTok;
+  const int t0 = kTok * blockIdx.x, t = t0 + tok;
+  // turns of 64 others; what stands past T precedes nothing
+  const int turns = (a.T + 63) / 64;
+#pragma unroll
+  for (int i = 0; i < kMost / kThreads; i += 4) {
+    if (i * kThreads >= 64 * turns) break;
+    int32_t k[4];
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+      const int o = (i + m) * kThreads + threadIdx.x;
+      k[m] = o < a.T ? key_of(a.ids, o, a.V) : INT32_MAX;
+    }
+#pragma unroll
+    for (int m = 0; m < 4; ++m) all[(i + m) * kThreads + threadIdx.x] = k[m];
+  }
+  __syncthreads();
+  const int key = t < a.T ? all[t] : INT32_MIN;
+  const int4* p = reinterpret_cast<const int4*>(all) + set;
+  const int own = t0 / 64;  // the turn with this block's tokens
+  int n = 0;
+#pragma unroll 4
+  for (int j = 0; j < own; ++j) {
+    const int4 v = p[j * kSets];
+    n += (v.x <= key) + (v.y <= key) + (v.z <= key) + (v.w <= key);
+  }
+  {
+    const int4 v = p[own * kSets];
+    const int o = 4 * (own * kSets + set);
+    n += v.x < key || (v.x == key && o < t);
+    n += v.y < key || (v.y == key && o + 1 < t);
+    n += v.z < key || (v.z == key && o + 2 < t);
+    n += v.w < key || (v.w == key && o + 3 < t);
+  }
+#pragma unroll 4
+  for (int j = own + 1; j < turns; ++j) {
+    const int4 v = p[j * kSets];
+    n += (v.x < key) + (v.y < key) + (v.z < key) + (v.w < key);
+  }
+  // a token's sets: lanes kTok apart, then the waves
+#pragma unroll
+  for (int d = kTok; d < 64; d *= 2) n += __shfl_xor(n, d);
+  count[threadIdx.x / 64][threadIdx.x % 64] = n;
+  __syncthreads();
+  if (threadIdx.x >= kTok || t >= a.T) return;
+  int at = 0;
+#pragma unroll
+  for (int w = 0; w < kThreads / 64; ++w) at += count[w][tok];
+  a.keys[at] = key;
+  a.perm[at] = t;
+}
+
+// More tokens: a radix sort by digits of up to nine bits, the lowest first,
+// three launches each; tiles of 4096 tokens, a wave's 1024 in order.
 constexpr int kTile = 4096, kBins = 512;
+
+// The lanes of a wave whose digit is this lane's.
+__device__ __forceinline__ uint64_t same_digit(int d, int bits) {
+  uint64_t same = ~0ull;
+  for (int b = 0; b < bits; ++b) {
+    const uint64_t one = __ballot((d >> b) & 1);
+    same &= (d >> b) & 1 ? one : ~one;
+  }
+  return same;
+}
 
 struct RadixArgs {
   IdsArg ids;  // the first pass's input
@@ -626,6 +702,7 @@ struct RadixArgs {
   int32_t* total;  // [kBins]
   int T, V, tiles;
   int shift, bits, first;
+  ZeroArgs zero;  // for blocks behind the tiles of the first pass's counts
 };
 __device__ __forceinline__ int radix_key(const RadixArgs& a, int t) {
   return a.first ? key_of(a.ids, t, a.V) : a.keys_in[t];
@@ -633,6 +710,10 @@ __device__ __forceinline__ int radix_key(const RadixArgs& a, int t) {
 
 __global__ __launch_bounds__(256) void radix_count(RadixArgs a) {
   __shared__ int32_t bin[kBins];
+  if ((int)blockIdx.x >= a.tiles) {
+    zero_share(a.zero, blockIdx.x - a.tiles, gridDim.x - a.tiles, 256);
+    return;
+  }
   const int mask = (1 << a.bits) - 1;
   for (int i = threadIdx.x; i < kBins; i += 256) bin[i] = 0;
   __syncthreads();
@@ -720,11 +801,7 @@ __global__ __launch_bounds__(256) void radix_scatter(RadixArgs a) {
     const int t = base + 64 * r + lane;
     const bool live = t < a.T;
     const int d = (key[r] >> a.shift) & mask;
-    uint64_t same = __ballot(live);
-    for (int b = 0; b < a.bits; ++b) {
-      const uint64_t one = __ballot((d >> b) & 1);
-      same &= (d >> b) & 1 ? one : ~one;
-    }
+    const uint64_t same = same_digit(d, a.bits) & __ballot(live);
     const int rank = __builtin_popcountll(same & ((1ull << lane) - 1));
     int p = 0;
     if (live) p = at[wave][d] + rank;
@@ -757,9 +834,10 @@ __device__ __forceinline__ int lower_bound(const int32_t* keys, int n, int v) {
   return lo;
 }
 
-// Rows of one token are summed in runs of kRun from its first on, a wave and
-// 512 columns each; a token of more rows leaves its runs' sums in parts.
-constexpr int kRun = 64;
+// Rows of one token are summed in runs of kRun from its first on, all of a
+// run's rows in flight together, a wave and a vector a lane of the columns
+// each; a token of more rows leaves its runs' sums in parts.
+constexpr int kRun = 16;
 
 struct EmbedGradArgs {
   const int32_t* keys;
@@ -771,153 +849,140 @@ struct EmbedGradArgs {
   int T, H, V;
   float scale;
   int accumulate;
-  int waves;       // of a block, on one position (1, 2 or 4), by H
-  int item_blocks;
-  int zero_rows;   // rows of grad a block behind item_blocks looks at
+  int slices;  // of the columns, a wave each
 };
 
 // The part of the run that starts at position i: a token's first run, or a
 // later one, can each start only once in kRun positions.
 __device__ __forceinline__ int64_t part_of(int i, bool first) { return 2 * (int64_t)(i / kRun) + first; }
 
-template <class O>
-__device__ __forceinline__ void grad_row(const EmbedGradArgs& a, int key, int c, const F8& sum) {
-  O* p = static_cast<O*>(a.grad) + (int64_t)key * a.H + c;
-  F8 f;
+// grad = old + scale * sum, or scale * sum.
+template <int V, class O>
+__device__ __forceinline__ void grad_row(const EmbedGradArgs& a, O* p, const Raw<O, V>& old, const FV<V>& sum, int n) {
+  FV<V> f;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) f.v[j] = a.scale * sum.v[j];
+  for (int j = 0; j < V; ++j) f.v[j] = a.scale * sum.v[j];
   if (a.accumulate) {
-    const F8 old = widen(load(p, a.H - c));
+    const FV<V> o = widen(old);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) f.v[j] = old.v[j] + f.v[j];
+    for (int j = 0; j < V; ++j) f.v[j] = o.v[j] + f.v[j];
   }
-  store(p, f, a.H - c);
+  store(p, f, n);
 }
 
 template <class G, class O>
-__device__ __forceinline__ void embed_item(const EmbedGradArgs& a, int i, int slice, int slices) {
+__device__ __forceinline__ void embed_item(const EmbedGradArgs& a, int i, int slice) {
+  constexpr int V = width_of<G, O>(), kBatch = 8;
   const int lane = threadIdx.x % 64;
   const int32_t* k = a.keys;
-  const int key = __builtin_amdgcn_readfirstlane(k[i]);
-  if (key >= a.V) return;
   const int ahead = i + lane < a.T ? k[i + lane] : -1;
   const int back = i - 1 - lane >= 0 ? k[i - 1 - lane] : -1;
   const int my_row = i + lane < a.T ? a.perm[i + lane] : 0;
+  const int key = __builtin_amdgcn_readfirstlane(ahead);
+  if (key >= a.V) return;
   const uint64_t differ = __ballot(back != key);
-  bool first = true;
-  if (!(differ & 1)) {
-    // a run starts here only a multiple of kRun behind the token's first row
-    if (differ) return;
-    if ((i - lower_bound(k, a.T, key)) % kRun) return;
-    first = false;
-  }
+  // a run starts only a multiple of kRun behind the token's first row
+  const int behind = differ ? __builtin_ctzll(differ) : i - lower_bound(k, a.T, key);
+  if (behind % kRun) return;
+  const bool first = behind == 0;
   const uint64_t other = __ballot(ahead != key);
-  const int n = other ? __builtin_ctzll(other) : kRun;
-  const bool whole = first && (n < kRun || i + kRun >= a.T || k[i + kRun] != key);
-  // (whole waves turn the loop: rows' numbers are read from other lanes)
-  for (int c0 = 512 * slice; c0 < a.H; c0 += 512 * slices) {
-    const int c = c0 + 8 * lane;
-    F8 sum{};
-    const G* g = static_cast<const G*>(a.g) + c;
-    int j = 0;
-    for (; j + 4 <= n; j += 4) {
-      Raw<G> r[4];
+  const int more = other ? __builtin_ctzll(other) : 64, n = min(more, kRun);
+  const bool whole = first && more <= kRun;
+  const int c = V * (64 * slice + lane), left = a.H - c;
+  O* p = static_cast<O*>(a.grad) + (int64_t)key * a.H + c;
+  Raw<O, V> old{};
+  if (whole && a.accumulate) old = load<V>(p, left);
+  const G* g = static_cast<const G*>(a.g) + c;
+  FV<V> sum{};
+  for (int j = 0; j < n; j += kBatch) {
+    Raw<G, V> r[kBatch];
 #pragma unroll
-      for (int m = 0; m < 4; ++m)
-        r[m] = load(g + __builtin_amdgcn_readlane(my_row, j + m) * a.ldg, a.H - c);
+    for (int m = 0; m < kBatch; ++m)
+      if (j + m < n) r[m] = load<V>(g + __builtin_amdgcn_readlane(my_row, j + m) * a.ldg, left);
 #pragma unroll
-      for (int m = 0; m < 4; ++m) {
-        const F8 f = widen(r[m]);
+    for (int m = 0; m < kBatch; ++m) {
+      if (j + m < n) {
+        const FV<V> f = widen(r[m]);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) sum.v[e] += f.v[e];
+        for (int e = 0; e < V; ++e) sum.v[e] += f.v[e];
       }
     }
-    for (; j < n; ++j) {
-      const F8 f = widen(load(g + __builtin_amdgcn_readlane(my_row, j) * a.ldg, a.H - c));
-#pragma unroll
-      for (int e = 0; e < 8; ++e) sum.v[e] += f.v[e];
-    }
-    if (whole) grad_row<O>(a, key, c, sum);
-    else store(a.part + part_of(i, first) * a.H + c, sum, a.H - c);
   }
+  if (whole) grad_row(a, p, old, sum, left);
+  else store(a.part + part_of(i, first) * a.H + c, sum, left);
 }
 
-// Zeroes the rows [v0, v1) of the gradient whose token does not occur.
-template <class O>
-__device__ __forceinline__ void embed_zero(const EmbedGradArgs& a, int v0, int v1) {
-  const int lane = threadIdx.x % 64;
-  uint64_t there = 0;  // bit v - v0; v1 - v0 <= 64
-  for (int p = lower_bound(a.keys, a.T, v0); p < a.T;) {
-    const int k = p + lane < a.T ? a.keys[p + lane] : a.V;
-    const int last = __builtin_amdgcn_readlane(k, 63);
-    for (int v = v0; v < v1; ++v)
-      if (__ballot(k == v)) there |= 1ull << (v - v0);
-    if (last >= v1) break;
-    p = p + 64 < a.T && a.keys[p + 64] != last ? p + 64 : lower_bound(a.keys, a.T, last + 1);
-  }
-  for (int v = v0; v < v1; ++v) {
-    if (there >> (v - v0) & 1) continue;
-    O* p = static_cast<O*>(a.grad) + (int64_t)v * a.H;
-    for (int c = 8 * threadIdx.x; c < a.H; c += 8 * 256) store(p + c, F8{}, a.H - c);
-  }
-}
-
+// A wave a position and slice (64 vectors) of the columns.
 template <class G, class O>
 __global__ __launch_bounds__(256) void embed_grad(EmbedGradArgs a) {
-  if ((int)blockIdx.x < a.item_blocks) {
-    const int wave = threadIdx.x / 64, per = 4 / a.waves;
-    for (int64_t i = (int64_t)blockIdx.x * per + wave / a.waves; i < a.T; i += (int64_t)a.item_blocks * per)
-      embed_item<G, O>(a, __builtin_amdgcn_readfirstlane((int)i), wave % a.waves, a.waves);
-  } else {
-    const int64_t zero_blocks = gridDim.x - a.item_blocks;
-    for (int64_t v = (int64_t)(blockIdx.x - a.item_blocks) * a.zero_rows; v < a.V; v += zero_blocks * a.zero_rows)
-      embed_zero<O>(a, (int)v, (int)min(v + a.zero_rows, (int64_t)a.V));
+  const int64_t items = (int64_t)a.T * a.slices;
+  for (int64_t w = (int64_t)blockIdx.x * 4 + threadIdx.x / 64; w < items; w += (int64_t)gridDim.x * 4) {
+    const int i = __builtin_amdgcn_readfirstlane((int)(w / a.slices));
+    embed_item<G, O>(a, i, (int)(w - (int64_t)i * a.slices));
   }
 }
 
 // Tokens of more than kRun rows: their runs' sums, in order.  A block for the
-// one such token that can start in kRun positions, 512 columns at a time: 16
-// waves sum consecutive sixteenths, and these are summed in order.
+// one such token whose first row can stand in kRun positions, 256 columns at a
+// time: four waves sum consecutive quarters, and these are summed in order.
 template <class O>
-__global__ __launch_bounds__(1024) void embed_grad_join(EmbedGradArgs a) {
-  __shared__ F8 lds[16][64];
+__global__ __launch_bounds__(256) void embed_grad_join(EmbedGradArgs a) {
+  constexpr int V = 4;
+  __shared__ FV<V> lds[4][64];
   const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
   const int32_t* k = a.keys;
-  const int base = blockIdx.x * kRun, p = base + lane;
-  const int key = p < a.T ? k[p] : a.V;
-  const bool start = key < a.V && p + kRun < a.T && k[p + kRun] == key && (p == 0 || k[p - 1] != key);
-  const uint64_t at = __ballot(start);
+  const int p = blockIdx.x * kRun + lane;
+  const int key = lane < kRun && p < a.T ? k[p] : a.V;
+  const int before = lane < kRun && p > 0 && p < a.T ? k[p - 1] : -1;
+  const int behind = lane < kRun && p + kRun < a.T ? k[p + kRun] : -1;
+  const uint64_t at = __ballot(key < a.V && behind == key && before != key);
   if (!at) return;  // the same for all waves
-  const int s = base + __builtin_ctzll(at);
-  const int token = __builtin_amdgcn_readlane(key, s - base);
-  const int end = lower_bound(k, a.T, token + 1);
-  const int runs = (end - s + kRun - 1) / kRun, per = (runs + 15) / 16;
+  const int s = blockIdx.x * kRun + __builtin_ctzll(at);
+  const int token = __builtin_amdgcn_readlane(key, __builtin_ctzll(at));
+  // runs, 64 starts at a time
+  int runs = 0;
+  for (;;) {
+    const int64_t q = s + (int64_t)kRun * (runs + lane);
+    const uint64_t other = __ballot(q >= a.T || k[q] != token);
+    runs += other ? __builtin_ctzll(other) : 64;
+    if (other) break;
+  }
+  const int per = (runs + 3) / 4;
   const int lo = min(wave * per, runs), hi = min(lo + per, runs);
-  for (int c0 = blockIdx.y * 512; c0 < a.H; c0 += gridDim.y * 512) {
-    const int c = c0 + 8 * lane, n = a.H - c;
-    F8 sum{};
+  for (int c0 = blockIdx.y * 64 * V; c0 < a.H; c0 += gridDim.y * 64 * V) {
+    const int c = c0 + V * lane, n = a.H - c;
+    O* grad = static_cast<O*>(a.grad) + (int64_t)token * a.H + c;
+    Raw<O, V> old{};
+    if (a.accumulate && wave == 0) old = load<V>(grad, n);
+    FV<V> sum{};
+#pragma unroll 8
     for (int r = lo; r < hi; ++r) {
-      const F8 f = widen(load(a.part + part_of(s + r * kRun, r == 0) * a.H + c, n));
+      const FV<V> f = widen(load<V>(a.part + part_of(s + r * kRun, r == 0) * a.H + c, n));
 #pragma unroll
-      for (int e = 0; e < 8; ++e) sum.v[e] += f.v[e];
+      for (int e = 0; e < V; ++e) sum.v[e] += f.v[e];
     }
     lds[wave][lane] = sum;
     __syncthreads();
     if (wave == 0 && n > 0) {
-      for (int w = 1; w < 16; ++w) {
-        const F8 f = lds[w][lane];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) sum.v[e] += f.v[e];
+      for (int w = 1; w < 4; ++w) {
+        const FV<V> f = lds[w][lane];
+#pragma unroll
+        for (int e = 0; e < V; ++e) sum.v[e] += f.v[e];
       }
-      grad_row<O>(a, token, c, sum);
+      grad_row(a, grad, old, sum, n);
     }
     __syncthreads();
   }
 }
 
 // --- gradients of a step ---------------------------------------------------------
-constexpr int kTensors = 96;       // of one launch (its arguments stay below 4 KB)
-constexpr int kChunkElems = 16384;  // a block's unit of work
+// Both kernels move all data once and keep none for later (non-temporal, with
+// which reads reach 7.0 TB/s instead of 6.3).  The scaling takes a block for
+// every few KB: a grid that strides over larger chunks moves 10 to 25 % less.
+constexpr int kTensors = 96;        // of one launch (its arguments stay below 4 KB)
+constexpr int kSquareElems = 8192;  // a block's unit of work, squares
+constexpr int kScaleElems = 4096;   // ..., scaling
 
 struct TensorsArgs {
   const void* in[kTensors];
@@ -926,9 +991,10 @@ struct TensorsArgs {
   int32_t first[kTensors + 1];  // the tensor's first chunk
   uint32_t in_f32[kTensors / 32], out_f32[kTensors / 32];
   int count;
-  double* part;
-  int parts;       // of all launches (scaling)
+  double* part;   // sums of squares
+  int parts;      // of all launches; 0: `c` holds the factor
   float* norm;
+  float* c;
   float max_norm;
 };
 
@@ -942,6 +1008,37 @@ __device__ __forceinline__ int tensor_of(const TensorsArgs& a, int chunk) {
   return lo;
 }
 
+// A vector that is not read again soon.
+template <int V, class T>
+__device__ __forceinline__ Raw<T, V> load_once(const T* p, int64_t n) {
+  if (n < V) return load<V>(p, (int)n);
+  constexpr int kBytes = sizeof(T) * V, kWords = kBytes / 4;
+  typedef uint32_t words __attribute__((ext_vector_type(kWords), aligned(sizeof(T))));
+  const words w = __builtin_nontemporal_load(reinterpret_cast<const words*>(p));
+  Raw<T, V> r;
+#pragma unroll
+  for (int i = 0; i < kWords; ++i) r.q[i] = w[i];
+  return r;
+}
+template <int V, class T>
+__device__ __forceinline__ void store_once(T* p, const FV<V>& f, int64_t n) {
+  if (n < V) {
+    store(p, f, (int)n);
+    return;
+  }
+  constexpr int kWords = sizeof(T) * V / 4;
+  typedef uint32_t words __attribute__((ext_vector_type(kWords), aligned(sizeof(T))));
+  words w;
+  if constexpr (sizeof(T) == 4) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) w[i] = __float_as_uint(f.v[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) w[i] = pack_bf16x2(f.v[2 * i], f.v[2 * i + 1]);
+  }
+  __builtin_nontemporal_store(w, reinterpret_cast<words*>(p));
+}
+
 __device__ __forceinline__ double block_sum(double v, double* lds) {
 #pragma unroll
   for (int d = 1; d < 64; d *= 2) v += __shfl_xor(v, d);
@@ -950,24 +1047,23 @@ __device__ __forceinline__ double block_sum(double v, double* lds) {
   return (lds[0] + lds[1]) + (lds[2] + lds[3]);
 }
 
+// Vectors of a chunk are dealt to the block's threads, all in flight.
 template <class T>
 __device__ __forceinline__ void square_sum(const T* p, int64_t n, double (&s)[4]) {
+  constexpr int V = width_of<T>(), kTurns = kSquareElems / (256 * V);
+  Raw<T, V> r[kTurns];
 #pragma unroll
-  for (int h = 0; h < kChunkElems / 2048; h += 4) {
-    Raw<T> r[4];
+  for (int i = 0; i < kTurns; ++i) {
+    const int c = V * (i * 256 + threadIdx.x);
+    r[i] = load_once<V>(p + c, n - c);
+  }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int64_t c = 8 * (int64_t)((h + i) * 256 + threadIdx.x);
-      r[i] = load(p + c, (int)min<int64_t>(n - c, 8));
-    }
+  for (int i = 0; i < kTurns; ++i) {
+    const FV<V> f = widen(r[i]);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const F8 f = widen(r[i]);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const double d = (double)f.v[j];
-        s[j & 3] = __builtin_fma(d, d, s[j & 3]);
-      }
+    for (int j = 0; j < V; ++j) {
+      const double d = (double)f.v[j];
+      s[j & 3] = __builtin_fma(d, d, s[j & 3]);
     }
   }
 }
@@ -980,7 +1076,7 @@ __global__ __launch_bounds__(256) void grads_square(TensorsArgs a) {
   const int chunks = a.first[a.count];
   for (int64_t chunk = blockIdx.x; chunk < chunks; chunk += gridDim.x) {
     const int i = tensor_of(a, (int)chunk);
-    const int64_t at = (chunk - a.first[i]) * kChunkElems, n = a.n[i] - at;
+    const int64_t at = (chunk - a.first[i]) * kSquareElems, n = a.n[i] - at;
     if (a.in_f32[i / 32] >> (i % 32) & 1) square_sum(static_cast<const float*>(a.in[i]) + at, n, s);
     else square_sum(static_cast<const uint16_t*>(a.in[i]) + at, n, s);
   }
@@ -990,53 +1086,65 @@ __global__ __launch_bounds__(256) void grads_square(TensorsArgs a) {
 
 __device__ __forceinline__ double norm_of(const double* part, int parts, double* lds) {
   double s = 0.;
+#pragma unroll 4
   for (int i = threadIdx.x; i < parts; i += 256) s += part[i];
   return __builtin_sqrt(block_sum(s, lds));
 }
+__device__ __forceinline__ float factor_of(double norm, float max_norm) {
+  return norm <= (double)max_norm ? 1.f : (float)((double)max_norm / norm);
+}
 
-__global__ __launch_bounds__(256) void grads_norm(const double* part, int parts, float* norm) {
+// The norm, and the factor of a clipping (c not NULL).
+__global__ __launch_bounds__(256) void grads_norm(const double* part, int parts, float* norm, float* c,
+                                                  float max_norm) {
   __shared__ double lds[4];
   const double v = norm_of(part, parts, lds);
-  if (threadIdx.x == 0) *norm = (float)v;
+  if (threadIdx.x) return;
+  *norm = (float)v;
+  if (c) *c = factor_of(v, max_norm);
 }
 
 template <class T, class O>
 __device__ __forceinline__ void scale_chunk(const T* p, O* o, int64_t n, float c) {
+  constexpr int V = sizeof(T) == 2 && sizeof(O) == 2 ? 8 : 4, kTurns = kScaleElems / (256 * V);
+  Raw<T, V> r[kTurns];
 #pragma unroll
-  for (int h = 0; h < kChunkElems / 2048; h += 4) {
-    Raw<T> r[4];
+  for (int i = 0; i < kTurns; ++i) {
+    const int e = V * (i * 256 + threadIdx.x);
+    r[i] = load_once<V>(p + e, n - e);
+  }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int64_t e = 8 * (int64_t)((h + i) * 256 + threadIdx.x);
-      r[i] = load(p + e, (int)min<int64_t>(n - e, 8));
-    }
+  for (int i = 0; i < kTurns; ++i) {
+    const int e = V * (i * 256 + threadIdx.x);
+    FV<V> f = widen(r[i]);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int64_t e = 8 * (int64_t)((h + i) * 256 + threadIdx.x);
-      F8 f = widen(r[i]);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) f.v[j] *= c;
-      store(o + e, f, (int)min<int64_t>(n - e, 8));
-    }
+    for (int j = 0; j < V; ++j) f.v[j] *= c;
+    store_once(o + e, f, n - e);
   }
 }
 
-// out = c grads; every block finds the norm from the parts for itself.
+// out = c grads.  A few blocks find c from the parts for themselves (one
+// launch less); many read it.
 __global__ __launch_bounds__(256) void grads_scale(TensorsArgs a) {
-  __shared__ double lds[4];
-  const double norm = norm_of(a.part, a.parts, lds);
-  const float c = norm <= (double)a.max_norm ? 1.f : (float)((double)a.max_norm / norm);
-  if (a.norm && blockIdx.x == 0 && threadIdx.x == 0) *a.norm = (float)norm;
+  float c;
+  if (a.parts) {
+    __shared__ double lds[4];
+    const double norm = norm_of(a.part, a.parts, lds);
+    c = factor_of(norm, a.max_norm);
+    if (a.norm && blockIdx.x == 0 && threadIdx.x == 0) *a.norm = (float)norm;
+  } else {
+    c = *a.c;
+  }
   const int chunks = a.first[a.count];
   for (int64_t chunk = blockIdx.x; chunk < chunks; chunk += gridDim.x) {
     const int i = tensor_of(a, (int)chunk);
-    const int64_t at = (chunk - a.first[i]) * kChunkElems, n = a.n[i] - at;
+    if (a.in[i] == a.out[i] && c == 1.f) continue;
+    const int64_t at = (chunk - a.first[i]) * kScaleElems, n = a.n[i] - at;
     const bool f = a.in_f32[i / 32] >> (i % 32) & 1, of = a.out_f32[i / 32] >> (i % 32) & 1;
     const float* p = static_cast<const float*>(a.in[i]) + at;
     const uint16_t* pb = static_cast<const uint16_t*>(a.in[i]) + at;
     float* o = static_cast<float*>(a.out[i]) + at;
     uint16_t* ob = static_cast<uint16_t*>(a.out[i]) + at;
-    if (a.in[i] == a.out[i] && c == 1.f) continue;
     if (f && of) scale_chunk(p, o, n, c);
     else if (f) scale_chunk(p, ob, n, c);
     else if (of) scale_chunk(pb, o, n, c);

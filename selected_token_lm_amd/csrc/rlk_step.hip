@@ -20,9 +20,9 @@ using namespace rlk::step;
 constexpr int64_t kMaxRows = int64_t(1) << 23;
 constexpr int64_t kMaxStride = int64_t(1) << 40;
 constexpr int64_t kMaxTensors = int64_t(1) << 20;
-// of a tensor: more than the memory holds, and a launch's chunks stay below 2^31
-constexpr int64_t kMaxElems = int64_t(1) << 38;
-static_assert(kTensors * (kMaxElems / kChunkElems) < INT32_MAX, "chunk indices");
+// of a tensor: a launch's chunks stay below 2^31
+constexpr int64_t kMaxElems = int64_t(1) << 36;
+static_assert(kTensors * (kMaxElems / kScaleElems) < INT32_MAX, "chunk indices");
 
 inline bool is_dtype(int32_t d) { return d == RLK_DT_F32 || d == RLK_DT_BF16; }
 inline bool aligned_to(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
@@ -72,21 +72,21 @@ inline size_t norm_bwd_bytes(int64_t T, int64_t H) {
   return align256(2 * sizeof(float) * (size_t)norm_parts(T, H) * padded_width(H));
 }
 
-template <class X, class Y, bool kCenter, int R, int N>
+template <class X, class Y, bool kCenter, int R, int E>
 rlk_status launch_norm_fwd(const NormFwdArgs& a, hipStream_t st) {
-  RLK_LAUNCH_FN("norm_fwd", (norm_fwd<X, Y, kCenter, R, N>),
+  RLK_LAUNCH_FN("norm_fwd", (norm_fwd<X, Y, kCenter, R, E>),
                 dim3(blocks_for(ceil_div(a.T, norm_rows(R)), norm_block(R))), dim3(norm_block(R)), st, a);
   return RLK_OK;
 }
 
 template <class X, class Y, bool kCenter>
 rlk_status norm_fwd_by_width(const NormFwdArgs& a, hipStream_t st) {
-  if (a.H <= 512) return launch_norm_fwd<X, Y, kCenter, 64, 1>(a, st);
-  if (a.H <= 1024) return launch_norm_fwd<X, Y, kCenter, 64, 2>(a, st);
-  if (a.H <= 2048) return launch_norm_fwd<X, Y, kCenter, 256, 1>(a, st);
-  if (a.H <= 4096) return launch_norm_fwd<X, Y, kCenter, 256, 2>(a, st);
-  if (a.H <= 8192) return launch_norm_fwd<X, Y, kCenter, 512, 2>(a, st);
-  if (a.H <= kWideFwd) return launch_norm_fwd<X, Y, kCenter, 1024, 2>(a, st);
+  if (a.H <= 512) return launch_norm_fwd<X, Y, kCenter, 64, 8>(a, st);
+  if (a.H <= 1024) return launch_norm_fwd<X, Y, kCenter, 64, 16>(a, st);
+  if (a.H <= 2048) return launch_norm_fwd<X, Y, kCenter, 256, 8>(a, st);
+  if (a.H <= 4096) return launch_norm_fwd<X, Y, kCenter, 256, 16>(a, st);
+  if (a.H <= 8192) return launch_norm_fwd<X, Y, kCenter, 512, 16>(a, st);
+  if (a.H <= kWideFwd) return launch_norm_fwd<X, Y, kCenter, 1024, 16>(a, st);
   RLK_LAUNCH_FN("norm_fwd_wide", (norm_fwd_wide<X, Y, kCenter>), dim3(blocks_for(a.T, 1024)), dim3(1024), st, a);
   return RLK_OK;
 }
@@ -126,13 +126,13 @@ rlk_status norm_forward(const void* x, int32_t x_dtype, int64_t ldx, const void*
   return ok();
 }
 
-template <class X, class G, bool kCenter, int R, int N>
+template <class X, class G, bool kCenter, int R, int E>
 rlk_status launch_norm_bwd(const NormBwdArgs& a, int64_t parts, bool sums, hipStream_t st) {
   static_assert(norm_rows(R) == 1 || norm_rows(R) == 4, "norm_row_group");
   if (sums)
-    RLK_LAUNCH_FN("norm_bwd", (norm_bwd<X, G, kCenter, true, R, N>), dim3((unsigned)parts), dim3(norm_block(R)), st, a);
+    RLK_LAUNCH_FN("norm_bwd", (norm_bwd<X, G, kCenter, true, R, E>), dim3((unsigned)parts), dim3(norm_block(R)), st, a);
   else
-    RLK_LAUNCH_FN("norm_bwd", (norm_bwd<X, G, kCenter, false, R, N>), dim3((unsigned)parts), dim3(norm_block(R)), st, a);
+    RLK_LAUNCH_FN("norm_bwd", (norm_bwd<X, G, kCenter, false, R, E>), dim3((unsigned)parts), dim3(norm_block(R)), st, a);
   return RLK_OK;
 }
 
@@ -143,14 +143,14 @@ rlk_status norm_bwd_by_width(const NormBwdArgs& a, int64_t parts, bool sums, hip
       RLK_LAUNCH_FN("norm_bwd_wide", (norm_bwd_wide<X, G, kCenter>), dim3(blocks_for(a.T, 1024)), dim3(1024), st, a);
     if (sums)
       RLK_LAUNCH_FN("norm_sums_wide", (norm_sums_wide<X, G, kCenter>),
-                    dim3((unsigned)ceil_div(a.H, 2048), (unsigned)parts), dim3(256), st, a);
+                    dim3((unsigned)ceil_div(a.H, 256 * width_of<X, G>()), (unsigned)parts), dim3(256), st, a);
     return RLK_OK;
   }
-  if (a.H <= 512) return launch_norm_bwd<X, G, kCenter, 64, 1>(a, parts, sums, st);
-  if (a.H <= 1024) return launch_norm_bwd<X, G, kCenter, 64, 2>(a, parts, sums, st);
-  if (a.H <= 2048) return launch_norm_bwd<X, G, kCenter, 256, 1>(a, parts, sums, st);
-  if (a.H <= 4096) return launch_norm_bwd<X, G, kCenter, 256, 2>(a, parts, sums, st);
-  return launch_norm_bwd<X, G, kCenter, 512, 2>(a, parts, sums, st);
+  if (a.H <= 512) return launch_norm_bwd<X, G, kCenter, 64, 8>(a, parts, sums, st);
+  if (a.H <= 1024) return launch_norm_bwd<X, G, kCenter, 64, 16>(a, parts, sums, st);
+  if (a.H <= 2048) return launch_norm_bwd<X, G, kCenter, 256, 8>(a, parts, sums, st);
+  if (a.H <= 4096) return launch_norm_bwd<X, G, kCenter, 256, 16>(a, parts, sums, st);
+  return launch_norm_bwd<X, G, kCenter, 512, 16>(a, parts, sums, st);
 }
 
 template <bool kCenter>
@@ -269,22 +269,19 @@ rlk_status launch_embed(const EmbedArgs& a, hipStream_t st) {
 }
 
 template <class G, class O>
-rlk_status launch_embed_grad(EmbedGradArgs a, hipStream_t st) {
-  const int64_t per = 4 / a.waves;
-  a.item_blocks = a.T ? (int)blocks_for(ceil_div(a.T, per), 1024) : 0;
-  // about 64 KB of the gradient to a block
-  a.zero_rows = (int)std::max<int64_t>(4, std::min<int64_t>(64, (64 << 10) / (sizeof(O) * (int64_t)a.H)));
-  const int64_t zero_blocks = a.accumulate ? 0 : blocks_for(ceil_div(a.V, a.zero_rows), 1024);
-  if (a.item_blocks + zero_blocks)
-    RLK_LAUNCH_FN("embed_grad", (embed_grad<G, O>), dim3((unsigned)(a.item_blocks + zero_blocks)), dim3(256), st, a);
+rlk_status launch_embed_grad(const EmbedGradArgs& a, hipStream_t st) {
+  if (a.T == 0) return RLK_OK;
+  RLK_LAUNCH_FN("embed_grad", (embed_grad<G, O>), dim3(blocks_for(ceil_div((int64_t)a.T * a.slices, 4))), dim3(256),
+                st, a);
   if (a.T > kRun)
     RLK_LAUNCH_FN("embed_grad_join", (embed_grad_join<O>),
-                  dim3((unsigned)ceil_div(a.T, kRun), (unsigned)ceil_div(a.H, 512)), dim3(1024), st, a);
+                  dim3((unsigned)ceil_div(a.T, kRun), (unsigned)ceil_div(a.H, 256)), dim3(256), st, a);
   return RLK_OK;
 }
 
-rlk_status sort_tokens(const IdsArg& ids, int64_t T, int64_t V, const EmbedWs& L, void* ws, const int32_t** keys,
-                       const int32_t** perm, hipStream_t st) {
+// Sorts the tokens by (id, t) and zeroes zero.p on the way.
+rlk_status sort_tokens(const IdsArg& ids, int64_t T, int64_t V, const ZeroArgs& zero, const EmbedWs& L, void* ws,
+                       const int32_t** keys, const int32_t** perm, hipStream_t st) {
   char* base = static_cast<char*>(ws);
   int32_t* k[2];
   int32_t* p[2];
@@ -294,11 +291,28 @@ rlk_status sort_tokens(const IdsArg& ids, int64_t T, int64_t V, const EmbedWs& L
   }
   *keys = k[0];
   *perm = p[0];
+  // blocks that zero: 4 KB each, which is faster (6.7 TB/s) than fewer blocks
+  // that stride (4.3 to 5.4)
+  const int64_t zero_blocks = zero.p ? std::min<int64_t>(kRowBlocks, ceil_div(zero.bytes, 4096)) : 0;
   if (T <= kRankRows) {
-    RLK_LAUNCH(step::embed_rank, dim3((unsigned)ceil_div(T, 64)), dim3(1024), st, ids, (int)T, (int)V, k[0], p[0]);
+    RankArgs a{};
+    a.ids = ids;
+    a.keys = k[0];
+    a.perm = p[0];
+    a.T = (int)T;
+    a.V = (int)V;
+    a.zero = zero;
+    const bool few = T <= 4096;
+    a.blocks = (int)ceil_div(T, few ? 16 : 64);
+    const int64_t zeroing = few ? zero_blocks : ceil_div(zero_blocks, 4);
+    if (a.blocks + zeroing == 0) return RLK_OK;
+    if (few)
+      RLK_LAUNCH_FN("embed_rank", (embed_rank<16, 4096>), dim3((unsigned)(a.blocks + zeroing)), dim3(256), st, a);
+    else
+      RLK_LAUNCH_FN("embed_rank", (embed_rank<64, kRankRows>), dim3((unsigned)(a.blocks + zeroing)), dim3(1024), st, a);
     return RLK_OK;
   }
-  const int bits = key_bits(V), digit = (int)ceil_div(bits, L.passes);
+  const int bits = (int)ceil_div(key_bits(V), L.passes);
   RadixArgs a{};
   a.ids = ids;
   a.T = (int)T;
@@ -306,17 +320,18 @@ rlk_status sort_tokens(const IdsArg& ids, int64_t T, int64_t V, const EmbedWs& L
   a.tiles = (int)L.tiles;
   a.hist = reinterpret_cast<int32_t*>(base + L.hist);
   a.total = reinterpret_cast<int32_t*>(base + L.total_);
-  a.bits = digit;
+  a.bits = bits;
+  a.zero = zero;
   for (int pass = 0; pass < L.passes; ++pass) {
     const int to = pass & 1;
     a.first = pass == 0;
-    a.shift = pass * digit;
+    a.shift = pass * bits;
     a.keys_in = k[1 - to];
     a.perm_in = p[1 - to];
     a.keys = k[to];
     a.perm = p[to];
-    RLK_LAUNCH(step::radix_count, dim3((unsigned)L.tiles), dim3(256), st, a);
-    RLK_LAUNCH(step::radix_scan, dim3(1u << digit), dim3(256), st, a);
+    RLK_LAUNCH(step::radix_count, dim3((unsigned)(L.tiles + (a.first ? zero_blocks : 0))), dim3(256), st, a);
+    RLK_LAUNCH(step::radix_scan, dim3(1u << bits), dim3(256), st, a);
     RLK_LAUNCH(step::radix_scatter, dim3((unsigned)L.tiles), dim3(256), st, a);
     *keys = a.keys;
     *perm = a.perm;
@@ -327,7 +342,9 @@ rlk_status sort_tokens(const IdsArg& ids, int64_t T, int64_t V, const EmbedWs& L
 // --- gradients of a step -----------------------------------------------------------
 // Parts of the sum of squares: 2048 blocks fill the card; many launches share them.
 constexpr int64_t kGradParts = 2048;
-inline size_t grads_bytes(int64_t n) { return align256(sizeof(double) * (size_t)(kGradParts + ceil_div(n, kTensors) + 1)); }
+// the parts, and the factor behind them
+inline size_t grads_parts_bytes(int64_t n) { return sizeof(double) * (size_t)(kGradParts + ceil_div(n, kTensors) + 1); }
+inline size_t grads_bytes(int64_t n) { return align256(grads_parts_bytes(n) + sizeof(float)); }
 
 struct Span {
   uintptr_t lo, hi;
@@ -341,7 +358,7 @@ rlk_status check_tensors(const void* const* grads, const int64_t* sizes, const i
   for (int32_t i = 0; i < n; ++i) {
     if (!is_dtype(dtypes[i])) return fail(RLK_ERR_BAD_ARG, "dtypes[%d]=%d", i, dtypes[i]);
     if (sizes[i] < 0 || sizes[i] > kMaxElems)
-      return fail(RLK_ERR_BAD_SHAPE, "sizes[%d]=%lld out of [0, 2^38]", i, (long long)sizes[i]);
+      return fail(RLK_ERR_BAD_SHAPE, "sizes[%d]=%lld out of [0, 2^36]", i, (long long)sizes[i]);
     if (sizes[i] > 0 && !grads[i]) return fail(RLK_ERR_NULL_ARG, "grads[%d] is NULL", i);
     if (!aligned_as(grads[i], dtypes[i]))
       return fail(RLK_ERR_BAD_ALIGNMENT, "grads[%d] must be aligned to its elements", i);
@@ -385,12 +402,12 @@ rlk_status check_outputs(const void* const* grads, const int64_t* sizes, const i
 // f(args, chunks).
 template <class F>
 rlk_status each_batch(const void* const* grads, const int64_t* sizes, const int32_t* dtypes, int32_t n,
-                      void* const* out, const int32_t* out_dtypes, F f) {
+                      void* const* out, const int32_t* out_dtypes, int64_t chunk, F f) {
   for (int32_t i = 0; i < n;) {
     TensorsArgs a{};
     int64_t chunks = 0;
     for (; i < n && a.count < kTensors; ++i) {
-      const int64_t c = ceil_div(sizes[i], kChunkElems);
+      const int64_t c = ceil_div(sizes[i], chunk);
       if (c == 0) continue;
       const int k = a.count++;
       a.in[k] = grads[i];
@@ -415,7 +432,7 @@ rlk_status square_parts(const void* const* grads, const int64_t* sizes, const in
                         int* parts, hipStream_t st) {
   const int64_t most = std::max<int64_t>(1, kGradParts / std::max<int64_t>(1, ceil_div(n, kTensors)));
   *parts = 0;
-  return each_batch(grads, sizes, dtypes, n, nullptr, nullptr, [&](TensorsArgs& a, int64_t chunks) {
+  return each_batch(grads, sizes, dtypes, n, nullptr, nullptr, kSquareElems, [&](TensorsArgs& a, int64_t chunks) {
     const int blocks = (int)std::min(chunks, most);
     a.part = part + *parts;
     *parts += blocks;
@@ -507,8 +524,8 @@ rlk_status rlk_embed_bwd(const void* ids, int32_t id_bytes, const void* g, int32
   RLK_TRY(check_device());
   hipStream_t st = static_cast<hipStream_t>(stream);
   EmbedGradArgs a{};
-  if (T > 0)
-    RLK_TRY(sort_tokens(IdsArg{ids, ignore_index, id_bytes == 8}, T, V, L, ws, &a.keys, &a.perm, st));
+  const ZeroArgs zero{accumulate ? nullptr : static_cast<char*>(grad_E), (int64_t)size_of(grad_dtype) * V * H};
+  RLK_TRY(sort_tokens(IdsArg{ids, ignore_index, id_bytes == 8}, T, V, zero, L, ws, &a.keys, &a.perm, st));
   a.g = g;
   a.ldg = ldg;
   a.grad = grad_E;
@@ -518,7 +535,7 @@ rlk_status rlk_embed_bwd(const void* ids, int32_t id_bytes, const void* g, int32
   a.V = (int)V;
   a.scale = scale;
   a.accumulate = accumulate;
-  a.waves = H <= 512 ? 1 : H <= 1024 ? 2 : 4;
+  a.slices = (int)ceil_div(H, 64 * (g_dtype == RLK_DT_F32 && grad_dtype == RLK_DT_F32 ? 4 : 8));
   const bool gf = g_dtype == RLK_DT_F32, of = grad_dtype == RLK_DT_F32;
   RLK_TRY(gf ? (of ? launch_embed_grad<float, float>(a, st) : launch_embed_grad<float, uint16_t>(a, st))
              : (of ? launch_embed_grad<uint16_t, float>(a, st) : launch_embed_grad<uint16_t, uint16_t>(a, st)));
@@ -536,7 +553,7 @@ rlk_status rlk_grad_norm(const void* const* grads, const int64_t* sizes, const i
   double* part = static_cast<double*>(ws);
   int parts = 0;
   RLK_TRY(square_parts(grads, sizes, dtypes, n, part, &parts, st));
-  RLK_LAUNCH(step::grads_norm, dim3(1), dim3(256), st, part, parts, norm);
+  RLK_LAUNCH(step::grads_norm, dim3(1), dim3(256), st, part, parts, norm, static_cast<float*>(nullptr), 0.f);
   return ok();
 }
 
@@ -554,18 +571,22 @@ rlk_status rlk_clip_grads(const void* const* grads, const int64_t* sizes, const 
   double* part = static_cast<double*>(ws);
   int parts = 0;
   RLK_TRY(square_parts(grads, sizes, dtypes, n, part, &parts, st));
-  if (parts == 0) {
-    RLK_LAUNCH(step::grads_norm, dim3(1), dim3(256), st, part, parts, norm);
-    return ok();
-  }
+  // the factor has a launch of its own where more blocks than the card holds
+  // at once would find it for themselves (or none would)
+  int64_t blocks = 0;
+  for (int32_t i = 0; i < n; ++i) blocks += ceil_div(sizes[i], kScaleElems);
+  const bool apart = blocks == 0 || blocks > kGradParts;
+  float* c = reinterpret_cast<float*>(static_cast<char*>(ws) + grads_parts_bytes(n));
+  if (apart) RLK_LAUNCH(step::grads_norm, dim3(1), dim3(256), st, part, parts, norm, c, max_norm);
   bool first = true;
-  RLK_TRY(each_batch(grads, sizes, dtypes, n, out, out_dtypes, [&](TensorsArgs& a, int64_t chunks) {
+  RLK_TRY(each_batch(grads, sizes, dtypes, n, out, out_dtypes, kScaleElems, [&](TensorsArgs& a, int64_t chunks) {
     a.part = part;
-    a.parts = parts;
+    a.parts = apart ? 0 : parts;
     a.norm = first ? norm : nullptr;
+    a.c = c;
     a.max_norm = max_norm;
     first = false;
-    RLK_LAUNCH(step::grads_scale, dim3((unsigned)std::min(chunks, kGradParts)), dim3(256), st, a);
+    RLK_LAUNCH(step::grads_scale, dim3(blocks_for(chunks)), dim3(256), st, a);
     return (rlk_status)RLK_OK;
   }));
   return ok();

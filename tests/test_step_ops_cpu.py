@@ -175,7 +175,7 @@ def test_gradient_list_refusals():
         assert f(lists(3, None)[0], s, c, 3, **more) == NULL_ARG
         assert f(lists(3, OFF2)[0], s, c, 3, **more) == BAD_ALIGN
         assert f(p, lists(3, size=-1)[1], c, 3, **more) == BAD_SHAPE
-        assert f(p, lists(3, size=(1 << 38) + 1)[1], c, 3, **more) == BAD_SHAPE
+        assert f(p, lists(3, size=(1 << 36) + 1)[1], c, 3, **more) == BAD_SHAPE
         assert f(p, s, lists(3, code=2)[2], 3, **more) == BAD_ARG
     for most in (-1e-9, NAN, -INF):
         assert clip_call(p, s, c, 3, most, p, c) == BAD_ARG
