@@ -547,41 +547,58 @@ struct EmbedArgs {
   const void* E;
   void* out;
   int T, H, V;
+  int slices;  // of a row, a wave each
   float scale;
 };
 
-// out[t] = scale E[id]: L lanes a row, each vectors lane, lane + L, ...
-template <class E, class O, int L>
+// out[t] = scale E[id]: a wave for kRowVecs vectors a lane of a row, all loaded
+// before the first is stored.
+constexpr int kRowVecs = 4;
+
+template <class E, class O>
 __global__ __launch_bounds__(256) void embed_rows(EmbedArgs a) {
   constexpr int V = width_of<E, O>();
-  const int lane = threadIdx.x % L;
-  for (int64_t t = (int64_t)blockIdx.x * (256 / L) + threadIdx.x / L; t < a.T; t += (int64_t)gridDim.x * (256 / L)) {
+  const int lane = threadIdx.x % 64;
+  const int64_t items = (int64_t)a.T * a.slices;
+  for (int64_t w = (int64_t)blockIdx.x * 4 + threadIdx.x / 64; w < items; w += (int64_t)gridDim.x * 4) {
+    const int64_t t = w / a.slices;
+    const int c = V * (64 * kRowVecs * (int)(w - t * a.slices) + lane);
     const int64_t id = id_at(a.ids, t);
     O* out = static_cast<O*>(a.out) + t * a.H;
-    const bool ignored = id == a.ids.ignore;
-    if (ignored || id < 0 || id >= a.V) {
-      FV<V> f;
+    const bool ignored = id == a.ids.ignore, bad = id < 0 || id >= a.V;
+    Raw<E, V> r[kRowVecs] = {};
+    if (!ignored && !bad) {
+      const E* row = static_cast<const E*>(a.E) + id * a.H;
 #pragma unroll
-      for (int j = 0; j < V; ++j) f.v[j] = ignored ? 0.f : __builtin_nanf("");
-      for (int c = V * lane; c < a.H; c += V * L) store(out + c, f, a.H - c);
-      continue;
+      for (int i = 0; i < kRowVecs; ++i) r[i] = load<V>(row + c + 64 * V * i, a.H - c - 64 * V * i);
     }
-    const E* row = static_cast<const E*>(a.E) + id * a.H;
-#pragma unroll 4
-    for (int c = V * lane; c < a.H; c += V * L) {
-      FV<V> f = widen(load<V>(row + c, a.H - c));
+    const float nan = __builtin_nanf("");
 #pragma unroll
-      for (int j = 0; j < V; ++j) f.v[j] *= a.scale;
-      store(out + c, f, a.H - c);
+    for (int i = 0; i < kRowVecs; ++i) {
+      FV<V> f = widen(r[i]);
+#pragma unroll
+      for (int j = 0; j < V; ++j) f.v[j] = ignored ? 0.f : bad ? nan : f.v[j] * a.scale;
+      store(out + c + 64 * V * i, f, a.H - c - 64 * V * i);
     }
   }
 }
 
-// The gradient goes by positions of the tokens sorted by (id, t): keys[i] and
-// the row perm[i].  Ids that reach no row have the key V and stand last.
-__device__ __forceinline__ int key_of(const IdsArg& a, int64_t t, int V) {
+// The gradient goes by positions of the tokens sorted by (key, t): keys[i] and
+// the row perm[i].  A key is the token with its `low` lowest bits moved to the
+// top (frequent tokens have low ids: these bits spread them); ids that reach
+// no row have the key `none`, above all others.
+struct KeyMap {
+  int low, high;  // bits; low + high cover the vocabulary
+  int none;
+  int V;
+};
+__device__ __forceinline__ int key_of(const IdsArg& a, const KeyMap& m, int64_t t) {
   const int64_t id = id_at(a, t);
-  return id == a.ignore || id < 0 || id >= V ? V : (int)id;
+  if (id == a.ignore || id < 0 || id >= m.V) return m.none;
+  return ((int)id & ((1 << m.low) - 1)) << m.high | (int)id >> m.low;
+}
+__device__ __forceinline__ int token_of(const KeyMap& m, int key) {
+  return (key & ((1 << m.high) - 1)) << m.low | key >> m.high;
 }
 
 // Zeroes of the dense gradient, by the blocks of a sort's launch that do not
@@ -601,80 +618,105 @@ __device__ __forceinline__ void zero_share(const ZeroArgs& z, int64_t block, int
     reinterpret_cast<uint16_t*>(z.p + 16 * n16)[threadIdx.x] = 0;
 }
 
-// Up to kRankRows tokens: a token's place is the number of tokens before it in
-// that order, counted against all others, which wait in LDS.  kTok tokens a
-// block; a thread counts a sixteenth of the others for one of them.  Up to
-// 4096 tokens small blocks with little LDS leave the units to the blocks that
-// zero; beyond, fewer blocks read all ids.
-constexpr int kRankRows = 16384;
+// Up to kRankRows tokens, one launch: every block sorts all keys into buckets by
+// their first ten bits in LDS (in any order), and finds the places of kTok
+// tokens: the buckets before, and the tokens before it in its own, which 16
+// threads count.  Up to 4096 tokens small blocks with little LDS leave the
+// units to the blocks that zero; beyond, fewer blocks read all ids.
+// (16384 tokens: 9 us, against 25 for counting against all others.)
+constexpr int kRankRows = 16384, kBucketBits = 10, kBuckets = 1 << kBucketBits;
 
 struct RankArgs {
   IdsArg ids;
+  KeyMap map;
   int32_t* keys;
   int32_t* perm;
-  int T, V;
+  int T;
   int blocks;  // that rank
   ZeroArgs zero;
 };
 
-template <int kTok, int kMost>
+template <int kTok>
 __global__ __launch_bounds__(16 * kTok) void embed_rank(RankArgs a) {
-  constexpr int kThreads = 16 * kTok, kSets = 16;  // others: groups of four, set, set + 16, ...
-  __shared__ int32_t all[kMost];
+  constexpr int kThreads = 16 * kTok, kMost = 256 * kTok, kKeys = 16;
+  __shared__ uint32_t entry[kMost];      // by bucket: the key's other bits and t
+  __shared__ int32_t bucket[kBuckets];   // its entries, then its first one, then its end
+  __shared__ int32_t waves[kThreads / 64];
   __shared__ int32_t count[kThreads / 64][64];
   if ((int)blockIdx.x >= a.blocks) {
     zero_share(a.zero, blockIdx.x - a.blocks, gridDim.x - a.blocks, kThreads);
     return;
   }
-  const int tok = threadIdx.x % kTok, set = threadIdx.x / kTok;
-  const int t0 = kTok * blockIdx.x, t = t0 + tok;
-  // turns of 64 others; what stands past T precedes nothing
-  const int turns = (a.T + 63) / 64;
+  const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
+  const int keys = (a.T + kThreads - 1) / kThreads;  // of a thread
+  constexpr int kTBits = 14;
+  static_assert(kRankRows <= 1 << kTBits && kMost <= kRankRows, "t in an entry");
+  for (int i = threadIdx.x; i < kBuckets; i += kThreads) bucket[i] = 0;
+  __syncthreads();
+  int key[kKeys];
 #pragma unroll
-  for (int i = 0; i < kMost / kThreads; i += 4) {
-    if (i * kThreads >= 64 * turns) break;
-    int32_t k[4];
+  for (int i = 0; i < kKeys; ++i) {
+    const int t = i * kThreads + threadIdx.x;
+    key[i] = i < keys && t < a.T ? key_of(a.ids, a.map, t) : a.map.none;
+  }
 #pragma unroll
-    for (int m = 0; m < 4; ++m) {
-      const int o = (i + m) * kThreads + threadIdx.x;
-      k[m] = o < a.T ? key_of(a.ids, o, a.V) : INT32_MAX;
-    }
+  for (int i = 0; i < kKeys; ++i)
+    if (key[i] != a.map.none) atomicAdd(&bucket[key[i] >> a.map.high], 1);
+  __syncthreads();
+  // exclusive sums: kBuckets / kThreads buckets a thread
+  constexpr int kPer = kBuckets / kThreads;
+  int own[kPer], sum = 0;
 #pragma unroll
-    for (int m = 0; m < 4; ++m) all[(i + m) * kThreads + threadIdx.x] = k[m];
+  for (int i = 0; i < kPer; ++i) {
+    own[i] = sum;
+    sum += bucket[threadIdx.x * kPer + i];
+  }
+  int upto = sum;
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2) {
+    const int o = __shfl_up(upto, d);
+    if (lane >= d) upto += o;
+  }
+  if (lane == 63) waves[wave] = upto;
+  __syncthreads();
+  int before = upto - sum;
+  for (int w = 0; w < wave; ++w) before += waves[w];
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) bucket[threadIdx.x * kPer + i] = before + own[i];
+  __syncthreads();
+  const int rest = (1 << a.map.high) - 1;
+#pragma unroll
+  for (int i = 0; i < kKeys; ++i) {
+    if (key[i] == a.map.none) continue;
+    const int at = atomicAdd(&bucket[key[i] >> a.map.high], 1);
+    entry[at] = (uint32_t)(key[i] & rest) << kTBits | (uint32_t)(i * kThreads + threadIdx.x);
   }
   __syncthreads();
-  const int key = t < a.T ? all[t] : INT32_MIN;
-  const int4* p = reinterpret_cast<const int4*>(all) + set;
-  const int own = t0 / 64;  // the turn with this block's tokens
-  int n = 0;
+  const int tok = threadIdx.x % kTok, set = threadIdx.x / kTok;
+  const int t = kTok * blockIdx.x + tok;
+  const int mine = t < a.T ? key_of(a.ids, a.map, t) : a.map.none;
+  int n = 0, first = 0;
+  if (mine != a.map.none) {
+    const int b = mine >> a.map.high;
+    const uint32_t e = (uint32_t)(mine & rest) << kTBits | (uint32_t)t;
+    first = b ? bucket[b - 1] : 0;
+    const int end = bucket[b];
 #pragma unroll 4
-  for (int j = 0; j < own; ++j) {
-    const int4 v = p[j * kSets];
-    n += (v.x <= key) + (v.y <= key) + (v.z <= key) + (v.w <= key);
-  }
-  {
-    const int4 v = p[own * kSets];
-    const int o = 4 * (own * kSets + set);
-    n += v.x < key || (v.x == key && o < t);
-    n += v.y < key || (v.y == key && o + 1 < t);
-    n += v.z < key || (v.z == key && o + 2 < t);
-    n += v.w < key || (v.w == key && o + 3 < t);
-  }
-#pragma unroll 4
-  for (int j = own + 1; j < turns; ++j) {
-    const int4 v = p[j * kSets];
-    n += (v.x < key) + (v.y < key) + (v.z < key) + (v.w < key);
+    for (int i = first + set; i < end; i += 16) n += entry[i] < e;
   }
   // a token's sets: lanes kTok apart, then the waves
 #pragma unroll
   for (int d = kTok; d < 64; d *= 2) n += __shfl_xor(n, d);
-  count[threadIdx.x / 64][threadIdx.x % 64] = n;
+  count[wave][lane] = n;
   __syncthreads();
   if (threadIdx.x >= kTok || t >= a.T) return;
-  int at = 0;
+  // places behind the tokens that reach a row
+  if (t >= bucket[kBuckets - 1]) a.keys[t] = a.map.none;
+  if (mine == a.map.none) return;
+  int at = first;
 #pragma unroll
   for (int w = 0; w < kThreads / 64; ++w) at += count[w][tok];
-  a.keys[at] = key;
+  a.keys[at] = mine;
   a.perm[at] = t;
 }
 
@@ -694,18 +736,19 @@ __device__ __forceinline__ uint64_t same_digit(int d, int bits) {
 
 struct RadixArgs {
   IdsArg ids;  // the first pass's input
+  KeyMap map;
   const int32_t* keys_in;
   const int32_t* perm_in;
   int32_t* keys;
   int32_t* perm;
   int32_t* hist;   // [kBins][tiles]
   int32_t* total;  // [kBins]
-  int T, V, tiles;
+  int T, tiles;
   int shift, bits, first;
   ZeroArgs zero;  // for blocks behind the tiles of the first pass's counts
 };
 __device__ __forceinline__ int radix_key(const RadixArgs& a, int t) {
-  return a.first ? key_of(a.ids, t, a.V) : a.keys_in[t];
+  return a.first ? key_of(a.ids, a.map, t) : a.keys_in[t];
 }
 
 __global__ __launch_bounds__(256) void radix_count(RadixArgs a) {
@@ -834,9 +877,8 @@ __device__ __forceinline__ int lower_bound(const int32_t* keys, int n, int v) {
   return lo;
 }
 
-// Rows of one token are summed in runs of kRun from its first on, all of a
-// run's rows in flight together, a wave and a vector a lane of the columns
-// each; a token of more rows leaves its runs' sums in parts.
+// Rows of one token are summed in runs of kRun from its first on; a token of
+// more rows leaves its runs' sums in parts.
 constexpr int kRun = 16;
 
 struct EmbedGradArgs {
@@ -846,10 +888,12 @@ struct EmbedGradArgs {
   int64_t ldg;
   void* grad;
   float* part;  // [2 * runs][H], runs = ceil(T / kRun)
-  int T, H, V;
+  KeyMap map;
+  int T, H;
   float scale;
   int accumulate;
   int slices;  // of the columns, a wave each
+  int window;  // positions of a wave
 };
 
 // The part of the run that starts at position i: a token's first run, or a
@@ -870,55 +914,84 @@ __device__ __forceinline__ void grad_row(const EmbedGradArgs& a, O* p, const Raw
   store(p, f, n);
 }
 
-template <class G, class O>
-__device__ __forceinline__ void embed_item(const EmbedGradArgs& a, int i, int slice) {
-  constexpr int V = width_of<G, O>(), kBatch = 8;
-  const int lane = threadIdx.x % 64;
-  const int32_t* k = a.keys;
-  const int ahead = i + lane < a.T ? k[i + lane] : -1;
-  const int back = i - 1 - lane >= 0 ? k[i - 1 - lane] : -1;
-  const int my_row = i + lane < a.T ? a.perm[i + lane] : 0;
-  const int key = __builtin_amdgcn_readfirstlane(ahead);
-  if (key >= a.V) return;
-  const uint64_t differ = __ballot(back != key);
-  // a run starts only a multiple of kRun behind the token's first row
-  const int behind = differ ? __builtin_ctzll(differ) : i - lower_bound(k, a.T, key);
-  if (behind % kRun) return;
-  const bool first = behind == 0;
-  const uint64_t other = __ballot(ahead != key);
-  const int more = other ? __builtin_ctzll(other) : 64, n = min(more, kRun);
-  const bool whole = first && more <= kRun;
-  const int c = V * (64 * slice + lane), left = a.H - c;
-  O* p = static_cast<O*>(a.grad) + (int64_t)key * a.H + c;
-  Raw<O, V> old{};
-  if (whole && a.accumulate) old = load<V>(p, left);
-  const G* g = static_cast<const G*>(a.g) + c;
-  FV<V> sum{};
-  for (int j = 0; j < n; j += kBatch) {
-    Raw<G, V> r[kBatch];
-#pragma unroll
-    for (int m = 0; m < kBatch; ++m)
-      if (j + m < n) r[m] = load<V>(g + __builtin_amdgcn_readlane(my_row, j + m) * a.ldg, left);
-#pragma unroll
-    for (int m = 0; m < kBatch; ++m) {
-      if (j + m < n) {
-        const FV<V> f = widen(r[m]);
-#pragma unroll
-        for (int e = 0; e < V; ++e) sum.v[e] += f.v[e];
-      }
-    }
-  }
-  if (whole) grad_row(a, p, old, sum, left);
-  else store(a.part + part_of(i, first) * a.H + c, sum, left);
+// Vectors by the gradient's type: an fp32 row that is read and written goes by
+// 16 bytes a lane (16384 rows of H = 2048 added to fp32: 33 us, 42 by 32 bytes).
+template <class O>
+constexpr int grad_width() {
+  return sizeof(O) == 4 ? 4 : 8;
 }
 
-// A wave a position and slice (64 vectors) of the columns.
+// A wave takes the runs that start in a window of a.window (<= 16) positions,
+// for 64 vectors of the columns: their rows follow each other in the sorted
+// order, up to 15 past the window, and are loaded kBatch at a time.
+template <class G, class O>
+__device__ __forceinline__ void embed_window(const EmbedGradArgs& a, int p0, int slice) {
+  constexpr int V = grad_width<O>(), kBatch = 8;
+  const int lane = threadIdx.x % 64;
+  const int32_t* k = a.keys;
+  // lane l: position q = p0 + l - 16
+  const int q = p0 + lane - kRun;
+  const bool in = q >= 0 && q < a.T;
+  const int key = in ? k[q] : -1;
+  const int row = in ? a.perm[q] : 0;
+  const int prev = __shfl_up(key, 1), next = __shfl_down(key, 1);
+  const int key0 = __builtin_amdgcn_readlane(key, kRun);
+  if (key0 == a.map.none) return;
+  // the first position of a lane's token: the last one at or before it whose
+  // predecessor differs (found outside where 16 rows before p0 are the same)
+  const uint64_t starts = __ballot(lane > 0 && key != prev);
+  const uint64_t upto = starts & (~0ull >> (63 - lane));
+  int start0 = 0;
+  if (!(starts & (~0ull >> (63 - kRun)))) start0 = lower_bound(k, a.T, key0);
+  const int start = upto ? p0 - kRun + 63 - __builtin_clzll(upto) : start0;
+  const int behind = q - start, head = lane - (behind & (kRun - 1));
+  const bool mine = in && key != a.map.none && lane >= kRun && head >= kRun && head < kRun + a.window;
+  const uint64_t own = __ballot(mine);
+  const int token = token_of(a.map, key);
+  if (!own) return;
+  const bool leaves = lane == 63 || next != key;  // the token's last row (lane 63 owns nothing)
+  const uint64_t ends = __ballot(mine && ((behind & (kRun - 1)) == kRun - 1 || leaves));
+  const uint64_t whole = __ballot(mine && behind < kRun && leaves);  // at a run's end: the token's only run
+  const int c = V * (64 * slice + lane), left = a.H - c;
+  const G* g = static_cast<const G*>(a.g) + c;
+  FV<V> sum{};
+  const int first = __builtin_ctzll(own), last = 63 - __builtin_clzll(own);
+  for (int j = first; j <= last; j += kBatch) {
+    Raw<G, V> r[kBatch];
+    Raw<O, V> old[kBatch];
+#pragma unroll
+    for (int m = 0; m < kBatch; ++m) {
+      if (j + m > last) continue;
+      r[m] = load<V>(g + __builtin_amdgcn_readlane(row, j + m) * a.ldg, left);
+      if (a.accumulate && (whole >> (j + m) & 1))
+        old[m] = load<V>(static_cast<const O*>(a.grad) + (int64_t)__builtin_amdgcn_readlane(token, j + m) * a.H + c, left);
+    }
+#pragma unroll
+    for (int m = 0; m < kBatch; ++m) {
+      if (j + m > last) continue;
+      const FV<V> f = widen(r[m]);
+#pragma unroll
+      for (int e = 0; e < V; ++e) sum.v[e] += f.v[e];
+      if (!(ends >> (j + m) & 1)) continue;
+      if (whole >> (j + m) & 1) {
+        O* p = static_cast<O*>(a.grad) + (int64_t)__builtin_amdgcn_readlane(token, j + m) * a.H + c;
+        grad_row(a, p, old[m], sum, left);
+      } else {
+        const int b = __builtin_amdgcn_readlane(behind, j + m);
+        const int h = __builtin_amdgcn_readlane(head, j + m) + p0 - kRun;
+        store(a.part + part_of(h, b < kRun) * a.H + c, sum, left);
+      }
+      sum = FV<V>{};
+    }
+  }
+}
+
 template <class G, class O>
 __global__ __launch_bounds__(256) void embed_grad(EmbedGradArgs a) {
-  const int64_t items = (int64_t)a.T * a.slices;
+  const int64_t items = (int64_t)((a.T + a.window - 1) / a.window) * a.slices;
   for (int64_t w = (int64_t)blockIdx.x * 4 + threadIdx.x / 64; w < items; w += (int64_t)gridDim.x * 4) {
     const int i = __builtin_amdgcn_readfirstlane((int)(w / a.slices));
-    embed_item<G, O>(a, i, (int)(w - (int64_t)i * a.slices));
+    embed_window<G, O>(a, i * a.window, (int)(w - (int64_t)i * a.slices));
   }
 }
 
@@ -932,18 +1005,18 @@ __global__ __launch_bounds__(256) void embed_grad_join(EmbedGradArgs a) {
   const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
   const int32_t* k = a.keys;
   const int p = blockIdx.x * kRun + lane;
-  const int key = lane < kRun && p < a.T ? k[p] : a.V;
+  const int key = lane < kRun && p < a.T ? k[p] : a.map.none;
   const int before = lane < kRun && p > 0 && p < a.T ? k[p - 1] : -1;
   const int behind = lane < kRun && p + kRun < a.T ? k[p + kRun] : -1;
-  const uint64_t at = __ballot(key < a.V && behind == key && before != key);
+  const uint64_t at = __ballot(key != a.map.none && behind == key && before != key);
   if (!at) return;  // the same for all waves
   const int s = blockIdx.x * kRun + __builtin_ctzll(at);
-  const int token = __builtin_amdgcn_readlane(key, __builtin_ctzll(at));
+  const int same = __builtin_amdgcn_readlane(key, __builtin_ctzll(at)), token = token_of(a.map, same);
   // runs, 64 starts at a time
   int runs = 0;
   for (;;) {
     const int64_t q = s + (int64_t)kRun * (runs + lane);
-    const uint64_t other = __ballot(q >= a.T || k[q] != token);
+    const uint64_t other = __ballot(q >= a.T || k[q] != same);
     runs += other ? __builtin_ctzll(other) : 64;
     if (other) break;
   }

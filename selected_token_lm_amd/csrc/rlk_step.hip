@@ -258,21 +258,23 @@ inline rlk_status check_embed(const void* ids, int32_t id_bytes, int64_t T, int6
 }
 
 template <class E, class O>
-rlk_status launch_embed(const EmbedArgs& a, hipStream_t st) {
-  // a wave a row, four vectors in flight each, where the rows fill the card;
-  // else a block a row
-  if (a.T > 2048 || a.H <= 512)
-    RLK_LAUNCH_FN("embed_rows", (embed_rows<E, O, 64>), dim3(blocks_for(ceil_div(a.T, 4))), dim3(256), st, a);
-  else
-    RLK_LAUNCH_FN("embed_rows", (embed_rows<E, O, 256>), dim3(blocks_for(a.T)), dim3(256), st, a);
+rlk_status launch_embed(EmbedArgs a, hipStream_t st) {
+  a.slices = (int)ceil_div(a.H, 64 * kRowVecs * width_of<E, O>());
+  RLK_LAUNCH_FN("embed_rows", (embed_rows<E, O>), dim3(blocks_for(ceil_div((int64_t)a.T * a.slices, 4))), dim3(256), st,
+                a);
   return RLK_OK;
 }
 
 template <class G, class O>
-rlk_status launch_embed_grad(const EmbedGradArgs& a, hipStream_t st) {
+rlk_status launch_embed_grad(EmbedGradArgs a, hipStream_t st) {
   if (a.T == 0) return RLK_OK;
-  RLK_LAUNCH_FN("embed_grad", (embed_grad<G, O>), dim3(blocks_for(ceil_div((int64_t)a.T * a.slices, 4))), dim3(256),
-                st, a);
+  a.slices = (int)ceil_div(a.H, 64 * grad_width<O>());
+  // windows of up to 16 positions while they leave 32 waves to a unit (16384
+  // rows of H = 2048, bf16: 20 us with windows of 16, 32 with windows of 1)
+  a.window = 1;
+  while (a.window < kRun && (int64_t)a.T * a.slices > 8192 * a.window) a.window *= 2;
+  RLK_LAUNCH_FN("embed_grad", (embed_grad<G, O>),
+                dim3(blocks_for(ceil_div(ceil_div(a.T, a.window) * a.slices, 4))), dim3(256), st, a);
   if (a.T > kRun)
     RLK_LAUNCH_FN("embed_grad_join", (embed_grad_join<O>),
                   dim3((unsigned)ceil_div(a.T, kRun), (unsigned)ceil_div(a.H, 256)), dim3(256), st, a);
@@ -281,7 +283,7 @@ rlk_status launch_embed_grad(const EmbedGradArgs& a, hipStream_t st) {
 
 // Sorts the tokens by (id, t) and zeroes zero.p on the way.
 rlk_status sort_tokens(const IdsArg& ids, int64_t T, int64_t V, const ZeroArgs& zero, const EmbedWs& L, void* ws,
-                       const int32_t** keys, const int32_t** perm, hipStream_t st) {
+                       const int32_t** keys, const int32_t** perm, KeyMap* map, hipStream_t st) {
   char* base = static_cast<char*>(ws);
   int32_t* k[2];
   int32_t* p[2];
@@ -291,32 +293,39 @@ rlk_status sort_tokens(const IdsArg& ids, int64_t T, int64_t V, const ZeroArgs& 
   }
   *keys = k[0];
   *perm = p[0];
+  map->V = (int)V;
   // blocks that zero: 4 KB each, which is faster (6.7 TB/s) than fewer blocks
   // that stride (4.3 to 5.4)
   const int64_t zero_blocks = zero.p ? std::min<int64_t>(kRowBlocks, ceil_div(zero.bytes, 4096)) : 0;
   if (T <= kRankRows) {
+    map->low = kBucketBits;
+    map->high = std::max(0, key_bits(V - 1) - kBucketBits);
+    map->none = 1 << (map->low + map->high);
     RankArgs a{};
     a.ids = ids;
+    a.map = *map;
     a.keys = k[0];
     a.perm = p[0];
     a.T = (int)T;
-    a.V = (int)V;
     a.zero = zero;
     const bool few = T <= 4096;
     a.blocks = (int)ceil_div(T, few ? 16 : 64);
     const int64_t zeroing = few ? zero_blocks : ceil_div(zero_blocks, 4);
     if (a.blocks + zeroing == 0) return RLK_OK;
     if (few)
-      RLK_LAUNCH_FN("embed_rank", (embed_rank<16, 4096>), dim3((unsigned)(a.blocks + zeroing)), dim3(256), st, a);
+      RLK_LAUNCH_FN("embed_rank", (embed_rank<16>), dim3((unsigned)(a.blocks + zeroing)), dim3(256), st, a);
     else
-      RLK_LAUNCH_FN("embed_rank", (embed_rank<64, kRankRows>), dim3((unsigned)(a.blocks + zeroing)), dim3(1024), st, a);
+      RLK_LAUNCH_FN("embed_rank", (embed_rank<64>), dim3((unsigned)(a.blocks + zeroing)), dim3(1024), st, a);
     return RLK_OK;
   }
   const int bits = (int)ceil_div(key_bits(V), L.passes);
+  map->low = 24;  // keys are tokens
+  map->high = 0;
+  map->none = (int)V;
   RadixArgs a{};
   a.ids = ids;
+  a.map = *map;
   a.T = (int)T;
-  a.V = (int)V;
   a.tiles = (int)L.tiles;
   a.hist = reinterpret_cast<int32_t*>(base + L.hist);
   a.total = reinterpret_cast<int32_t*>(base + L.total_);
@@ -525,17 +534,15 @@ rlk_status rlk_embed_bwd(const void* ids, int32_t id_bytes, const void* g, int32
   hipStream_t st = static_cast<hipStream_t>(stream);
   EmbedGradArgs a{};
   const ZeroArgs zero{accumulate ? nullptr : static_cast<char*>(grad_E), (int64_t)size_of(grad_dtype) * V * H};
-  RLK_TRY(sort_tokens(IdsArg{ids, ignore_index, id_bytes == 8}, T, V, zero, L, ws, &a.keys, &a.perm, st));
+  RLK_TRY(sort_tokens(IdsArg{ids, ignore_index, id_bytes == 8}, T, V, zero, L, ws, &a.keys, &a.perm, &a.map, st));
   a.g = g;
   a.ldg = ldg;
   a.grad = grad_E;
   a.part = T > 0 ? reinterpret_cast<float*>(static_cast<char*>(ws) + L.part) : nullptr;
   a.T = (int)T;
   a.H = (int)H;
-  a.V = (int)V;
   a.scale = scale;
   a.accumulate = accumulate;
-  a.slices = (int)ceil_div(H, 64 * (g_dtype == RLK_DT_F32 && grad_dtype == RLK_DT_F32 ? 4 : 8));
   const bool gf = g_dtype == RLK_DT_F32, of = grad_dtype == RLK_DT_F32;
   RLK_TRY(gf ? (of ? launch_embed_grad<float, float>(a, st) : launch_embed_grad<float, uint16_t>(a, st))
              : (of ? launch_embed_grad<uint16_t, float>(a, st) : launch_embed_grad<uint16_t, uint16_t>(a, st)));
