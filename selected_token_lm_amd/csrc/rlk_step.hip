@@ -259,9 +259,11 @@ inline rlk_status check_embed(const void* ids, int32_t id_bytes, int64_t T, int6
 
 template <class E, class O>
 rlk_status launch_embed(EmbedArgs a, hipStream_t st) {
-  a.slices = (int)ceil_div(a.H, 64 * kRowVecs * width_of<E, O>());
-  RLK_LAUNCH_FN("embed_rows", (embed_rows<E, O>), dim3(blocks_for(ceil_div((int64_t)a.T * a.slices, 4))), dim3(256), st,
-                a);
+  const int64_t vectors = ceil_div(a.H, 64 * width_of<E, O>());
+  const int vecs = a.T * vectors <= 8192 ? 1 : 4;
+  a.slices = (int)ceil_div(vectors, vecs);
+  RLK_LAUNCH_FN("embed_rows", (vecs == 1 ? embed_rows<E, O, 1> : embed_rows<E, O, 4>),
+                dim3(blocks_for(ceil_div((int64_t)a.T * a.slices, 4))), dim3(256), st, a);
   return RLK_OK;
 }
 
@@ -308,7 +310,8 @@ rlk_status sort_tokens(const IdsArg& ids, int64_t T, int64_t V, const ZeroArgs& 
     a.perm = p[0];
     a.T = (int)T;
     a.zero = zero;
-    const bool few = T <= 4096;
+    // small blocks for few tokens, and beside blocks that zero
+    const bool few = T <= (zero.p ? 4096 : 1024);
     a.blocks = (int)ceil_div(T, few ? 16 : 64);
     const int64_t zeroing = few ? zero_blocks : ceil_div(zero_blocks, 4);
     if (a.blocks + zeroing == 0) return RLK_OK;

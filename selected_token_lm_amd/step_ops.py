@@ -22,11 +22,12 @@ are bfloat16 or float32, in any mixture; rows may be strided.
 from __future__ import annotations
 
 import ctypes
+from array import array
 
 import torch
 from torch.autograd.function import once_differentiable
 
-from . import IGNORE_INDEX, _c_void_p, _check, _given_workspace, _i32, _i64, _ptr, _rows, _size, _stream, lib
+from . import IGNORE_INDEX, _c_void_p, _check, _given_workspace, _i32, _i64, _ptr, _rows, _size, lib
 from .vocab_ops import _on
 
 SOP_NORM_BWD, SOP_EMBED_BWD, SOP_GRADS = 0, 1, 2
@@ -65,6 +66,11 @@ def _ws(ws, op, T, H, V, device):
     return torch.empty(n, dtype=torch.uint8, device=device), n
 
 
+def _stream(device):
+    """The device's current stream, without the object around it (2.6 us)."""
+    return torch._C._cuda_getCurrentRawStream(device.index)
+
+
 def _dtype(name, dtype):
     code = _DTYPES.get(dtype)
     if code is None:
@@ -89,9 +95,10 @@ def _matrix(name, t, shape=None, device=None):
 
 def _vectors(H, device, **named):
     """(the tensors, contiguous, and the code of the dtype they share)."""
-    code = None
+    code, out = None, []
     for name, t in named.items():
         if t is None:
+            out.append(None)
             continue
         if t.dim() != 1 or t.shape[0] != H:
             raise ValueError(f"{name} must be [H] = [{H}], got {list(t.shape)}")
@@ -99,10 +106,11 @@ def _vectors(H, device, **named):
         if code is not None and c != code:
             raise TypeError(f"{' and '.join(named)} must have one dtype")
         code = c
+        out.append(t if t.is_contiguous() else t.contiguous())
     for name, t in named.items():
-        if t is not None and (not t.is_cuda or t.device != device):
+        if t is not None and (t.device != device or not t.is_cuda):
             raise ValueError(f"{name} must be on {device}")
-    return [t if t is None else t.contiguous() for t in named.values()], code or 0
+    return out, code or 0
 
 
 def _eps(eps):
@@ -122,16 +130,16 @@ def _norm_fwd(center, x, weight, bias, eps, out_dtype, stats):
     out_dtype = x.dtype if out_dtype is None else out_dtype
     yd = _dtype("out_dtype", out_dtype)
     with _on(dev):
-        y = torch.empty((T, H), dtype=out_dtype, device=dev)
+        y = torch.empty_like(x) if out_dtype is x.dtype and x.is_contiguous() else x.new_empty((T, H), dtype=out_dtype)
         mean = torch.empty(T, dtype=torch.float32, device=dev) if stats and center else None
         rstd = torch.empty(T, dtype=torch.float32, device=dev) if stats else None
         if center:
             _check(lib().rlk_layer_norm_fwd(_ptr(x), xd, ld, _ptr(weight), _ptr(bias), wd, T, H, eps, _ptr(y), yd,
-                                            _ptr(mean), _ptr(rstd), _stream()),
+                                            _ptr(mean), _ptr(rstd), _stream(dev)),
                    "rlk_layer_norm_fwd")
         else:
             _check(lib().rlk_rms_norm_fwd(_ptr(x), xd, ld, _ptr(weight), wd, T, H, eps, _ptr(y), yd, _ptr(rstd),
-                                          _stream()),
+                                          _stream(dev)),
                    "rlk_rms_norm_fwd")
     return y, mean, rstd
 
@@ -157,11 +165,11 @@ def _norm_bwd(center, x, weight, mean, rstd, g, need_x, need_w, need_b, grad_dty
         if center:
             _check(lib().rlk_layer_norm_bwd(_ptr(x), xd, ldx, _ptr(weight), wd, _ptr(mean), _ptr(rstd), _ptr(g), gd,
                                             ldg, T, H, _ptr(grad_x), _ptr(grad_w), _ptr(grad_b), code, _ptr(ws), n,
-                                            _stream()),
+                                            _stream(dev)),
                    "rlk_layer_norm_bwd")
         else:
             _check(lib().rlk_rms_norm_bwd(_ptr(x), xd, ldx, _ptr(weight), wd, _ptr(rstd), _ptr(g), gd, ldg, T, H,
-                                          _ptr(grad_x), _ptr(grad_w), code, _ptr(ws), n, _stream()),
+                                          _ptr(grad_x), _ptr(grad_w), code, _ptr(ws), n, _stream(dev)),
                    "rlk_rms_norm_bwd")
     return grad_x, grad_w, grad_b
 
@@ -274,10 +282,11 @@ def embed_fwd(ids, E, scale: float = 1.0, ignore_index: int = IGNORE_INDEX, out_
     out_dtype = E.dtype if out_dtype is None else out_dtype
     od = _dtype("out_dtype", out_dtype)
     scale, ignore_index = _scale(scale), _ignore(ignore_index)
-    with _on(E.device):
-        out = torch.empty((T, H), dtype=out_dtype, device=E.device)
+    dev = E.device
+    with _on(dev):
+        out = torch.empty((T, H), dtype=out_dtype, device=dev)
         _check(lib().rlk_embed_fwd(_ptr(ids), width, _ptr(E), ed, T, H, V, ignore_index, scale, _ptr(out), od,
-                                   _stream()),
+                                   _stream(dev)),
                "rlk_embed_fwd")
     return out
 
@@ -308,7 +317,7 @@ def embed_bwd(ids, g, V: int, scale: float = 1.0, ignore_index: int = IGNORE_IND
         if not add:
             grad_E = torch.empty((V, H), dtype=grad_E_dtype, device=dev)
         _check(lib().rlk_embed_bwd(_ptr(ids), width, _ptr(g), gd, ldg, T, H, V, ignore_index, scale, _ptr(grad_E), od,
-                                   int(add), _ptr(ws), n, _stream()),
+                                   int(add), _ptr(ws), n, _stream(dev)),
                "rlk_embed_bwd")
     if add:
         _written([grad_E])
@@ -338,26 +347,35 @@ def embed(ids, E, scale: float = 1.0, ignore_index: int = IGNORE_INDEX, out_dtyp
 
 def _tensors(what, tensors):
     """The device and the host arrays of a list of dense tensors: pointers,
-    sizes, dtypes.  A sum of squares and a scaling go by memory, so any dense
-    layout serves."""
-    n = len(tensors)
-    ptrs, sizes, codes = (ctypes.c_void_p * n)(), (ctypes.c_int64 * n)(), (ctypes.c_int32 * n)()
-    device = tensors[0].device if n else None
-    for i, t in enumerate(tensors):
-        code = _DTYPES.get(t.dtype)
-        if code is None:
-            raise TypeError(f"{what}[{i}] must be float32 or bfloat16, got {t.dtype}")
-        if not t.is_contiguous() and not torch.ops.aten.is_non_overlapping_and_dense(t):
-            raise ValueError(f"{what}[{i}] must be dense in memory, got strides {list(t.stride())}")
-        if not t.is_cuda or t.device != device:
-            raise ValueError(f"all of {what} must be on one GPU")
-        ptrs[i], sizes[i], codes[i] = t.data_ptr(), t.numel(), code
-    return device, ptrs, sizes, codes
+    sizes, dtypes; and whether all are contiguous.  A sum of squares and a
+    scaling go by memory, so any dense layout serves."""
+    device = tensors[0].device
+    codes = array("i", [_DTYPES.get(t.dtype, -1) for t in tensors])
+    if -1 in codes:
+        i = codes.index(-1)
+        raise TypeError(f"{what}[{i}] must be float32 or bfloat16, got {tensors[i].dtype}")
+    if not tensors[0].is_cuda or any([t.device != device for t in tensors]):
+        raise ValueError(f"all of {what} must be on one GPU")
+    contiguous = [t.is_contiguous() for t in tensors]
+    plain = all(contiguous)
+    for i, c in enumerate(() if plain else contiguous):
+        if not c and not torch.ops.aten.is_non_overlapping_and_dense(tensors[i]):
+            raise ValueError(f"{what}[{i}] must be dense in memory, got strides {list(tensors[i].stride())}")
+    ptrs, sizes = array("Q", [t.data_ptr() for t in tensors]), array("q", [t.numel() for t in tensors])
+    return device, ptrs, sizes, codes, plain
+
+
+def _at(values):
+    """The address of an array's values (the library reads them before it returns)."""
+    return values.buffer_info()[0]
 
 
 def _written(tensors):
     """Tells autograd that these tensors were changed in place."""
-    torch.autograd.graph.increment_version([t for t in tensors if not t.is_inference()])
+    try:
+        torch.autograd.graph.increment_version(tensors)
+    except RuntimeError:  # inference tensors have no version
+        torch.autograd.graph.increment_version([t for t in tensors if not t.is_inference()])
 
 
 def _list(tensors):
@@ -370,12 +388,13 @@ def grad_norm(grads, ws=None):
     grads = _list(grads)
     if not grads:
         raise ValueError("grads is empty")
-    dev, ptrs, sizes, codes = _tensors("grads", grads)
+    dev, ptrs, sizes, codes, _ = _tensors("grads", grads)
     n = len(grads)
     with _on(dev):
         ws, size = _ws(ws, SOP_GRADS, n, 0, 0, dev)
         norm = torch.empty((), dtype=torch.float32, device=dev)
-        _check(lib().rlk_grad_norm(ptrs, sizes, codes, n, _ptr(norm), _ptr(ws), size, _stream()), "rlk_grad_norm")
+        _check(lib().rlk_grad_norm(_at(ptrs), _at(sizes), _at(codes), n, _ptr(norm), _ptr(ws), size, _stream(dev)),
+               "rlk_grad_norm")
     return norm
 
 
@@ -391,7 +410,7 @@ def clip_grads(grads, max_norm: float, out=None, ws=None):
     max_norm = float(max_norm)
     if not max_norm >= 0.0:
         raise ValueError(f"max_norm must not be negative, got {max_norm}")
-    dev, ptrs, sizes, codes = _tensors("grads", grads)
+    dev, ptrs, sizes, codes, plain = _tensors("grads", grads)
     n = len(grads)
     if out is None:
         out, optrs, ocodes = grads, ptrs, codes
@@ -399,19 +418,20 @@ def clip_grads(grads, max_norm: float, out=None, ws=None):
         out = _list(out)
         if len(out) != n:
             raise ValueError(f"out must have {n} tensors, got {len(out)}")
-        odev, optrs, _, ocodes = _tensors("out", out)
+        odev, optrs, _, ocodes, oplain = _tensors("out", out)
         if odev != dev:
             raise ValueError(f"out must be on {dev}")
         for i, (t, o) in enumerate(zip(grads, out)):
-            if o.shape != t.shape or (o.stride() != t.stride() and not (o.is_contiguous() and t.is_contiguous())):
+            if o.shape != t.shape or (not (plain and oplain) and not (o.is_contiguous() and t.is_contiguous())
+                                      and o.stride() != t.stride()):
                 raise ValueError(f"out[{i}] must have the shape and layout of grads[{i}]")
-    if torch.is_grad_enabled() and any(t.requires_grad for t in out):
+    if torch.is_grad_enabled() and any([t.requires_grad for t in out]):
         raise ValueError("gradients to be scaled require a gradient themselves: pass p.grad, not p")
     with _on(dev):
         ws, size = _ws(ws, SOP_GRADS, n, 0, 0, dev)
         norm = torch.empty((), dtype=torch.float32, device=dev)
-        _check(lib().rlk_clip_grads(ptrs, sizes, codes, n, max_norm, optrs, ocodes, _ptr(norm),
-                                    _ptr(ws), size, _stream()),
+        _check(lib().rlk_clip_grads(_at(ptrs), _at(sizes), _at(codes), n, max_norm, _at(optrs), _at(ocodes),
+                                    _ptr(norm), _ptr(ws), size, _stream(dev)),
                "rlk_clip_grads")
     _written(out)
     return norm, out
