@@ -310,6 +310,8 @@ def embed_bwd(ids, g, V: int, scale: float = 1.0, ignore_index: int = IGNORE_IND
         od = _table("grad_E", grad_E)
         if grad_E.shape != (V, H) or not grad_E.is_contiguous() or grad_E.device != dev:
             raise ValueError(f"grad_E must be a contiguous [{V}, {H}] tensor on {dev}, got {list(grad_E.shape)}")
+        if grad_E.requires_grad and torch.is_grad_enabled():
+            raise ValueError("grad_E requires a gradient itself: pass E.grad, not E")
     else:
         od = _dtype("grad_E_dtype", grad_E_dtype)
     with _on(dev):
@@ -346,23 +348,30 @@ def embed(ids, E, scale: float = 1.0, ignore_index: int = IGNORE_INDEX, out_dtyp
 
 
 def _tensors(what, tensors):
-    """The device and the host arrays of a list of dense tensors: pointers,
-    sizes, dtypes; and whether all are contiguous.  A sum of squares and a
-    scaling go by memory, so any dense layout serves."""
-    device = tensors[0].device
-    codes = array("i", [_DTYPES.get(t.dtype, -1) for t in tensors])
-    if -1 in codes:
-        i = codes.index(-1)
-        raise TypeError(f"{what}[{i}] must be float32 or bfloat16, got {tensors[i].dtype}")
-    if not tensors[0].is_cuda or any([t.device != device for t in tensors]):
+    """The device and the host arrays of a list of dense tensors: pointers and
+    dtypes; and whether all are contiguous.  A sum of squares and a scaling go
+    by memory, so any dense layout serves."""
+    n, device = len(tensors), tensors[0].device
+    dtypes = [t.dtype for t in tensors]
+    if dtypes.count(dtypes[0]) == n and dtypes[0] in _DTYPES:
+        codes = array("i", [_DTYPES[dtypes[0]]]) * n
+    else:
+        codes = array("i", [_DTYPES.get(d, -1) for d in dtypes])
+        if -1 in codes:
+            i = codes.index(-1)
+            raise TypeError(f"{what}[{i}] must be float32 or bfloat16, got {dtypes[i]}")
+    if not tensors[0].is_cuda or [t.get_device() for t in tensors].count(device.index) != n:
         raise ValueError(f"all of {what} must be on one GPU")
     contiguous = [t.is_contiguous() for t in tensors]
     plain = all(contiguous)
     for i, c in enumerate(() if plain else contiguous):
         if not c and not torch.ops.aten.is_non_overlapping_and_dense(tensors[i]):
             raise ValueError(f"{what}[{i}] must be dense in memory, got strides {list(tensors[i].stride())}")
-    ptrs, sizes = array("Q", [t.data_ptr() for t in tensors]), array("q", [t.numel() for t in tensors])
-    return device, ptrs, sizes, codes, plain
+    return device, array("Q", [t.data_ptr() for t in tensors]), codes, plain
+
+
+def _sizes(tensors):
+    return array("q", [t.numel() for t in tensors])
 
 
 def _at(values):
@@ -388,8 +397,8 @@ def grad_norm(grads, ws=None):
     grads = _list(grads)
     if not grads:
         raise ValueError("grads is empty")
-    dev, ptrs, sizes, codes, _ = _tensors("grads", grads)
-    n = len(grads)
+    dev, ptrs, codes, _ = _tensors("grads", grads)
+    n, sizes = len(grads), _sizes(grads)
     with _on(dev):
         ws, size = _ws(ws, SOP_GRADS, n, 0, 0, dev)
         norm = torch.empty((), dtype=torch.float32, device=dev)
@@ -410,20 +419,20 @@ def clip_grads(grads, max_norm: float, out=None, ws=None):
     max_norm = float(max_norm)
     if not max_norm >= 0.0:
         raise ValueError(f"max_norm must not be negative, got {max_norm}")
-    dev, ptrs, sizes, codes, plain = _tensors("grads", grads)
-    n = len(grads)
+    dev, ptrs, codes, plain = _tensors("grads", grads)
+    n, sizes = len(grads), _sizes(grads)
     if out is None:
         out, optrs, ocodes = grads, ptrs, codes
     else:
         out = _list(out)
         if len(out) != n:
             raise ValueError(f"out must have {n} tensors, got {len(out)}")
-        odev, optrs, _, ocodes, oplain = _tensors("out", out)
+        odev, optrs, ocodes, oplain = _tensors("out", out)
         if odev != dev:
             raise ValueError(f"out must be on {dev}")
-        for i, (t, o) in enumerate(zip(grads, out)):
-            if o.shape != t.shape or (not (plain and oplain) and not (o.is_contiguous() and t.is_contiguous())
-                                      and o.stride() != t.stride()):
+        same = [t.shape for t in grads] == [o.shape for o in out]
+        for i, (t, o) in enumerate(() if same and plain and oplain else zip(grads, out)):
+            if o.shape != t.shape or (o.stride() != t.stride() and not (o.is_contiguous() and t.is_contiguous())):
                 raise ValueError(f"out[{i}] must have the shape and layout of grads[{i}]")
     if torch.is_grad_enabled() and any([t.requires_grad for t in out]):
         raise ValueError("gradients to be scaled require a gradient themselves: pass p.grad, not p")

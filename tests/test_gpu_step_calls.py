@@ -121,6 +121,8 @@ def test_in_place_results_are_seen_by_autograd():
         y.backward()
     with pytest.raises(ValueError, match="p.grad"):
         rlk.clip_grads([t], 1.0)
+    with pytest.raises(ValueError, match="E.grad"):
+        rlk.embed_bwd(torch.tensor([1], device=DEV), torch.ones((1, 10), device=DEV), 1, grad_E=t.view(1, 10))
     with torch.inference_mode():
         n, out = rlk.clip_grads([torch.ones(16, device=DEV)], 2.0)
         assert n == 4 and (out[0] == 0.5).all()

@@ -135,6 +135,63 @@ def test_a_tokens_row_depends_on_its_own_rows(H):
         assert same(rlk.embed_bwd(ids_dev(more, torch.int32), gm, V, 0.5), got), pad
 
 
+@pytest.mark.parametrize("grad", ["bf16", "f32"])
+@pytest.mark.parametrize("H", [5, 300, 1025])
+@pytest.mark.parametrize("sizes", [
+    [1] * 40, [2, 15, 1, 16, 17, 1], [31, 32, 33, 1, 47, 48, 49], [63, 64, 65], [16] * 30, [17] * 30,
+    [1, 255, 256, 257, 1, 3], [1023, 1024, 1025, 2], [4097, 1, 16, 5000, 15], [16, 9000, 17, 8000],
+], ids=lambda s: "-".join(map(str, s[:4])))
+def test_tokens_of_every_number_of_rows(sizes, H, grad):
+    """Around runs, their batches and their joins; sums of small whole numbers,
+    exact in fp32."""
+    r = rng(10, len(sizes), H, sizes[0])
+    names = r.permutation(3 * len(sizes))[:len(sizes)]
+    ids = r.permutation(np.concatenate([np.full(n, v) for n, v in zip(sizes, names)] + [np.full(11, -100)]))
+    V = 3 * len(sizes)
+    g = r.integers(-2, 3, (len(ids), H)).astype(np.float32)
+    gd, gn = dev(g, BF16)
+    want = torch.from_numpy(O.embed_backward(ids, gn, V, 0.5)).to(DTYPES[grad])
+    assert torch.equal(rlk.embed_bwd(ids_dev(ids), gd, V, 0.5, grad_E_dtype=DTYPES[grad]).cpu(), want)
+    base = torch.ones((V, H), dtype=DTYPES[grad], device=DEV)
+    want = torch.from_numpy(O.embed_backward(ids, gn, V, 0.5) + 1).to(DTYPES[grad])
+    assert torch.equal(rlk.embed_bwd(ids_dev(ids), gd, V, 0.5, grad_E=base).cpu(), want)
+
+
+@pytest.mark.parametrize("T", [3, 40, 2000])
+@pytest.mark.parametrize("H", [8191, 16384, 65535, 65536])
+def test_wide_rows(H, T):
+    V = 20
+    ids = tokens(T, V, 11, mask=0.1)
+    r = rng(12, H)
+    Ed, En = dev(r.normal(size=(V, H)), BF16)
+    assert same(rlk.embed(ids_dev(np.abs(ids) % V), Ed), Ed[ids_dev(np.abs(ids) % V)])
+    g = r.integers(-3, 4, (T, 64)).astype(np.float32)
+    gd = dev(g, BF16)[0].repeat(1, -(-H // 64))[:, :H]
+    want = torch.from_numpy(O.embed_backward(ids, g, V, 1.0)).float().repeat(1, -(-H // 64))[:, :H]
+    assert torch.equal(rlk.embed_bwd(ids_dev(ids), gd, V).cpu(), want)
+
+
+@pytest.mark.parametrize("V", [1, 2, 1023, 1024, 1025, 2048, 131072, 131073, 8_000_000])
+def test_vocabularies_around_powers_of_two(V):
+    """Every token once (or the first and last 300, a thousand random ones), by
+    both sorts."""
+    r = rng(13, V)
+    ids = r.permutation(np.unique(np.concatenate([np.arange(min(V, 300)), np.arange(max(0, V - 300), V),
+                                                  r.integers(0, V, 1000)])))
+    g = r.integers(-3, 4, (len(ids), 8)).astype(np.float32)
+    gd = dev(g)[0]
+    want = torch.zeros((V, 8))
+    want[torch.from_numpy(ids)] = torch.from_numpy(g)
+    got = rlk.embed_bwd(ids_dev(ids), gd, V)
+    assert torch.equal(got.cpu(), want)
+    more = 17000 - len(ids)
+    nan = gd.new_full((more, 8), float("nan"))
+    got2 = rlk.embed_bwd(ids_dev(np.concatenate([ids, np.full(more, -100)])), torch.cat([gd, nan]), V)
+    assert same(got2, got)
+    E = want.to(DEV)
+    assert torch.equal(rlk.embed(ids_dev(ids), E), gd)
+
+
 def test_strided_and_broadcast_gradients():
     V, T, H = 30, 400, 100
     ids = tokens(T, V, 8)
