@@ -132,36 +132,44 @@ __device__ __forceinline__ FV<V> load_any(const void* p, bool f32, int64_t at, i
   return widen(load<V>(static_cast<const uint16_t*>(p) + at, n));
 }
 
-// Sum over a wave, in every lane: pairs 1, 2, then mirrored quads and octets
-// (lanes 4 and 8 apart hold sums of four and eight), rows of 16, halves.
+// Sum over groups of R lanes (16, 32 or 64) of a wave, in every lane: pairs 1,
+// 2, then mirrored quads and octets (lanes 4 and 8 apart hold sums of four and
+// eight), rows of 16, halves.  Groups may sit out as a whole.
 template <int kCtrl>
 __device__ __forceinline__ float dpp(float v) {
   return __uint_as_float(__builtin_amdgcn_update_dpp(0u, __float_as_uint(v), kCtrl, 0xf, 0xf, true));
 }
-__device__ __forceinline__ float wave_sum(float v) {
+template <int R>
+__device__ __forceinline__ float lane_sum(float v) {
   v += dpp<0xb1>(v);   // quad_perm [1, 0, 3, 2]
   v += dpp<0x4e>(v);   // quad_perm [2, 3, 0, 1]
   v += dpp<0x141>(v);  // row_half_mirror
   v += dpp<0x140>(v);  // row_mirror
-  const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-  v = __uint_as_float(r[0]) + __uint_as_float(r[1]);
-  float lo, hi;
-  lane_halves(v, lo, hi);
-  return lo + hi;
+  if constexpr (R >= 32) {
+    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+  }
+  if constexpr (R >= 64) {
+    float lo, hi;
+    lane_halves(v, lo, hi);
+    v = lo + hi;
+  }
+  return v;
 }
 
 // --- norms -------------------------------------------------------------------
-// R threads hold a row in registers, N vectors of V each: vector i * R + lane.
-// The split goes by H and the types alone, so a row's sums have one order.
+// Bound by HBM: a few operations an element.  R threads hold a row in registers,
+// N vectors of V each: vector i * R + lane.  The split goes by H and the types
+// alone, so a row's sums have one order.
 template <int R>
 struct RowSum {
-  static constexpr int kWaves = R / 64;
-  // red: kWaves floats for each of the kVals sums; consecutive calls take
-  // different ones (one barrier a call).
+  static constexpr int kWaves = R > 64 ? R / 64 : 1;
+  // red (R > 64): kWaves floats for each of the kVals sums; consecutive calls
+  // take different ones (one barrier a call).
   template <int kVals>
   static __device__ __forceinline__ void run(float (&v)[kVals], float* red) {
 #pragma unroll
-    for (int k = 0; k < kVals; ++k) v[k] = wave_sum(v[k]);
+    for (int k = 0; k < kVals; ++k) v[k] = lane_sum<R < 64 ? R : 64>(v[k]);
     if constexpr (R > 64) {
       const int wave = threadIdx.x / 64;
       if (threadIdx.x % 64 == 0) {
@@ -198,12 +206,15 @@ struct NormFwdArgs {
 
 // y = (x - mean) rstd w + b (kCenter), or x rstd w.  The row is read once; the
 // variance is taken about the mean (a second sum over registers).  Weights are
-// loaded with the row, not after its sums (16384 x 2048: 45 -> 36 us).
+// loaded with the row, not after its sums (16384 x 2048, fp32 -> bf16: 48 -> 41
+// us, 4.9 TB/s; 4096 x 4096 bf16: 13 us, 5.0 TB/s; one row 2.3 us).  Narrow rows
+// share a wave (163840 rows of 128, bf16: 16 us, 100000 of 64: 9,
+// where a wave a row takes 30).
 template <class X, class Y, bool kCenter, int R, int E>
 __global__ __launch_bounds__(norm_block(R)) void norm_fwd(NormFwdArgs a) {
   constexpr int V = width_of<X, Y>(), N = E / V;
   constexpr int kRows = norm_rows(R);
-  constexpr int kWaves = R / 64;
+  constexpr int kWaves = RowSum<R>::kWaves;
   __shared__ float red[2 * kWaves];
   const int lane = threadIdx.x % R;
   const float fH = (float)a.H;
@@ -283,15 +294,18 @@ struct NormBwdArgs {
   int w_f32;
 };
 
-// A block takes rows b, b + P, ...: grad_x of each, and the block's sums for
-// the weight's and bias's gradients in registers.  The next row's loads are
-// issued before the current row's sums are exchanged.
+// A block takes rows b, b + P, ... (several at a time where they are narrow):
+// grad_x of each, and the block's sums for the weight's and bias's gradients in
+// registers, so that x and g are read once.  The next row's loads are issued
+// before the current row's sums are exchanged.  512 blocks: twice as many leave
+// twice the parts to fold, half as many do not hide the memory (16384 x 2048,
+// fp32 and bf16: 59 us, 5.7 TB/s; 4096 x 4096 bf16: 19 us, 5.3 TB/s).
 template <class X, class G, bool kCenter, bool kSums, int R, int E>
 __global__ __launch_bounds__(norm_block(R)) void norm_bwd(NormBwdArgs a) {
   constexpr int V = width_of<X, G>(), N = E / V;
   constexpr int kRows = norm_rows(R);
   constexpr int kVals = kCenter ? 2 : 1;
-  constexpr int kWaves = R / 64;
+  constexpr int kWaves = RowSum<R>::kWaves;
   __shared__ float red[2][kVals * kWaves];
   const int lane = threadIdx.x % R;
   const float fH = (float)a.H;
@@ -538,7 +552,8 @@ struct NormSumArgs {
 };
 
 // The blocks' sums folded: 32 columns a block, 32 groups of parts (p, p + 32,
-// ...), then these groups in order.
+// ...), then these groups in order.  Latency: 4 us for 512 parts of 4096, as
+// for 256.
 __global__ __launch_bounds__(256) void norm_grad_sum(NormSumArgs a) {
   __shared__ float4 lds[32][8];
   void* out = a.out[blockIdx.y];
@@ -590,7 +605,8 @@ struct EmbedArgs {
 
 // out[t] = scale E[id]: a wave for kRowVecs vectors a lane of a row, all loaded
 // before the first is stored.  Four, or one where the rows are so few that
-// all waves are there at once (48 rows of H = 2048: 3.6 -> 2.9 us).
+// all waves are there at once (48 rows of H = 2048: 3.6 -> 3.0 us).  Bound by
+// HBM's random rows: 16384 of H = 2048 20 us, 4.7 TB/s.
 template <class E, class O, int kRowVecs>
 __global__ __launch_bounds__(256) void embed_rows(EmbedArgs a) {
   constexpr int V = width_of<E, O>();
@@ -659,7 +675,8 @@ __device__ __forceinline__ void zero_share(const ZeroArgs& z, int64_t block, int
 // tokens: the buckets before, and the tokens before it in its own, which 16
 // threads count.  Up to 4096 tokens small blocks with little LDS leave the
 // units to the blocks that zero; beyond, fewer blocks read all ids.
-// (16384 tokens: 13 us, against 25 for counting against all others.)
+// Bound by LDS latency: 16384 tokens of text 13 us (25 for counting against all
+// others), of one token 60, which all add to one counter.
 constexpr int kRankRows = 16384, kBucketBits = 10, kBuckets = 1 << kBucketBits;
 
 struct RankArgs {
@@ -757,7 +774,9 @@ __global__ __launch_bounds__(16 * kTok) void embed_rank(RankArgs a) {
 }
 
 // More tokens: a radix sort by digits of up to nine bits, the lowest first,
-// three launches each; tiles of 4096 tokens, a wave's 1024 in order.
+// three launches each; tiles of 4096 tokens, a wave's 1024 in order.  Bound by
+// latency: 131072 tokens, two digits, 60 us in six launches (the rows after them
+// take 110).
 constexpr int kTile = 4096, kBins = 512;
 
 // The lanes of a wave whose digit is this lane's.
@@ -923,7 +942,8 @@ struct EmbedGradArgs {
   const void* g;
   int64_t ldg;
   void* grad;
-  float* part;  // [2 * runs][H], runs = ceil(T / kRun)
+  float* part;  // [2][runs][H]
+  int runs;     // ceil(T / kRun)
   KeyMap map;
   int T, H;
   float scale;
@@ -934,7 +954,9 @@ struct EmbedGradArgs {
 
 // The part of the run that starts at position i: a token's first run, or a
 // later one, can each start only once in kRun positions.
-__device__ __forceinline__ int64_t part_of(int i, bool first) { return 2 * (int64_t)(i / kRun) + first; }
+__device__ __forceinline__ float* part_of(const EmbedGradArgs& a, int i, bool first) {
+  return a.part + ((first ? a.runs : 0) + (int64_t)(i / kRun)) * a.H;
+}
 
 // grad = old + scale * sum, or scale * sum; stored non-temporally (16384 rows of
 // H = 2048 added to fp32 34 -> 30 us, else the same).
@@ -1016,13 +1038,15 @@ __device__ __forceinline__ void embed_window(const EmbedGradArgs& a, int p0, int
       } else {
         const int b = __builtin_amdgcn_readlane(behind, j + m);
         const int h = __builtin_amdgcn_readlane(head, j + m) + p0 - kRun;
-        store(a.part + part_of(h, b < kRun) * a.H + c, sum, left);
+        store(part_of(a, h, b < kRun) + c, sum, left);
       }
       sum = FV<V>{};
     }
   }
 }
 
+// Bound by HBM's random rows and their latency: 16384 tokens of H = 2048 (6200
+// distinct) added to fp32 38 us, 4.2 TB/s; 4096 of H = 4096 into bf16 19 us.
 template <class G, class O>
 __global__ __launch_bounds__(256) void embed_grad(EmbedGradArgs a) {
   const int64_t items = (int64_t)((a.T + a.window - 1) / a.window) * a.slices;
@@ -1032,57 +1056,75 @@ __global__ __launch_bounds__(256) void embed_grad(EmbedGradArgs a) {
   }
 }
 
-// Tokens of more than kRun rows: their runs' sums, in order.  A block for the
-// one such token whose first row can stand in kRun positions, 256 columns at a
-// time: four waves sum consecutive quarters, and these are summed in order.
+// Tokens of more than kRun rows: their runs' sums, in order.  A block looks for
+// the first rows of such tokens in 128 positions and takes each in turn, 256
+// columns at a time: eight waves sum consecutive eighths, eight parts in flight
+// each, and these are summed in order.  Bound by latency: 5 to 7 us where few
+// tokens have more than a few runs, 45 us for one token of 16384 rows.
 template <class O>
-__global__ __launch_bounds__(256) void embed_grad_join(EmbedGradArgs a) {
-  constexpr int V = 4;
-  __shared__ FV<V> lds[4][64];
+__global__ __launch_bounds__(512) void embed_grad_join(EmbedGradArgs a) {
+  constexpr int V = 4, kWaves = 8, kSpan = 128, kStarts = kSpan / kRun;
+  __shared__ FV<V> lds[kWaves][64];
+  __shared__ int32_t found[kStarts];
   const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
   const int32_t* k = a.keys;
-  const int p = blockIdx.x * kRun + lane;
-  const int key = lane < kRun && p < a.T ? k[p] : a.map.none;
-  const int before = lane < kRun && p > 0 && p < a.T ? k[p - 1] : -1;
-  const int behind = lane < kRun && p + kRun < a.T ? k[p + kRun] : -1;
-  const uint64_t at = __ballot(key != a.map.none && behind == key && before != key);
-  if (!at) return;  // the same for all waves
-  const int s = blockIdx.x * kRun + __builtin_ctzll(at);
-  const int same = __builtin_amdgcn_readlane(key, __builtin_ctzll(at)), token = token_of(a.map, same);
-  // runs, 64 starts at a time
-  int runs = 0;
-  for (;;) {
-    const int64_t q = s + (int64_t)kRun * (runs + lane);
-    const uint64_t other = __ballot(q >= a.T || k[q] != same);
-    runs += other ? __builtin_ctzll(other) : 64;
-    if (other) break;
+  if (threadIdx.x < kStarts) found[threadIdx.x] = -1;
+  __syncthreads();
+  if (threadIdx.x < kSpan) {
+    const int p = blockIdx.x * kSpan + threadIdx.x;
+    const int key = p < a.T ? k[p] : a.map.none;
+    const int before = p > 0 && p < a.T ? k[p - 1] : -1;
+    const int behind = p + kRun < a.T ? k[p + kRun] : -1;
+    // (one at most in kRun positions)
+    if (key != a.map.none && behind == key && before != key) found[threadIdx.x / kRun] = p;
   }
-  const int per = (runs + 3) / 4;
-  const int lo = min(wave * per, runs), hi = min(lo + per, runs);
-  for (int c0 = blockIdx.y * 64 * V; c0 < a.H; c0 += gridDim.y * 64 * V) {
-    const int c = c0 + V * lane, n = a.H - c;
-    O* grad = static_cast<O*>(a.grad) + (int64_t)token * a.H + c;
-    Raw<O, V> old{};
-    if (a.accumulate && wave == 0) old = load<V>(grad, n);
-    FV<V> sum{};
-#pragma unroll 8
-    for (int r = lo; r < hi; ++r) {
-      const FV<V> f = widen(load<V>(a.part + part_of(s + r * kRun, r == 0) * a.H + c, n));
+  __syncthreads();
+  for (int f = 0; f < kStarts; ++f) {
+    const int s = found[f];
+    if (s < 0) continue;  // the same for all waves
+    const int same = k[s], token = token_of(a.map, same);
+    // up to 64 runs are counted by one probe of their starts
+    const int64_t q = s + (int64_t)kRun * lane;
+    const uint64_t other = __ballot(q >= a.T || k[q] != same);
+    const int runs = other ? __builtin_ctzll(other) : (lower_bound(k, a.T, same + 1) - s + kRun - 1) / kRun;
+    const int per = (runs + kWaves - 1) / kWaves;
+    const int lo = min(wave * per, runs), hi = min(lo + per, runs);
+    for (int c0 = blockIdx.y * 64 * V; c0 < a.H; c0 += gridDim.y * 64 * V) {
+      const int c = c0 + V * lane, n = a.H - c;
+      O* grad = static_cast<O*>(a.grad) + (int64_t)token * a.H + c;
+      Raw<O, V> old{};
+      if (a.accumulate && wave == 0) old = load<V>(grad, n);
+      FV<V> sum{};
+      int r = lo;
+      for (; r + 8 <= hi; r += 8) {
+        Raw<float, V> raw[8];
 #pragma unroll
-      for (int e = 0; e < V; ++e) sum.v[e] += f.v[e];
-    }
-    lds[wave][lane] = sum;
-    __syncthreads();
-    if (wave == 0 && n > 0) {
+        for (int m = 0; m < 8; ++m) raw[m] = load<V>(part_of(a, s + (r + m) * kRun, r + m == 0) + c, n);
 #pragma unroll
-      for (int w = 1; w < 4; ++w) {
-        const FV<V> f = lds[w][lane];
+        for (int m = 0; m < 8; ++m) {
+          const FV<V> v = widen(raw[m]);
 #pragma unroll
-        for (int e = 0; e < V; ++e) sum.v[e] += f.v[e];
+          for (int e = 0; e < V; ++e) sum.v[e] += v.v[e];
+        }
       }
-      grad_row(a, grad, old, sum, n);
+      for (; r < hi; ++r) {
+        const FV<V> v = widen(load<V>(part_of(a, s + r * kRun, r == 0) + c, n));
+#pragma unroll
+        for (int e = 0; e < V; ++e) sum.v[e] += v.v[e];
+      }
+      lds[wave][lane] = sum;
+      __syncthreads();
+      if (wave == 0 && n > 0) {
+#pragma unroll
+        for (int w = 1; w < kWaves; ++w) {
+          const FV<V> v = lds[w][lane];
+#pragma unroll
+          for (int e = 0; e < V; ++e) sum.v[e] += v.v[e];
+        }
+        grad_row(a, grad, old, sum, n);
+      }
+      __syncthreads();
     }
-    __syncthreads();
   }
 }
 
@@ -1148,7 +1190,8 @@ __device__ __forceinline__ void square_sum(const T* p, int64_t n, double (&s)[4]
 }
 
 // part[b] = the sum of squares of chunks b, b + gridDim.x, ..., in fp64: no
-// square overflows or is lost, and the sum needs no care for its order.
+// square overflows or is lost, and the sum needs no care for its order.  Bound
+// by HBM: 622 M fp32 in 350 us, 7.1 TB/s (the fp64 operations hide behind it).
 __global__ __launch_bounds__(256) void grads_square(TensorsArgs a) {
   __shared__ double lds[4];
   double s[4] = {0., 0., 0., 0.};
@@ -1203,7 +1246,8 @@ __device__ __forceinline__ void scale_chunk(const T* p, O* o, int64_t n, float c
 }
 
 // out = c grads.  A few blocks find c from the parts for themselves (one
-// launch less); many read it.
+// launch less); many read it.  Bound by HBM: 412 M fp32 -> bf16 in 396 us, 6.2
+// TB/s.
 __global__ __launch_bounds__(256) void grads_scale(TensorsArgs a) {
   float c;
   if (a.parts) {

@@ -62,7 +62,7 @@ inline rlk_status check_ws(const void* ws, size_t got, size_t need) {
 // Rows a backward's block works on at a time, and the blocks (parts of the
 // weight's gradient): by T and H alone.
 constexpr int64_t kWideFwd = 16384, kWideBwd = 8192;  // widths above: the *_wide kernels
-inline int norm_row_group(int64_t H) { return H <= 1024 ? 4 : 1; }
+inline int norm_row_group(int64_t H) { return H <= 128 ? 16 : H <= 256 ? 8 : H <= 1024 ? 4 : 1; }
 inline int64_t norm_parts(int64_t T, int64_t H) {
   const int64_t most = H > kWideBwd ? 64 : H > 4096 ? 256 : 512;
   return std::max<int64_t>(1, std::min(most, ceil_div(T, norm_row_group(H))));
@@ -81,6 +81,8 @@ rlk_status launch_norm_fwd(const NormFwdArgs& a, hipStream_t st) {
 
 template <class X, class Y, bool kCenter>
 rlk_status norm_fwd_by_width(const NormFwdArgs& a, hipStream_t st) {
+  if (a.H <= 128) return launch_norm_fwd<X, Y, kCenter, 16, 8>(a, st);
+  if (a.H <= 256) return launch_norm_fwd<X, Y, kCenter, 32, 8>(a, st);
   if (a.H <= 512) return launch_norm_fwd<X, Y, kCenter, 64, 8>(a, st);
   if (a.H <= 1024) return launch_norm_fwd<X, Y, kCenter, 64, 16>(a, st);
   if (a.H <= 2048) return launch_norm_fwd<X, Y, kCenter, 256, 8>(a, st);
@@ -128,7 +130,6 @@ rlk_status norm_forward(const void* x, int32_t x_dtype, int64_t ldx, const void*
 
 template <class X, class G, bool kCenter, int R, int E>
 rlk_status launch_norm_bwd(const NormBwdArgs& a, int64_t parts, bool sums, hipStream_t st) {
-  static_assert(norm_rows(R) == 1 || norm_rows(R) == 4, "norm_row_group");
   if (sums)
     RLK_LAUNCH_FN("norm_bwd", (norm_bwd<X, G, kCenter, true, R, E>), dim3((unsigned)parts), dim3(norm_block(R)), st, a);
   else
@@ -146,6 +147,8 @@ rlk_status norm_bwd_by_width(const NormBwdArgs& a, int64_t parts, bool sums, hip
                     dim3((unsigned)ceil_div(a.H, 256 * width_of<X, G>()), (unsigned)parts), dim3(256), st, a);
     return RLK_OK;
   }
+  if (a.H <= 128) return launch_norm_bwd<X, G, kCenter, 16, 8>(a, parts, sums, st);
+  if (a.H <= 256) return launch_norm_bwd<X, G, kCenter, 32, 8>(a, parts, sums, st);
   if (a.H <= 512) return launch_norm_bwd<X, G, kCenter, 64, 8>(a, parts, sums, st);
   if (a.H <= 1024) return launch_norm_bwd<X, G, kCenter, 64, 16>(a, parts, sums, st);
   if (a.H <= 2048) return launch_norm_bwd<X, G, kCenter, 256, 8>(a, parts, sums, st);
@@ -279,7 +282,7 @@ rlk_status launch_embed_grad(EmbedGradArgs a, hipStream_t st) {
                 dim3(blocks_for(ceil_div(ceil_div(a.T, a.window) * a.slices, 4))), dim3(256), st, a);
   if (a.T > kRun)
     RLK_LAUNCH_FN("embed_grad_join", (embed_grad_join<O>),
-                  dim3((unsigned)ceil_div(a.T, kRun), (unsigned)ceil_div(a.H, 256)), dim3(256), st, a);
+                  dim3((unsigned)ceil_div(a.T, 128), (unsigned)ceil_div(a.H, 256)), dim3(512), st, a);
   return RLK_OK;
 }
 
@@ -542,6 +545,7 @@ rlk_status rlk_embed_bwd(const void* ids, int32_t id_bytes, const void* g, int32
   a.ldg = ldg;
   a.grad = grad_E;
   a.part = T > 0 ? reinterpret_cast<float*>(static_cast<char*>(ws) + L.part) : nullptr;
+  a.runs = (int)L.runs;
   a.T = (int)T;
   a.H = (int)H;
   a.scale = scale;

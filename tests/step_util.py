@@ -67,8 +67,8 @@ def norm_bounds(x, w, n, rstd, y):
 
 def norm_grad_bounds(x, w, g, n, rstd, gx, T, center):
     """(of grad_x, grad_w, grad_b), from the formulas: sums over a row have L
-    roundings, sums over the rows those of a block's rows (at least 64 blocks,
-    or one a row), of up to 512 blocks and their 32 groups."""
+    roundings, sums over the rows those of a thread's rows (at least 64 blocks, or
+    one a row), of up to 16 groups of rows in a block, 16 blocks and 32 groups."""
     L = ROW_CHAIN
     _, dn = norm_bounds(x, None, n, rstd, np.zeros_like(n))
     A = np.abs(x).mean(axis=1, keepdims=True) * rstd[:, None]
@@ -79,6 +79,6 @@ def norm_grad_bounds(x, w, g, n, rstd, gx, T, center):
     d2 = (L + 2) * U * c2
     r = rstd[:, None]
     bx = rel * np.abs(gx) + r * (4 * U * (gw + c2 + np.abs(n) * c1) + d2 + np.abs(n) * d1 + dn * c1)
-    rows = -(-T // 64) + 4 + 16 + 32 + 4
+    rows = -(-T // 64) + 16 + 16 + 32 + 4
     bw = (np.abs(g) * dn).sum(axis=0) + rows * U * np.abs(g * n).sum(axis=0)
     return bx, bw, rows * U * np.abs(g).sum(axis=0)

@@ -11,7 +11,7 @@ from selected_token_lm_amd import build as B
 
 # kernels and their instances: types of input and output (4), with and
 # without a mean (2), sums or not (2), widths
-KERNELS = {"norm_fwd": 8 * 6, "norm_fwd_wide": 8, "norm_bwd": 16 * 5, "norm_bwd_wide": 8, "norm_sums_wide": 8,
+KERNELS = {"norm_fwd": 8 * 8, "norm_fwd_wide": 8, "norm_bwd": 16 * 7, "norm_bwd_wide": 8, "norm_sums_wide": 8,
            "norm_grad_sum": 1, "embed_rows": 4 * 2, "embed_rank": 2, "radix_count": 1, "radix_scan": 1,
            "radix_scatter": 1, "embed_grad": 4, "embed_grad_join": 2, "grads_square": 1, "grads_norm": 1,
            "grads_scale": 1}

@@ -52,7 +52,7 @@ def check(center, devs, hosts, eps, x, y, grad=F32):
     return got
 
 
-WIDTHS = [1, 2, 7, 8, 9, 63, 64, 255, 256, 505, 512, 513, 1000, 1024, 1025, 1999, 2048, 2050, 4095, 4096, 4097, 8191,
+WIDTHS = [1, 2, 7, 8, 9, 16, 63, 64, 127, 128, 129, 255, 256, 257, 505, 512, 513, 1000, 1024, 1025, 1999, 2048, 2050, 4095, 4096, 4097, 8191,
           8192, 8200, 16384, 16385, 65535, 65536]
 
 
@@ -77,7 +77,7 @@ def test_types(H, x, y, w, center):
 
 
 @pytest.mark.parametrize("center", [False, True], ids=["rms", "layer"])
-@pytest.mark.parametrize("T,H", [(1, 4096), (2, 256), (63, 128), (257, 1024), (1777, 1999), (2049, 520), (5000, 64),
+@pytest.mark.parametrize("T,H", [(1, 4096), (2, 256), (63, 128), (257, 1024), (1777, 1999), (2049, 520), (5000, 64), (10001, 100), (4099, 250),
                                  (700, 8192), (300, 12000), (3, 1), (4096, 2048)])
 def test_row_counts(T, H, center):
     devs, hosts = make(T, H, seed=3, x=F32)
@@ -92,7 +92,7 @@ def test_without_weight_and_bias(center):
 
 
 @pytest.mark.parametrize("center", [False, True], ids=["rms", "layer"])
-@pytest.mark.parametrize("H", [100, 999, 2048, 4100, 9000, 17000])
+@pytest.mark.parametrize("H", [20, 100, 200, 999, 2048, 4100, 9000, 17000])
 def test_a_row_has_its_bits_in_every_batch_and_layout(H, center):
     """Alone, in a batch, with strided or unaligned rows, all rows the same."""
     (x, w, b, g), _ = make(37, H, seed=5)
