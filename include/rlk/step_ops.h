@@ -84,8 +84,9 @@ rlk_status rlk_rms_norm_bwd(const void* x, int32_t x_dtype, int64_t ldx, const v
 rlk_status rlk_embed_fwd(const void* ids, int32_t id_bytes, const void* E, int32_t E_dtype, int64_t T, int64_t H,
                          int64_t V, int64_t ignore_index, float scale, void* out, int32_t out_dtype, void* stream);
 
-/* grad_E[v] = scale * sum over t with ids[t] == v of g[t], rows ascending (runs
- * of 64 rows are summed by themselves, then these sums in order).
+/* grad_E[v] = scale * sum over t with ids[t] == v of g[t]: rows ascending in runs
+ * of 16 from the token's first row on, then these sums, in an order that goes by
+ * their number alone.
  *   g       [T,H] of g_dtype, row stride ldg >= 0
  *   grad_E  [V,H] of grad_dtype.  accumulate == 0: written whole, zero rows for
  *           tokens that do not occur.  accumulate == 1: the sum is added (in

@@ -31,11 +31,11 @@ def ids_dev(ids, dtype=torch.int64):
 
 
 def grad_bound(ids, gn, V, scale, base=None):
-    """Sums of up to 64 rows, of a sixteenth of these sums, of 16; the scale; the
-    sum with what is there."""
+    """Sums of up to 16 rows (15 roundings), of an eighth of these sums (n / 128 at
+    the most), of 8 (7); the scale; the sum with what is there."""
     n = np.bincount(ids[(ids >= 0) & (ids < V)], minlength=V)[:, None]
     total = O.embed_backward(ids, np.abs(gn), V, abs(scale))
-    chain = np.minimum(n, 64 + n / 1024 + 2 + 16)
+    chain = np.minimum(n, 15 + n / 128 + 7)
     b = (chain + 1) * U * total
     return b if base is None else b + U * (np.abs(base) + total)
 

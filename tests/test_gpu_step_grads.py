@@ -85,6 +85,15 @@ def test_one_tensor_and_generators():
     assert out[0] is t and abs(float(rlk.grad_norm(t)) - 1) < 4 * U
 
 
+def test_lists_of_nothing():
+    for ts in ([torch.empty(0, device=DEV)], [torch.empty((0, 3), dtype=BF16, device=DEV)] * 200):
+        assert float(rlk.grad_norm(ts)) == 0.0
+        norm, out = rlk.clip_grads(ts, 0.0)
+        assert float(norm) == 0.0 and all(a is b for a, b in zip(out, ts))
+    with pytest.raises(ValueError, match="empty"):
+        rlk.grad_norm([])
+
+
 def test_layouts():
     """Transposed and unaligned tensors; a flat buffer's pieces as outputs."""
     r = rng(3)
