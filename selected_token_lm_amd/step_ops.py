@@ -131,8 +131,8 @@ def _norm_fwd(center, x, weight, bias, eps, out_dtype, stats):
     yd = _dtype("out_dtype", out_dtype)
     with _on(dev):
         y = torch.empty_like(x) if out_dtype is x.dtype and x.is_contiguous() else x.new_empty((T, H), dtype=out_dtype)
-        mean = torch.empty(T, dtype=torch.float32, device=dev) if stats and center else None
-        rstd = torch.empty(T, dtype=torch.float32, device=dev) if stats else None
+        mean = x.new_empty(T, dtype=torch.float32) if stats and center else None
+        rstd = x.new_empty(T, dtype=torch.float32) if stats else None
         if center:
             _check(lib().rlk_layer_norm_fwd(_ptr(x), xd, ld, _ptr(weight), _ptr(bias), wd, T, H, eps, _ptr(y), yd,
                                             _ptr(mean), _ptr(rstd), _stream(dev)),
@@ -144,21 +144,28 @@ def _norm_fwd(center, x, weight, bias, eps, out_dtype, stats):
     return y, mean, rstd
 
 
+def _stat(name, t, T, device):
+    """A row statistic as _rows has it, at no cost where it is one already."""
+    if t is not None and t.dtype is torch.float32 and t.shape == (T,) and t.device == device and t.is_contiguous():
+        return t
+    return _rows(T, device, **{name: t})[0]
+
+
 def _norm_bwd(center, x, weight, mean, rstd, g, need_x, need_w, need_b, grad_dtype, ws):
     x, xd, ldx = _matrix("x", x)
     T, H = x.shape
     dev = x.device
     g, gd, ldg = _matrix("g", g, x.shape, dev)
     (weight,), wd = _vectors(H, dev, weight=weight)
-    if center:
-        mean, rstd = _rows(T, dev, mean=mean, rstd=rstd)
-    else:
-        rstd, = _rows(T, dev, rstd=rstd)
+    mean = _stat("mean", mean, T, dev) if center else None
+    rstd = _stat("rstd", rstd, T, dev)
     code = _dtype("grad_weight_dtype", grad_dtype)
     with _on(dev):
-        grad_x = torch.empty((T, H), dtype=x.dtype, device=dev) if need_x else None
-        grad_w = torch.empty(H, dtype=grad_dtype, device=dev) if need_w else None
-        grad_b = torch.empty(H, dtype=grad_dtype, device=dev) if need_b else None
+        grad_x = None
+        if need_x:
+            grad_x = torch.empty_like(x) if x.is_contiguous() else x.new_empty((T, H))
+        grad_w = x.new_empty(H, dtype=grad_dtype) if need_w else None
+        grad_b = x.new_empty(H, dtype=grad_dtype) if need_b else None
         n = 0
         if need_w or need_b:
             ws, n = _ws(ws, SOP_NORM_BWD, T, H, 0, dev)

@@ -178,6 +178,32 @@ def test_values_at_the_edges(H):
     assert torch.isnan(gw).all() and (gb == 8).all()
 
 
+@pytest.mark.parametrize("H", [5, 200, 4096, 20000])
+def test_squares_past_the_types_range(H):
+    """rstd is 0 there, and y the bias."""
+    x = torch.ones((3, H), device=DEV)
+    x[1, ::2], x[1, 1::2] = 3e25, -3e25
+    b = torch.arange(H, device=DEV).float()
+    y, _, rstd = rlk.layer_norm_fwd(x, None, b)
+    assert rstd[1] == 0 and torch.equal(y[1], b) and same(y[::2], rlk.layer_norm(x[::2], None, b))
+    z, rstd = rlk.rms_norm_fwd(x)
+    assert rstd[1] == 0 and not z[1].any() and same(z[::2], rlk.rms_norm(x[::2]))
+
+
+def test_statistics_given_otherwise():
+    """Strided and 64-bit statistics; wrong ones are refused."""
+    (x, w, _, g), _ = make(9, 100, seed=8)
+    _, mean, rstd = rlk.layer_norm_fwd(x, w)
+    want = rlk.layer_norm_bwd(x, w, mean, rstd, g)
+    wide = torch.stack([mean, rstd], dim=1)
+    got = rlk.layer_norm_bwd(x, w, wide[:, 0], rstd.double(), g)
+    assert all(same(a, c) for a, c in zip(got, want))
+    for m, r, text in ((None, rstd, "mean is required"), (mean, None, "rstd is required"), (mean[:8], rstd, "T = 9"),
+                       (mean, rstd[None], "T = 9"), (mean.cpu(), rstd, "must be on")):
+        with pytest.raises(ValueError, match=text):
+            rlk.layer_norm_bwd(x, w, m, r, g)
+
+
 def test_many_rows():
     """More rows than a launch of the backward has blocks for, by far, and a
     forward of 2^20 rows."""
