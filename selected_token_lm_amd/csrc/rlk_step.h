@@ -297,9 +297,9 @@ struct NormBwdArgs {
 // A block takes rows b, b + P, ... (several at a time where they are narrow):
 // grad_x of each, and the block's sums for the weight's and bias's gradients in
 // registers, so that x and g are read once.  The next row's loads are issued
-// before the current row's sums are exchanged.  512 blocks: twice as many leave
-// twice the parts to fold, half as many do not hide the memory (16384 x 2048,
-// fp32 and bf16: 59 us, 5.7 TB/s; 4096 x 4096 bf16: 19 us, 5.3 TB/s).
+// before the current row's sums are exchanged.  256 or 512 blocks: more leave
+// more parts to fold, fewer do not hide the memory (16384 x 2048, fp32 and bf16:
+// 59 us, 5.7 TB/s; 4096 x 4096 bf16: 19 us, 5.3 TB/s).
 template <class X, class G, bool kCenter, bool kSums, int R, int E>
 __global__ __launch_bounds__(norm_block(R)) void norm_bwd(NormBwdArgs a) {
   constexpr int V = width_of<X, G>(), N = E / V;
