@@ -275,3 +275,32 @@ def test_binding_refuses_gradient_lists():
     for most in (-1.0, NAN, -INF):
         with pytest.raises(ValueError, match="max_norm"):
             rlk.clip_grads([bf(3)], most)
+
+
+def stand_ins(monkeypatch):
+    """The kernels' forwards on the CPU, without a graph, as the kernels have none."""
+    def norm(center, x, weight, bias, eps, out_dtype, stats):
+        rows = x.detach()[:, 0].clone()
+        return x.detach().clone(), rows if center else None, rows
+
+    monkeypatch.setattr(so, "_norm_fwd", norm)
+    monkeypatch.setattr(so, "embed_fwd", lambda ids, E, *rest: E.detach()[ids])
+
+
+@pytest.mark.parametrize("grad", [True, False])
+def test_a_tangent_is_refused_not_dropped(monkeypatch, grad):
+    """Forward-mode derivatives are not implemented: an input with a tangent
+    raises, with and without no_grad; other inputs inside a dual level do not."""
+    from torch.autograd import forward_ad as fw
+    stand_ins(monkeypatch)
+    x, v, E, ids = torch.randn(T, H), torch.randn(H), torch.randn(V, H), torch.arange(T)
+    with fw.dual_level(), torch.set_grad_enabled(grad):
+        dual = lambda t: fw.make_dual(t, torch.ones_like(t))  # noqa: E731
+        for call in (lambda: rlk.rms_norm(dual(x)), lambda: rlk.rms_norm(x, dual(v)), lambda: rlk.layer_norm(dual(x), v, v),
+                     lambda: rlk.layer_norm(x, dual(v), v), lambda: rlk.layer_norm(x, v, dual(v)),
+                     lambda: rlk.embed(ids, dual(E))):
+            with pytest.raises(NotImplementedError, match="jvp"):
+                call()
+        assert torch.equal(rlk.rms_norm(x, v), x) and torch.equal(rlk.layer_norm(x, v, v), x)
+        assert torch.equal(rlk.embed(ids, E), E[ids])
+    assert rlk.rms_norm(x.requires_grad_(), v).requires_grad == torch.is_grad_enabled()
