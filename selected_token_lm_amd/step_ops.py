@@ -128,6 +128,13 @@ def _followed(*tensors):
     return forward_ad._current_level >= 0 and any(_tangent(t) for t in tensors)
 
 
+def _no_tangents(what, tensors):
+    """Refuses tangents that a result would lack, or that a change in place
+    would leave behind."""
+    if forward_ad._current_level >= 0 and any(_tangent(t) for t in tensors):
+        raise ValueError(f"{what} must carry no forward-mode tangent")
+
+
 def _eps(eps):
     eps = float(eps)
     if not 0.0 <= eps <= 3.4028234663852886e38:
@@ -334,6 +341,7 @@ def embed_bwd(ids, g, V: int, scale: float = 1.0, ignore_index: int = IGNORE_IND
             raise ValueError(f"grad_E must be a contiguous [{V}, {H}] tensor on {dev}, got {list(grad_E.shape)}")
         if grad_E.requires_grad and torch.is_grad_enabled():
             raise ValueError("grad_E requires a gradient itself: pass E.grad, not E")
+        _no_tangents("grad_E", [grad_E])
     else:
         od = _dtype("grad_E_dtype", grad_E_dtype)
     with _on(dev):
@@ -415,10 +423,12 @@ def _list(tensors):
 
 def grad_norm(grads, ws=None):
     """The norm of all elements of a list of tensors, fp32 [] on their device:
-    squares are summed in fp64 and the root rounded once."""
+    squares are summed in fp64 and the root rounded once.  A value: autograd
+    does not follow it."""
     grads = _list(grads)
     if not grads:
         raise ValueError("grads is empty")
+    _no_tangents("grads", grads)
     dev, ptrs, codes, _ = _tensors("grads", grads)
     n, sizes = len(grads), _sizes(grads)
     with _on(dev):
@@ -433,11 +443,12 @@ def clip_grads(grads, max_norm: float, out=None, ws=None):
     """(norm, out): the norm of all gradients (as grad_norm) and c grads, c =
     max_norm / norm where the norm is above max_norm, else 1.  In place, or
     into the list `out` of tensors of the same shapes and layouts (float32 or
-    bfloat16 each).  Nothing waits for the GPU.  With a NaN norm every
-    gradient becomes NaN."""
+    bfloat16 each).  Nothing waits for the GPU, and autograd does not follow.
+    With a NaN norm every gradient becomes NaN."""
     grads = _list(grads)
     if not grads:
         raise ValueError("grads is empty")
+    _no_tangents("grads", grads)
     max_norm = float(max_norm)
     if not max_norm >= 0.0:
         raise ValueError(f"max_norm must not be negative, got {max_norm}")
@@ -449,6 +460,7 @@ def clip_grads(grads, max_norm: float, out=None, ws=None):
         out = _list(out)
         if len(out) != n:
             raise ValueError(f"out must have {n} tensors, got {len(out)}")
+        _no_tangents("out", out)
         odev, optrs, ocodes, oplain = _tensors("out", out)
         if odev != dev:
             raise ValueError(f"out must be on {dev}")

@@ -304,3 +304,22 @@ def test_a_tangent_is_refused_not_dropped(monkeypatch, grad):
         assert torch.equal(rlk.rms_norm(x, v), x) and torch.equal(rlk.layer_norm(x, v, v), x)
         assert torch.equal(rlk.embed(ids, E), E[ids])
     assert rlk.rms_norm(x.requires_grad_(), v).requires_grad == torch.is_grad_enabled()
+
+
+def test_tangents_of_gradients_are_refused(monkeypatch):
+    """A norm or a changed gradient would lack them."""
+    from torch.autograd import forward_ad as fw
+    monkeypatch.setattr(so, "_tensors", lambda what, ts: (ts[0].device, None, None, True))
+    with fw.dual_level():
+        t = torch.ones(3)
+        d = fw.make_dual(torch.ones(3), t)
+        for call in (lambda: rlk.grad_norm([t, d]), lambda: rlk.clip_grads([t, d], 1.0),
+                     lambda: rlk.clip_grads([t, t], 1.0, out=[torch.ones(3), d])):
+            with pytest.raises(ValueError, match="must carry no forward-mode tangent"):
+                call()
+        monkeypatch.setattr(so, "_matrix", lambda name, g: (g, 0, g.stride(0)))
+        monkeypatch.setattr(so, "_ids", lambda ids, device: (ids, 8))
+        monkeypatch.setattr(so, "_table", lambda name, E: 0)
+        E = fw.make_dual(torch.zeros(V, H), torch.ones(V, H))
+        with pytest.raises(ValueError, match="grad_E must carry no forward-mode tangent"):
+            rlk.embed_bwd(torch.arange(T), torch.ones(T, H), V, grad_E=E)
