@@ -417,15 +417,22 @@ def _written(tensors):
         torch.autograd.graph.increment_version([t for t in tensors if not t.is_inference()])
 
 
-def _list(tensors):
-    return [tensors] if isinstance(tensors, torch.Tensor) else list(tensors)
+def _list(what, tensors):
+    tensors = [tensors] if isinstance(tensors, torch.Tensor) else list(tensors)
+    if set(map(type, tensors)) - {torch.Tensor}:
+        for i, t in enumerate(tensors):
+            if t is None:
+                raise TypeError(f"{what}[{i}] is None: leave out parameters without a gradient")
+            if not isinstance(t, torch.Tensor):
+                raise TypeError(f"{what}[{i}] must be a tensor, got {type(t)}")
+    return tensors
 
 
 def grad_norm(grads, ws=None):
     """The norm of all elements of a list of tensors, fp32 [] on their device:
     squares are summed in fp64 and the root rounded once.  A value: autograd
     does not follow it."""
-    grads = _list(grads)
+    grads = _list("grads", grads)
     if not grads:
         raise ValueError("grads is empty")
     _no_tangents("grads", grads)
@@ -445,10 +452,11 @@ def clip_grads(grads, max_norm: float, out=None, ws=None):
     into the list `out` of tensors of the same shapes and layouts (float32 or
     bfloat16 each).  Nothing waits for the GPU, and autograd does not follow.
     With a NaN norm every gradient becomes NaN."""
-    grads = _list(grads)
+    grads = _list("grads", grads)
     if not grads:
         raise ValueError("grads is empty")
     _no_tangents("grads", grads)
+    out = None if out is None else _list("out", out)
     max_norm = float(max_norm)
     if not max_norm >= 0.0:
         raise ValueError(f"max_norm must not be negative, got {max_norm}")
@@ -457,7 +465,6 @@ def clip_grads(grads, max_norm: float, out=None, ws=None):
     if out is None:
         out, optrs, ocodes = grads, ptrs, codes
     else:
-        out = _list(out)
         if len(out) != n:
             raise ValueError(f"out must have {n} tensors, got {len(out)}")
         _no_tangents("out", out)

@@ -323,3 +323,16 @@ def test_tangents_of_gradients_are_refused(monkeypatch):
         E = fw.make_dual(torch.zeros(V, H), torch.ones(V, H))
         with pytest.raises(ValueError, match="grad_E must carry no forward-mode tangent"):
             rlk.embed_bwd(torch.arange(T), torch.ones(T, H), V, grad_E=E)
+
+
+def test_missing_gradients_are_named():
+    """A frozen parameter's None, first or later, and what is no tensor."""
+    t = torch.ones(3)
+    for f in (rlk.grad_norm, lambda g: rlk.clip_grads(g, 1.0), lambda g: rlk.clip_grads([t] * len(g), 1.0, out=g)):
+        for i in (0, 1):
+            grads = [t, t]
+            grads[i] = None
+            with pytest.raises(TypeError, match=rf"(grads|out)\[{i}\] is None: leave out parameters without a gradient"):
+                f(grads)
+        with pytest.raises(TypeError, match=r"\[1\] must be a tensor, got <class 'float'>"):
+            f([t, 3.5])
