@@ -281,6 +281,15 @@ __global__ __launch_bounds__(norm_block(R)) void norm_fwd(NormFwdArgs a) {
   }
 }
 
+// Behind the row's end x is 0 and n = -mean rstd, which may be infinite where no
+// element's n is (a constant row of 2^121): 0 there, as g is.
+template <int V>
+__device__ __forceinline__ void zero_past(FV<V>& n, int left) {
+  if (left >= V) return;
+#pragma unroll
+  for (int j = 0; j < V; ++j) n.v[j] = j < left ? n.v[j] : 0.f;
+}
+
 struct NormBwdArgs {
   const void* x;
   const void* w;
@@ -347,10 +356,11 @@ __global__ __launch_bounds__(norm_block(R)) void norm_bwd(NormBwdArgs a) {
     for (int i = 0; i < N; ++i) {
       const FV<V> xv = widen(xr[i]), gv = widen(gr[i]);
 #pragma unroll
+      for (int j = 0; j < V; ++j) nv[i].v[j] = kCenter ? (xv.v[j] - mu) * r : xv.v[j] * r;
+      if constexpr (kCenter) zero_past(nv[i], a.H - V * (i * R + lane));
+#pragma unroll
       for (int j = 0; j < V; ++j) {
-        const float n = kCenter ? (xv.v[j] - mu) * r : xv.v[j] * r;
-        const float g = gv.v[j];
-        nv[i].v[j] = n;
+        const float n = nv[i].v[j], g = gv.v[j];
         gw[i].v[j] = g * w[i].v[j];
         if (kSums) {
           dw[i].v[j] = __builtin_fmaf(g, n, dw[i].v[j]);
@@ -495,6 +505,7 @@ __global__ __launch_bounds__(1024) void norm_bwd_wide(NormBwdArgs a) {
       }
 #pragma unroll
       for (int j = 0; j < V; ++j) nv.v[j] = kCenter ? (nv.v[j] - mu) * r : nv.v[j] * r;
+      if constexpr (kCenter) zero_past(nv, a.H - c);
     };
     float s[kVals] = {};
     for (int c = V * threadIdx.x; c < a.H; c += V * R) {

@@ -236,3 +236,19 @@ def test_offsets_past_32_bits():
     assert all(same(a, b) for a, b in zip(rlk.rms_norm_bwd(x, w, rstd, g), want))
     x.copy_(g)
     assert all(same(a, b) for a, b in zip(rlk.rms_norm_bwd(small[0], w, rstd, x), want))
+
+
+@pytest.mark.parametrize("x,y", [(BF16, BF16), (F32, F32), (F32, BF16)])
+@pytest.mark.parametrize("H", [1, 20, 100, 250, 500, 999, 1999, 3001, 5003, 9001, 65535])
+def test_a_large_constant_row_at_widths_that_fill_no_vector(H, x, y):
+    """All exact: x = 2^100, whose sums, mean and differences (0) need no rounding;
+    eps = 2^-80, so rstd = 2^40, and mean rstd is past the type's range.  n is 0
+    and g's sum is 0, so grad_x = 2^40 g, grad_weight = 0 and grad_bias = g."""
+    g = torch.zeros((3, H), device=DEV)
+    g[:, 0:H - H % 2:2], g[:, 1:H:2] = 1.0, -1.0
+    xd = torch.full((3, H), 2.0 ** 100, device=DEV)
+    xd[1] = 1.0
+    yd, mean, rstd = rlk.layer_norm_fwd(xd.to(x), None, None, 2.0 ** -80, out_dtype=y)
+    assert not yd.any() and torch.equal(mean, xd[:, 0]) and (rstd == 2.0 ** 40).all()
+    gx, gw, gb = rlk.layer_norm_bwd(xd.to(x), None, mean, rstd, g.to(y))
+    assert torch.equal(gx.float(), 2.0 ** 40 * g) and not gw.any() and torch.equal(gb, 3 * g[0])
