@@ -188,6 +188,12 @@ struct RowSum {
   }
 };
 
+// A mean whose sum left fp32 is taken again from terms scaled by a power of two
+// that 65536 of them do not leave it with (rows that hold a NaN or an infinity
+// end as they were).
+constexpr float kSmall = 1.f / (1 << 17);
+__device__ __forceinline__ bool in_range(float f) { return __builtin_fabsf(f) <= 3.402823466e38f; }
+
 constexpr int norm_block(int R) { return R < 256 ? 256 : R; }
 constexpr int norm_rows(int R) { return norm_block(R) / R; }
 
@@ -215,7 +221,7 @@ __global__ __launch_bounds__(norm_block(R)) void norm_fwd(NormFwdArgs a) {
   constexpr int V = width_of<X, Y>(), N = E / V;
   constexpr int kRows = norm_rows(R);
   constexpr int kWaves = RowSum<R>::kWaves;
-  __shared__ float red[2 * kWaves];
+  __shared__ float red[3 * kWaves];
   const int lane = threadIdx.x % R;
   const float fH = (float)a.H;
   for (int64_t row = (int64_t)blockIdx.x * kRows + threadIdx.x / R; row < a.T; row += (int64_t)gridDim.x * kRows) {
@@ -242,6 +248,15 @@ __global__ __launch_bounds__(norm_block(R)) void norm_fwd(NormFwdArgs a) {
     float mean = 0.f;
     if constexpr (kCenter) {
       mean = s[0] / fH;
+      if (!in_range(mean)) {  // the same for all threads of the row
+        s[0] = 0.f;
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+#pragma unroll
+          for (int j = 0; j < V; ++j) s[0] += v[i].v[j] * kSmall;
+        RowSum<R>::run(s, red + 2 * kWaves);
+        mean = s[0] / fH / kSmall;
+      }
       s[0] = 0.f;
 #pragma unroll
       for (int i = 0; i < N; ++i) {
@@ -434,7 +449,7 @@ __global__ __launch_bounds__(norm_block(R)) void norm_bwd(NormBwdArgs a) {
 template <class X, class Y, bool kCenter>
 __global__ __launch_bounds__(1024) void norm_fwd_wide(NormFwdArgs a) {
   constexpr int R = 1024, V = width_of<X, Y>();
-  __shared__ float red[2][R / 64];
+  __shared__ float red[3][R / 64];
   const float fH = (float)a.H;
   for (int64_t row = blockIdx.x; row < a.T; row += gridDim.x) {
     const X* x = static_cast<const X*>(a.x) + row * a.ldx;
@@ -447,6 +462,16 @@ __global__ __launch_bounds__(1024) void norm_fwd_wide(NormFwdArgs a) {
       }
       RowSum<R>::run(s, red[0]);
       mean = s[0] / fH;
+      if (!in_range(mean)) {
+        s[0] = 0.f;
+        for (int c = V * threadIdx.x; c < a.H; c += V * R) {
+          const FV<V> f = widen(load<V>(x + c, a.H - c));
+#pragma unroll
+          for (int j = 0; j < V; ++j) s[0] += f.v[j] * kSmall;
+        }
+        RowSum<R>::run(s, red[2]);
+        mean = s[0] / fH / kSmall;
+      }
       s[0] = 0.f;
     }
     for (int c = V * threadIdx.x; c < a.H; c += V * R) {

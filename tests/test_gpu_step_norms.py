@@ -8,7 +8,7 @@ import torch
 import selected_token_lm_amd as rlk
 from oracle import step_ops as O
 from tests.gpu_util import DEV
-from tests.step_util import DTYPES, dev, norm_bounds, norm_grad_bounds, rng, same, within
+from tests.step_util import DTYPES, ROW_CHAIN, U, dev, norm_bounds, norm_grad_bounds, np64, rng, same, within
 
 pytestmark = pytest.mark.gpu
 F32, BF16 = torch.float32, torch.bfloat16
@@ -252,3 +252,27 @@ def test_a_large_constant_row_at_widths_that_fill_no_vector(H, x, y):
     assert not yd.any() and torch.equal(mean, xd[:, 0]) and (rstd == 2.0 ** 40).all()
     gx, gw, gb = rlk.layer_norm_bwd(xd.to(x), None, mean, rstd, g.to(y))
     assert torch.equal(gx.float(), 2.0 ** 40 * g) and not gw.any() and torch.equal(gb, 3 * g[0])
+
+
+@pytest.mark.parametrize("x,y", [(BF16, BF16), (F32, F32), (F32, BF16)])
+@pytest.mark.parametrize("H", [2, 5, 200, 500, 999, 2048, 4096, 5003, 16384, 20000, 65535])
+def test_sums_past_the_types_range(H, x, y):
+    """Rows of one sign: the mean is in range though the sum is not.  Constant rows
+    of a power of two are exact: mean is the value, y the bias, rstd 2^20 (eps
+    2^-40).  Others have rstd 0, and y the bias."""
+    a = torch.full((4, H), 2.0 ** 127, device=DEV)
+    a[1] = -a[1]
+    a[2] = 1e38 + 2e38 * torch.rand(H, device=DEV, generator=torch.Generator(DEV).manual_seed(H))
+    a[3] = torch.arange(H, device=DEV) % 2
+    a = a.to(x)
+    b = (torch.arange(H, device=DEV) % 100).to(y)
+    out, mean, rstd = rlk.layer_norm_fwd(a, None, b, 2.0 ** -40, out_dtype=y)
+    assert torch.equal(mean[:2], a[:2, 0].float()) and (rstd[:2] == 2.0 ** 20).all() and rstd[2] == 0
+    assert all(torch.equal(out[t], b) for t in range(3))
+    assert same(out[3:], rlk.layer_norm(a[3:], None, b, 2.0 ** -40, out_dtype=y))
+    # the sum's roundings as in norm_bounds, relative to a mean of one sign
+    want = np64(a[2]).mean()
+    assert abs(float(mean[2]) - want) <= 1.01 * (ROW_CHAIN + 2) * U * want
+    g = torch.ones((4, H), device=DEV).to(y)
+    gx, gw, gb = rlk.layer_norm_bwd(a, None, mean, rstd, g)
+    assert torch.count_nonzero(gx[:3]) == 0 and (gb == 4).all() and torch.isfinite(gw).all()
