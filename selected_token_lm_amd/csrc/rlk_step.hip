@@ -70,6 +70,7 @@ inline int64_t norm_parts(int64_t T, int64_t H) {
   // 12.4 and 14.3; but 16384 x 2048 72 and 68, 8192 x 2048 bf16 31 and 24, and
   // rms_norm of 4096 x 4096, forward and backward, 38.8 and 37.3)
   const int64_t most = H > kWideBwd ? 64 : H > 4096 || (H > 2048 && T <= 2048) ? 256 : 512;
+  static_assert(kMaxParts == 512, "what norm_grad_sum folds");
   return std::max<int64_t>(1, std::min(most, ceil_div(T, norm_row_group(H))));
 }
 inline int64_t padded_width(int64_t H) { return ceil_div(H, 8) * 8; }

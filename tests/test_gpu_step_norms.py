@@ -276,3 +276,21 @@ def test_sums_past_the_types_range(H, x, y):
     g = torch.ones((4, H), device=DEV).to(y)
     gx, gw, gb = rlk.layer_norm_bwd(a, None, mean, rstd, g)
     assert torch.count_nonzero(gx[:3]) == 0 and (gb == 4).all() and torch.isfinite(gw).all()
+
+
+@pytest.mark.parametrize("T,H", [(512, 1999), (1777, 1999), (1777, 2048), (5000, 1040)])
+def test_sums_over_the_rows_are_a_tree(T, H):
+    """512 blocks, a row each of the first 512: 2^24 and 511 ones (further rows are
+    0), which lose what is added one at a time to the large one.  A tree adds in
+    nine steps, so nine roundings of at most U (2^24 + 511)."""
+    g = torch.zeros((T, H), device=DEV)
+    g[:512] = 1.0
+    total = 2.0 ** 24 + 511
+    x, one, zero = torch.ones((T, H), device=DEV), torch.ones(T, device=DEV), torch.zeros(T, device=DEV)
+    for large in (0, 37, 300, 511):
+        g[:512] = 1.0
+        g[large] = 2.0 ** 24
+        _, gw, gb = rlk.layer_norm_bwd(x, None, zero, one, g)  # n = 1
+        rw = rlk.rms_norm_bwd(x, None, one, g)[1]
+        for t in (gw, gb, rw):
+            assert (t.double() - total).abs().max() <= 9 * U * total, (large, float(t[0]) - total)
