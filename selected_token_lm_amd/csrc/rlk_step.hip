@@ -65,11 +65,20 @@ inline rlk_status check_ws(const void* ws, size_t got, size_t need) {
 constexpr int64_t kWideFwd = 16384, kWideBwd = 8192;
 inline int norm_row_group(int64_t H) { return H <= 128 ? 16 : H <= 256 ? 8 : H <= 1024 ? 4 : 1; }
 inline int64_t norm_parts(int64_t T, int64_t H) {
-  // wide rows, and few rows of more than 2048, do with 256 blocks, one a unit, and
-  // leave less to fold (256 and 512 blocks, us: 4096 x 6144 33 and 40, 1000 x 4096
-  // 12.4 and 14.3; but 16384 x 2048 72 and 68, 8192 x 2048 bf16 31 and 24, and
-  // rms_norm of 4096 x 4096, forward and backward, 38.8 and 37.3)
-  const int64_t most = H > kWideBwd ? 64 : H > 4096 || (H > 2048 && T <= 2048) ? 256 : 512;
+  // 512 blocks, two a unit, keep more rows in flight; 256 write fewer parts.  The
+  // whole backward of layer_norm (both launches), bf16, 256 and 512 parts, us:
+  //   H to 2048   8192 x 2048 33 and 26, 16384 x 2048 59 and 42 (fp32 72 and 68),
+  //               20000 x 1000 33 and 29; but 1000 x 2048 10.7 and 12.8
+  //   to 4096     rows of 2050, 3000, 4096: 1000 rows 14.8 and 16.6, 15.4 and 17.8,
+  //               15.4 and 18.4; 1536 rows of 2050 18.1 and 18.2; 2048 rows 20.9 and
+  //               19.3, 18.7 and 18.3, 19.4 and 20.3; 8192 rows 67 and 43, 45 and
+  //               36, 44.5 and 43.5 (the one place above 1536 rows where 256 do
+  //               better is fp32 rows near 4096: 8192 rows 66 and 71)
+  //   to 8192     4096 x 6144 34 and 40, 16384 x 6144 112 and 123, 8192 x 8192 82
+  //               and 89
+  // Wider rows' sums have a launch of their own, with blocks along H too; 32, 64
+  // and 128 parts: 1024 x 12000 41, 35 and 35, 512 x 65536 fp32 168, 172 and 184.
+  const int64_t most = H > kWideBwd ? 64 : H > 4096 || (H > 2048 && T <= 1536) ? 256 : 512;
   static_assert(kMaxParts == 512, "what norm_grad_sum folds");
   return std::max<int64_t>(1, std::min(most, ceil_div(T, norm_row_group(H))));
 }
