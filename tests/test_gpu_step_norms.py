@@ -294,3 +294,55 @@ def test_sums_over_the_rows_are_a_tree(T, H):
         rw = rlk.rms_norm_bwd(x, None, one, g)[1]
         for t in (gw, gb, rw):
             assert (t.double() - total).abs().max() <= 9 * U * total, (large, float(t[0]) - total)
+
+
+def rows_chain(T, H):
+    """Roundings of a sum over the rows: those a thread takes, the groups of rows
+    in a block one after the other, the blocks as a tree."""
+    group = 16 if H <= 128 else 8 if H <= 256 else 4 if H <= 1024 else 1
+    most = 64 if H > 8192 else 256 if H > 4096 or (H > 2048 and T <= 1536) else 512
+    parts = min(most, -(-T // group))
+    return -(-T // (parts * group)) + group + 9
+
+
+SEVERAL = [(1000, 4096), (1536, 2050), (1537, 4096), (2049, 4096), (4096, 3000), (1777, 1999), (2500, 1040), (700, 6000),
+           (300, 9001), (3000, 700), (9000, 200), (20000, 72)]
+
+
+@pytest.mark.parametrize("center", [False, True], ids=["rms", "layer"])
+@pytest.mark.parametrize("x,y", [(BF16, BF16), (F32, F32), (BF16, F32), (F32, BF16)])
+@pytest.mark.parametrize("T,H", SEVERAL)
+def test_blocks_that_take_several_rows(T, H, x, y, center):
+    """More rows than blocks (and their groups of rows) at every width's kernel,
+    on both sides of the rules for their number; the sums over the rows within
+    the roundings that their split has."""
+    devs, hosts = make(T, H, seed=20, x=x, y=y)
+    got = check(center, devs, hosts, 1e-5, x, y)
+    xn, wn, _, gn = hosts
+    _, n, _, rstd = O.norm_forward(xn, wn, None, 1e-5, center)
+    _, gw, gb = O.norm_backward(xn, wn, gn, 1e-5, center)
+    _, dn = norm_bounds(xn, None, n, rstd, np.zeros_like(n))
+    chain = rows_chain(T, H)
+    # each term g n has the error of n and a rounding of the product
+    within(got[4], gw, (np.abs(gn) * dn).sum(axis=0) + (chain + 1) * U * np.abs(gn * n).sum(axis=0), F32, "grad_weight")
+    if center:
+        within(got[5], gb, chain * U * np.abs(gn).sum(axis=0), F32, "grad_bias")
+
+
+@pytest.mark.parametrize("x,y", [(BF16, BF16), (F32, F32), (F32, BF16)])
+@pytest.mark.parametrize("T,H", [*SEVERAL, (1 << 20, 24), (300_000, 130), (70_000, 520), (30_011, 1500), (16384, 2048), (6000, 4096),
+                                 (5000, 8192), (2000, 20000), (1, 4096), (255, 3000)])
+def test_sums_over_the_rows_count_every_row_once(T, H, x, y):
+    """Whole numbers, |g n| <= 8 and |g| <= 1 with at most 2^20 rows: every sum, in
+    any order, is exact in fp32, so that a lost or repeated row, group or part
+    changes it."""
+    gen = torch.Generator(DEV).manual_seed(T * 7 + H)
+    xi = torch.randint(-8, 9, (T, H), device=DEV, generator=gen)
+    gi = torch.randint(-1, 2, (T, H), device=DEV, generator=gen)
+    one, zero = torch.ones(T, device=DEV), torch.zeros(T, device=DEV)
+    xs, gs = xi.to(x), gi.to(y)
+    want_w, want_b = (xi * gi).sum(dim=0), gi.sum(dim=0)
+    for need in (True, False):
+        _, gw, gb = rlk.layer_norm_bwd(xs, None, zero, one, gs, need_grad_x=need)  # n = x
+        assert torch.equal(gw, want_w.float()) and torch.equal(gb, want_b.float())
+        assert torch.equal(rlk.rms_norm_bwd(xs, None, one, gs, need_grad_x=need)[1], want_w.float())
