@@ -320,3 +320,24 @@ def test_two_host_threads_and_streams():
         assert len(got[k]) == 4
         for out in got[k]:
             assert all(same(a, b) for a, b in zip(out, want[k]))
+
+
+@pytest.mark.parametrize("T,H,V", [(5, 40, 7), (17, 100, 1), (1000, 512, 10), (4096, 2050, 30), (16384, 64, 9), (17000, 24, 600)])
+def test_the_workspace_asked_for_is_enough(T, H, V):
+    """Nothing behind it is written, and its contents before do not matter."""
+    r = rng(7, T)
+    x, g = dev(r.normal(size=(T, H)), BF16)[0], dev(r.normal(size=(T, H)), BF16)[0]
+    ids = torch.from_numpy(r.integers(0, V, T)).to(DEV)
+    _, mean, rstd = rlk.layer_norm_fwd(x)
+    calls = [(rlk.SOP_NORM_BWD, T, H, 0, lambda ws: rlk.layer_norm_bwd(x, None, mean, rstd, g, ws=ws)),
+             (rlk.SOP_EMBED_BWD, T, H, V, lambda ws: [rlk.embed_bwd(ids, g, V, ws=ws)]),
+             (rlk.SOP_EMBED_BWD, T, H, V, lambda ws: [rlk.embed_bwd(ids, g, V, grad_E=torch.ones((V, H), device=DEV), ws=ws)]),
+             (rlk.SOP_GRADS, 200, 0, 0, lambda ws: [rlk.grad_norm([x] * 200, ws=ws)]),
+             (rlk.SOP_GRADS, 2, 0, 0, lambda ws: [rlk.clip_grads([x.clone(), g.clone()], 0.5, ws=ws)[0]])]
+    for op, *sizes, call in calls:
+        n = rlk.step_workspace_bytes(op, *sizes)
+        want = call(None)
+        for fill in (0, 255):
+            buf = torch.full((n + 4096,), fill, dtype=torch.uint8, device=DEV)
+            got = call(buf[:n])
+            assert all(same(a, b) for a, b in zip(got, want)) and (buf[n:] == fill).all(), (op, sizes, fill)

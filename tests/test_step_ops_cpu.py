@@ -336,3 +336,17 @@ def test_missing_gradients_are_named():
                 f(grads)
         with pytest.raises(TypeError, match=r"\[1\] must be a tensor, got <class 'float'>"):
             f([t, 3.5])
+
+
+@pytest.mark.parametrize("T,H,V", [(17, 512, 10), (1000, 512, 10), (16384, 2048, 151936), (16385, 1, 3), (100_000, 33, 600),
+                                   (1 << 23, 65536, 8_000_000)])
+def test_workspace_holds_every_part(T, H, V):
+    """The embedding's gradient: a key and a row a token (twice where a radix sort
+    has more than one digit of nine bits), two sums of H for every run of 16 rows.
+    The norms': two rows of sums a block."""
+    digits = 1 if T <= 16384 else -(-V.bit_length() // 9)
+    need = 8 * T * min(2, digits) + 2 * -(-T // 16) * H * 4
+    assert need <= rlk.step_workspace_bytes(rlk.SOP_EMBED_BWD, T, H, V) <= need + 4 * 512 * (T // 4096 + 2) + 8 * 256
+    group = 16 if H <= 128 else 8 if H <= 256 else 4 if H <= 1024 else 1
+    blocks = min(64 if H > 8192 else 256, -(-T // group))
+    assert rlk.step_workspace_bytes(rlk.SOP_NORM_BWD, T, H) >= 2 * 4 * blocks * H
