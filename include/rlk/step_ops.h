@@ -112,8 +112,9 @@ rlk_status rlk_grad_norm(const void* const* grads, const int64_t* sizes, const i
 
 /* The norm as above, and out = c grads with c = max_norm / norm (fp64, rounded
  * to fp32) where norm > max_norm, else 1; each product rounded once to the
- * output's type.  A NaN norm makes c NaN; an infinite one, c = 0 (and NaN
- * where a gradient is infinite).
+ * output's type.  The norm's fp64 value is what counts: one that only fp32
+ * cannot hold is stored as infinity, and scales as any other.  A NaN norm makes c
+ * NaN; an infinite gradient, c = 0 (and NaN where a gradient is infinite).
  *   out, out_dtypes  HOST arrays of n; out[i] may be grads[i] with its type.
  * Arrays that overlap otherwise are refused (RLK_ERR_BAD_ARG): an output with
  * another output, or with a gradient that is not its own.
