@@ -49,10 +49,10 @@ size_t rlk_step_workspace_bytes(int32_t op, int64_t T, int64_t H, int64_t V);
  *   weight, bias  [H] of w_dtype; either may be NULL (ones, zeros)
  *   y       [T,H] out of y_dtype
  *   mean, rstd  fp32 [T] out, what the backward needs; either may be NULL
- * eps >= 0 and finite.  The sums are fp32: a row whose squares about the mean
- * add up past 3.4e38 has rstd 0, so its y is bias, or 0 (NaN where x - mean
- * itself passes it; the mean does not, whatever the sum of x).  A NaN or
- * infinite element reaches its own row only. */
+ * eps >= 0 and finite.  The sums are fp32.  The sum of x may pass 3.4e38; a row
+ * whose squares about the mean add up past it has rstd 0, so its y is bias, or 0
+ * (NaN where x - mean itself passes it).  A NaN or infinite element reaches its
+ * own row only. */
 rlk_status rlk_layer_norm_fwd(const void* x, int32_t x_dtype, int64_t ldx, const void* weight, const void* bias,
                               int32_t w_dtype, int64_t T, int64_t H, float eps, void* y, int32_t y_dtype, float* mean,
                               float* rstd, void* stream);
