@@ -72,8 +72,8 @@ inline int64_t norm_parts(int64_t T, int64_t H) {
   //   to 4096     rows of 2050, 3000, 4096: 1000 rows 14.8 and 16.6, 15.4 and 17.8,
   //               15.4 and 18.4; 1536 rows of 2050 18.1 and 18.2; 2048 rows 20.9 and
   //               19.3, 18.7 and 18.3, 19.4 and 20.3; 8192 rows 67 and 43, 45 and
-  //               36, 44.5 and 43.5 (the one place above 1536 rows where 256 do
-  //               better is fp32 rows near 4096: 8192 rows 66 and 71)
+  //               36, 44.5 and 43.5 (above 1536 rows 256 do better by more than 5 %
+  //               for fp32 rows near 4096 only: 8192 rows 66 and 71)
   //   to 8192     4096 x 6144 34 and 40, 16384 x 6144 112 and 123, 8192 x 8192 82
   //               and 89
   // Wider rows' sums have a launch of their own, with blocks along H too; 32, 64
